@@ -96,6 +96,48 @@ int sdm_project(const uint16_t* X, const uint16_t* Wt, int B, int T, int d_model
                 int d_v, float* s1, float* s2, float* q1, float* q2, float* v, float* alpha,
                 float* beta, void* stream);
 
+/* ---- 4-bit microscaled matrices: storage for the projections' operands at a
+ * quarter of bf16's bytes.  Blocks of 32 consecutive columns of a row share
+ * one scale, a power of two 2^(b - 127) held as the byte b:
+ *   b = max(127 + floor(log2 max|x|) - 2, 2) over the block; each element is
+ *   x / scale rounded to the nearest of +-{0, .5, 1, 1.5, 2, 3, 4, 6} (e2m1:
+ *   sign, two exponent bits, one mantissa bit; ties to the even code), held at
+ *   6 above it.  A block with a NaN or an infinity in it gets b = 255 and
+ *   codes 0, and reads as NaN.
+ *   codes   [rows, cols/2] bytes: columns 2c and 2c + 1 in the low and the
+ *           high nibble of byte c (16-byte aligned).
+ *   scales  [cols/128, rows, 4] bytes (4-byte aligned): byte j of entry
+ *           (g, r) scales columns 128 g + 32 j .. + 31 of row r.
+ *   x       [rows, cols] fp32 (dtype SDM_F32) or bf16 bits (SDM_BF16),
+ *           16-byte aligned.
+ * cols is a multiple of 128 in [128, 65536]; at most 2^24 - 1 tiles of 32
+ * rows x 512 columns per call (4 rows when there are fewer than 512 such
+ * tiles).  rows = 0 is a valid no-op (every array may then be NULL). */
+int sdm_mx4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, uint8_t* codes,
+                     uint8_t* scales, void* stream);
+
+/* The values of a 4-bit matrix: exact in either type, for any codes and
+ * scale bytes (values past the type's range become infinite). */
+int sdm_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype, int64_t rows,
+                       int64_t cols, void* x, void* stream);
+
+/* sdm_project from 4-bit operands: the same outputs, y = Wt[h] x_m on the
+ * values the codes stand for.
+ *   Xq, Xs  codes [B*T, d_model/2] and scales [d_model/128, B*T, 4] of the
+ *           tokens.
+ *   Wq, Ws  codes [H*P, d_model/2] and scales [d_model/128, H*P, 4] of the
+ *           weights (rows as in sdm_project: s1, s2, q1, q2, v, alpha, beta
+ *           of each head).
+ * Products of two elements are exact; each y is a binary32 sum of the d_model
+ * of them, in an unspecified but fixed order, within sdm_project's bound.  A
+ * token or weight row with a block of scale 255 gives NaN.  d_model is a
+ * multiple of 128 in [128, 65536]; every other size, and B*T = 0, as for
+ * sdm_project.  Few tokens (a decode step) take a kernel of their own that
+ * reads each weight once. */
+int sdm_project_mx4(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws,
+                    int B, int T, int d_model, int H, int n, int d_v, float* s1, float* s2,
+                    float* q1, float* q2, float* v, float* alpha, float* beta, void* stream);
+
 /* Product-key top-K selection with softmax weights ("Meccanismo Core",
  * item 2), for `units` independent (key or query) half pairs.
  *   x1, x2  [units, n] fp32 half sub-scores (all values finite, and every

@@ -9,6 +9,9 @@ libsdm.so is not built.  PyTorch is used only for device memory and streams.
 
 Calls (same names as the C ABI without the "sdm_" prefix):
   project(X, Wt, n)                      -> (s1, s2, q1, q2, v, alpha, beta)
+  mx4_quantize(x)                        -> (codes, scales)   (4-bit, blocks of 32)
+  mx4_dequantize(codes, scales, dtype)   -> x
+  project_mx4(Xq, Xs, Wq, Ws, n)         -> as project, from 4-bit operands
   select(x1, x2, K)                      -> (idx, score, weight)
   state_init(M0, B, dtype)               -> M
   scan(M, widx, wk, ridx, rw, v, alpha, beta) -> out      (M updated in place)
@@ -26,6 +29,7 @@ Planned scan (fp32 state; few memories, long sequences):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -39,7 +43,7 @@ SDM_FP8 = 2
 STATUS = {0: "SDM_OK", 1: "SDM_ERR_INVALID", 2: "SDM_ERR_UNSUPPORTED", 3: "SDM_ERR_HIP"}
 
 # Every symbol include/sdm.h declares.
-EXPORTS = ("sdm_project", "sdm_select", "sdm_state_init", "sdm_scan", "sdm_step_decode", "sdm_scan_train",
+EXPORTS = ("sdm_project", "sdm_mx4_quantize", "sdm_mx4_dequantize", "sdm_project_mx4", "sdm_select", "sdm_state_init", "sdm_scan", "sdm_step_decode", "sdm_scan_train",
            "sdm_scan_backward_workspace_size", "sdm_scan_backward", "sdm_scan_backward_noalloc",
            "sdm_select_backward", "sdm_scan_plan_workspace_size", "sdm_scan_plan",
            "sdm_scan_planned", "sdm_state_init_backward", "sdm_touch_prepare", "sdm_status_string", "sdm_last_error",
@@ -64,6 +68,9 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         p, i32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
         L.sdm_project.argtypes = [p, p, i32, i32, i32, i32, i32, i32] + [p] * 8
+        L.sdm_mx4_quantize.argtypes = [p, i32, i64, i64, p, p, p]
+        L.sdm_mx4_dequantize.argtypes = [p, p, i32, i64, i64, p, p]
+        L.sdm_project_mx4.argtypes = [p] * 4 + [i32] * 6 + [p] * 8
         L.sdm_select.argtypes = [p, p, i64, i32, i32, p, p, p, p]
         L.sdm_state_init.argtypes = [p, i32, p, i32, i32, i64, i32, p]
         L.sdm_scan.argtypes = [p, i32, i32, i32, i64, i32, i64, i32, i32] + [p] * 9
@@ -81,7 +88,8 @@ def lib():
         L.sdm_scan_planned.argtypes = [p, i32, i32, i64, i32, i64] + [p] * 5 + [ctypes.c_size_t, p]
         L.sdm_select_backward.argtypes = [p, p, p, i64, i32, i32, p, p, p]
         L.sdm_state_init_backward.argtypes = [p, i32, i32, i64, i32, p, p, p]
-        for f in ("sdm_project", "sdm_select", "sdm_state_init", "sdm_scan", "sdm_step_decode",
+        for f in ("sdm_project", "sdm_mx4_quantize", "sdm_mx4_dequantize", "sdm_project_mx4",
+                  "sdm_select", "sdm_state_init", "sdm_scan", "sdm_step_decode",
                   "sdm_abi_version", "sdm_scan_train", "sdm_scan_backward",
                   "sdm_scan_backward_noalloc",
                   "sdm_select_backward", "sdm_state_init_backward", "sdm_touch_prepare",
@@ -157,6 +165,22 @@ def _gpu(*args):
     return ptrs
 
 
+@contextlib.contextmanager
+def _on(t, stream):
+    """The stream handle for a call on tensor t's GPU, with that GPU current
+    while the call runs: the caller's stream, or t's GPU's current one.  A
+    stream of another GPU is refused."""
+    import torch
+
+    if isinstance(stream, torch.cuda.Stream) and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the call's tensors on {t.device}")
+    if t.device.index == torch.cuda.current_device():
+        yield _stream(stream)
+    else:
+        with torch.cuda.device(t.device):
+            yield _stream(stream)
+
+
 def _state_dtype(M):
     import torch
 
@@ -182,6 +206,25 @@ def _units(lead):
     return units
 
 
+def _project_out(B, T, H, P, n, weights, out, device):
+    """The projections' 7 output tensors, made unless the caller gives them,
+    and their checked arguments."""
+    import torch
+
+    f32 = torch.float32
+    d_v = P - 4 * n - 2
+    if n < 1 or d_v < 1:
+        raise ValueError(f"{weights} has P={P} rows per head: too few for n={n} "
+                         "(P = 4n + d_v + 2)")
+    shapes = [(B, H, T, n)] * 4 + [(B, H, T, d_v), (B, H, T), (B, H, T)]
+    names = ("s1", "s2", "q1", "q2", "v", "alpha", "beta")
+    if out is None:
+        out = tuple(torch.empty(sh, dtype=f32, device=device) for sh in shapes)
+    if len(out) != 7:
+        raise ValueError("out must hold 7 tensors (s1, s2, q1, q2, v, alpha, beta)")
+    return tuple(out), [_arg(t, f32, sh, nm) for t, sh, nm in zip(out, shapes, names)]
+
+
 def project(X, Wt, n: int, out=None, stream=None):
     """Token projections on the matrix cores: X [B, T, d_model] bfloat16,
     Wt [H, P, d_model] bfloat16 with P = 4n + d_v + 2 (rows s1, s2, q1, q2,
@@ -190,25 +233,96 @@ def project(X, Wt, n: int, out=None, stream=None):
     function).  out = that 7-tuple writes into caller tensors."""
     import torch
 
-    bf16, f32 = torch.bfloat16, torch.float32
+    bf16 = torch.bfloat16
     if X.dim() != 3 or Wt.dim() != 3:
         raise ValueError("X must be [B, T, d_model] and Wt [H, P, d_model]")
     B, T, d_model = X.shape
     H, P = Wt.shape[0], Wt.shape[1]
-    d_v = P - 4 * n - 2
-    if n < 1 or d_v < 1:
-        raise ValueError(f"Wt has P={P} rows per head: too few for n={n} (P = 4n + d_v + 2)")
-    shapes = [(B, H, T, n)] * 4 + [(B, H, T, d_v), (B, H, T), (B, H, T)]
-    names = ("s1", "s2", "q1", "q2", "v", "alpha", "beta")
-    if out is None:
-        out = tuple(torch.empty(sh, dtype=f32, device=X.device) for sh in shapes)
-    if len(out) != 7:
-        raise ValueError("out must hold 7 tensors (s1, s2, q1, q2, v, alpha, beta)")
-    ptrs = _gpu(_arg(X, bf16, (B, T, d_model), "X"), _arg(Wt, bf16, (H, P, d_model), "Wt"),
-                *(_arg(t, f32, sh, nm) for t, sh, nm in zip(out, shapes, names)))
-    _check(lib().sdm_project(ptrs[0], ptrs[1], B, T, d_model, H, n, d_v, *ptrs[2:],
+    out, outs = _project_out(B, T, H, P, n, "Wt", out, X.device)
+    ptrs = _gpu(_arg(X, bf16, (B, T, d_model), "X"), _arg(Wt, bf16, (H, P, d_model), "Wt"), *outs)
+    _check(lib().sdm_project(ptrs[0], ptrs[1], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[2:],
                              _stream(stream)))
-    return tuple(out)
+    return out
+
+
+def _value_dtype(dtype):
+    import torch
+
+    if dtype == torch.float32:
+        return SDM_F32
+    if dtype == torch.bfloat16:
+        return SDM_BF16
+    raise ValueError(f"values must be float32 or bfloat16, got {dtype}")
+
+
+def _mx4_args(codes, scales, shape, names=("codes", "scales")):
+    """Checked codes and scales of a 4-bit matrix of the given shape
+    [..., cols] (its leading dimensions flattened are the rows)."""
+    import torch
+
+    *lead, cols = shape
+    return [_arg(codes, torch.uint8, (*lead, cols // 2), names[0]),
+            _arg(scales, torch.uint8, (cols // 128, _units(lead), 4), names[1])]
+
+
+def mx4_quantize(x, out=None, stream=None):
+    """4-bit microscaled form of x [..., cols] (fp32 or bf16): returns codes
+    uint8 [..., cols/2] (two columns a byte) and scales uint8
+    [cols/128, rows, 4] (one byte per 32 columns; rows: the leading dimensions
+    together).  out = (codes, scales) writes into caller tensors."""
+    import torch
+
+    if x.dim() < 1:
+        raise ValueError("x must have a last dimension cols")
+    shape = tuple(x.shape)
+    *lead, cols = shape
+    rows, dtype = _units(lead), _value_dtype(x.dtype)
+    if out is None:
+        out = (torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device),
+               torch.empty((cols // 128, rows, 4), dtype=torch.uint8, device=x.device))
+    codes, scales = out
+    px, pc, ps = _gpu(_arg(x, x.dtype, shape, "x"), *_mx4_args(codes, scales, shape))
+    with _on(x, stream) as st:
+        _check(lib().sdm_mx4_quantize(px, dtype, rows, cols, pc, ps, st))
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, dtype=None, out=None, stream=None):
+    """Values [..., cols] (float32 unless dtype or out says bfloat16; exact in
+    both) of a 4-bit matrix from mx4_quantize."""
+    import torch
+
+    if codes.dim() < 1:
+        raise ValueError("codes must have a last dimension cols/2")
+    shape = (*codes.shape[:-1], 2 * codes.shape[-1])
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32 if dtype is None else dtype,
+                          device=codes.device)
+    elif dtype is not None and dtype != out.dtype:
+        raise ValueError(f"out must be {dtype}, got {out.dtype}")
+    dt = _value_dtype(out.dtype)
+    pc, ps, px = _gpu(*_mx4_args(codes, scales, shape), _arg(out, out.dtype, shape, "out"))
+    with _on(codes, stream) as st:
+        _check(lib().sdm_mx4_dequantize(pc, ps, dt, _units(shape[:-1]), shape[-1], px, st))
+    return out
+
+
+def project_mx4(Xq, Xs, Wq, Ws, n: int, out=None, stream=None):
+    """project() from 4-bit operands (mx4_quantize of X and of Wt): Xq
+    [B, T, d_model/2], Xs [d_model/128, B*T, 4], Wq [H, P, d_model/2], Ws
+    [d_model/128, H*P, 4], all uint8.  Returns (or writes into out)
+    project()'s 7 tensors."""
+    if Xq.dim() != 3 or Wq.dim() != 3:
+        raise ValueError("Xq must be [B, T, d_model/2] and Wq [H, P, d_model/2]")
+    B, T, half = Xq.shape
+    H, P = Wq.shape[0], Wq.shape[1]
+    d_model = 2 * half
+    out, outs = _project_out(B, T, H, P, n, "Wq", out, Xq.device)
+    ptrs = _gpu(*_mx4_args(Xq, Xs, (B, T, d_model), ("Xq", "Xs")),
+                *_mx4_args(Wq, Ws, (H, P, d_model), ("Wq", "Ws")), *outs)
+    with _on(Xq, stream) as st:
+        _check(lib().sdm_project_mx4(*ptrs[:4], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[4:], st))
+    return out
 
 
 def select(x1, x2, K: int, out=None, stream=None):

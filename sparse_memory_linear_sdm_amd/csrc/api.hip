@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "../../include/sdm.h"
+#include "api_common.h"
 #include "internal.h"
 #include "planned.h"
 #include "ranges.h"
@@ -14,20 +15,26 @@ namespace {
 
 thread_local char g_err[512] = "";
 
-int fail(int status, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof g_err, fmt, ap);
-  va_end(ap);
-  return status;
-}
-
 bool debug_sync() {
   static const int on = [] {
     const char* e = getenv("SDM_DEBUG_SYNC");
     return (e && e[0] == '1') ? 1 : 0;
   }();
   return on != 0;
+}
+
+}  // namespace
+
+// Shared with the other files of entry points (api_common.h).
+namespace sdm {
+namespace api {
+
+int fail(int status, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return status;
 }
 
 int finish(const char* what, hipError_t launch_err, hipStream_t stream) {
@@ -42,7 +49,12 @@ int finish(const char* what, hipError_t launch_err, hipStream_t stream) {
   return SDM_OK;
 }
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+}  // namespace api
+}  // namespace sdm
+
+namespace {
+
+using namespace sdm::api;
 
 bool n_supported(int n) {
   return (n >= 1 && n <= 64) || n == 128 || n == 256 || n == 512 || n == 1024 || n == 2048;
@@ -82,6 +94,42 @@ int check_state(const void* M, int dtype, int64_t N, int d_v) {
   return SDM_OK;
 }
 
+}  // namespace
+
+namespace sdm {
+namespace api {
+
+// Sizes of the projections' output: B*T tokens x H*(4n + d_v + 2) columns.
+int check_project_sizes(int B, int T, int H, int n, int d_v) {
+  if (B < 0 || T < 0) return fail(SDM_ERR_INVALID, "B and T must be >= 0 (got %d, %d)", B, T);
+  if (H < 1 || n < 1 || d_v < 1)
+    return fail(SDM_ERR_INVALID, "H, n and d_v must be >= 1 (got %d, %d, %d)", H, n, d_v);
+  const int64_t P = 4 * (int64_t)n + d_v + 2, cols = (int64_t)H * P, M = (int64_t)B * T;
+  if (cols >= ((int64_t)1 << 31))
+    return fail(SDM_ERR_UNSUPPORTED, "H*(4n + d_v + 2) must be below 2^31 (got %lld)",
+                (long long)cols);
+  if (M > 0 && sdm::project_blocks(M, cols) > sdm::kMaxStrideBlocks)
+    return fail(SDM_ERR_UNSUPPORTED, "more than 2^24 - 1 output tiles of 256 x 256 (B*T=%lld, "
+                "H*P=%lld); split the tokens over several calls", (long long)M, (long long)cols);
+  return SDM_OK;
+}
+
+int check_project_outputs(const float* s1, const float* s2, const float* q1, const float* q2,
+                          const float* v, const float* alpha, const float* beta) {
+  const float* outs[7] = {s1, s2, q1, q2, v, alpha, beta};
+  const char* names[7] = {"s1", "s2", "q1", "q2", "v", "alpha", "beta"};
+  for (int i = 0; i < 7; ++i) {
+    if (!outs[i]) return fail(SDM_ERR_INVALID, "%s is NULL", names[i]);
+    if (!aligned(outs[i], 4)) return fail(SDM_ERR_INVALID, "%s must be 4-byte aligned", names[i]);
+  }
+  return SDM_OK;
+}
+
+}  // namespace api
+}  // namespace sdm
+
+namespace {
+
 int64_t elem_bytes(int dtype) { return dtype == SDM_F32 ? 4 : (dtype == SDM_BF16 ? 2 : 1); }
 
 }  // namespace
@@ -105,29 +153,17 @@ const char* sdm_last_error(void) { return g_err; }
 int sdm_project(const uint16_t* X, const uint16_t* Wt, int B, int T, int d_model, int H, int n,
                 int d_v, float* s1, float* s2, float* q1, float* q2, float* v, float* alpha,
                 float* beta, void* stream) {
-  if (B < 0 || T < 0) return fail(SDM_ERR_INVALID, "B and T must be >= 0 (got %d, %d)", B, T);
-  if (H < 1 || n < 1 || d_v < 1)
-    return fail(SDM_ERR_INVALID, "H, n and d_v must be >= 1 (got %d, %d, %d)", H, n, d_v);
+  int rc;
   if (d_model < 64 || d_model > 65536 || d_model % 64 != 0)
     return fail(SDM_ERR_UNSUPPORTED, "d_model must be a multiple of 64 in [64, 65536] (got %d)",
                 d_model);
-  const int64_t P = 4 * (int64_t)n + d_v + 2, cols = (int64_t)H * P, M = (int64_t)B * T;
-  if (cols >= ((int64_t)1 << 31))
-    return fail(SDM_ERR_UNSUPPORTED, "H*(4n + d_v + 2) must be below 2^31 (got %lld)",
-                (long long)cols);
-  if (M == 0) return finish("sdm_project", hipSuccess, (hipStream_t)stream);  // arrays may be NULL
-  if (sdm::project_blocks(M, cols) > sdm::kMaxStrideBlocks)
-    return fail(SDM_ERR_UNSUPPORTED, "more than 2^24 - 1 output tiles of 256 x 256 (B*T=%lld, "
-                "H*P=%lld); split the tokens over several calls", (long long)M, (long long)cols);
+  if ((rc = check_project_sizes(B, T, H, n, d_v))) return rc;
+  if ((int64_t)B * T == 0)  // the arrays may be NULL
+    return finish("sdm_project", hipSuccess, (hipStream_t)stream);
   if (!X || !Wt) return fail(SDM_ERR_INVALID, "X and Wt must not be NULL");
   if (!aligned(X, 16) || !aligned(Wt, 16))
     return fail(SDM_ERR_INVALID, "X and Wt must be 16-byte aligned");
-  float* outs[7] = {s1, s2, q1, q2, v, alpha, beta};
-  const char* names[7] = {"s1", "s2", "q1", "q2", "v", "alpha", "beta"};
-  for (int i = 0; i < 7; ++i) {
-    if (!outs[i]) return fail(SDM_ERR_INVALID, "%s is NULL", names[i]);
-    if (!aligned(outs[i], 4)) return fail(SDM_ERR_INVALID, "%s must be 4-byte aligned", names[i]);
-  }
+  if ((rc = check_project_outputs(s1, s2, q1, q2, v, alpha, beta))) return rc;
   hipStream_t s = (hipStream_t)stream;
   return finish("sdm_project", sdm::launch_project(X, Wt, B, T, d_model, H, n, d_v, s1, s2, q1, q2,
                                                    v, alpha, beta, s), s);

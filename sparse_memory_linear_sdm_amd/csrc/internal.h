@@ -39,6 +39,30 @@ hipError_t launch_project(const uint16_t* X, const uint16_t* Wt, int B, int T, i
                           int n, int d_v, float* s1, float* s2, float* q1, float* q2, float* v,
                           float* alpha, float* beta, hipStream_t stream);
 
+// 4-bit microscaled matrices (mx4.hip): tiles of this many rows and 512
+// columns, fewer rows where that would leave compute units without a tile.
+constexpr int kQuantRows = 32, kQuantFewRows = 4;
+inline int quantize_rows(int64_t rows, int cols) {
+  const int64_t tiles = (rows + kQuantRows - 1) / kQuantRows * ((cols + 511) / 512);
+  return tiles >= 512 ? kQuantRows : kQuantFewRows;
+}
+inline int64_t quantize_blocks(int64_t rows, int cols) {
+  const int r = quantize_rows(rows, cols);
+  return (rows + r - 1) / r * ((cols + 511) / 512);
+}
+hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t rows, int cols, uint8_t* codes,
+                               uint8_t* scales, hipStream_t stream);
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype,
+                                 int64_t rows, int cols, void* x, hipStream_t stream);
+
+// Projections from 4-bit operands (project_mx4.hip): up to this many tokens
+// the weights are streamed once per call; from there on 256 x 256 tiles.
+constexpr int64_t kProjFewTokens = 64;
+hipError_t launch_project_mx4(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
+                              const uint8_t* Ws, int B, int T, int d_model, int H, int n, int d_v,
+                              float* s1, float* s2, float* q1, float* q2, float* v, float* alpha,
+                              float* beta, hipStream_t stream);
+
 hipError_t launch_state_init(void* M, int dtype, const float* M0, int B, int H, int64_t N,
                              int d_v, hipStream_t stream);
 

@@ -1,0 +1,175 @@
+// 4-bit microscaled matrices (mx.h): quantisation of fp32 or bf16 rows and
+// reading them back.
+//
+// Layout.  codes [rows, cols/2] bytes, the even column in the low nibble;
+// scales [cols/128, rows, 4] bytes: byte j of entry (g, r) is the scale of
+// columns 128 g + 32 j .. + 31 of row r.  The scales of one 128-column group
+// lie together for consecutive rows, as the product's tiles load them (one
+// 4-byte word per row and 128 columns).
+//
+// Both passes are streams bound by memory: each value is read once and
+// written once.  A workgroup takes kRows rows of 512 columns: a wavefront
+// reads 512 columns of a row at a time (8 values per lane: one 16-byte load
+// of bf16, two of fp32), the block maximum is two exchanges over the four
+// lanes that share a block, and the scale words are gathered in LDS so that
+// each group's kRows words go out together.
+#include "internal.h"
+#include "mx.h"
+
+namespace sdm {
+namespace {
+
+constexpr int kQCols = 512;  // columns of a workgroup's tile: 8 per lane
+constexpr int kQWaves = 4;
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const u32x4 q = *reinterpret_cast<const u32x4*>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4 q = reinterpret_cast<const f32x4*>(p)[i];
+      x[4 * i] = q.x;
+      x[4 * i + 1] = q.y;
+      x[4 * i + 2] = q.z;
+      x[4 * i + 3] = q.w;
+    }
+  }
+}
+
+template <typename T, int ROWS>
+__global__ __launch_bounds__(kQWaves* kWave) void quantize_kernel(const T* __restrict__ x,
+                                                                  int64_t rows, int cols,
+                                                                  uint32_t* __restrict__ codes,
+                                                                  uint32_t* __restrict__ scales) {
+  __shared__ uint32_t sc[kQCols / 128][ROWS];
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int64_t r0 = (int64_t)blockIdx.x * ROWS;
+  const int c0 = blockIdx.y * kQCols, c = c0 + lane * 8;
+  constexpr int kEach = ROWS / kQWaves;
+  float v[kEach][8];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t r = r0 + wave * kEach + i;
+    if (r < rows && c < cols) {
+      load8(x + r * cols + c, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t r = r0 + wave * kEach + i;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = umax(m, mag_bits(v[i][j]));
+    const uint32_t b = mx4_scale(quad_max(m));  // a block of 32 is four lanes of 8
+    const float s = scale_f32(b);
+    uint32_t q = 0;  // the conversion divides by s, rounds to nearest even and holds at +-6
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[i][0], v[i][1], s, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[i][2], v[i][3], s, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[i][4], v[i][5], s, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[i][6], v[i][7], s, 3);
+    if (r < rows && c < cols) codes[(r * cols + c) / 8] = b == kMxNan ? 0u : q;
+    if ((lane & 3) == 0)
+      reinterpret_cast<uint8_t*>(&sc[lane / 16][wave * kEach + i])[(lane / 4) & 3] = (uint8_t)b;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kQCols / 128 * ROWS; i += kQWaves * kWave) {
+    const int g = c0 / 128 + i / ROWS;
+    const int64_t r = r0 + i % ROWS;
+    if (g < cols / 128 && r < rows) scales[(int64_t)g * rows + r] = sc[i / ROWS][i % ROWS];
+  }
+}
+
+// Reading back: 8 codes (one word) per thread.
+template <typename T>
+__global__ __launch_bounds__(256) void dequantize_kernel(const uint32_t* __restrict__ codes,
+                                                         const uint8_t* __restrict__ scales,
+                                                         int64_t rows, int cols,
+                                                         T* __restrict__ x) {
+  const int64_t n8 = rows * (cols / 8);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / (cols / 8);
+    const int c = (int)(i - r * (cols / 8)) * 8;
+    const uint32_t b = scales[((int64_t)(c / 128) * rows + r) * 4 + (c / 32) % 4];
+    // code 0 is 2^-127, a subnormal; 255 reads as NaN
+    const float s = b == kMxNan ? __uint_as_float(0x7FC00000u)
+                                : (b == 0 ? __uint_as_float(0x00400000u) : scale_f32(b));
+    const uint32_t q = codes[i];
+    float f[8];
+    const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0);
+    const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1);
+    const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2);
+    const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      f[j] = p0[j] * s;
+      f[2 + j] = p1[j] * s;
+      f[4 + j] = p2[j] * s;
+      f[6 + j] = p3[j] * s;
+    }
+    if constexpr (sizeof(T) == 2) {
+      // two significant bits down to 2^-128: exact in bf16, by the upper halves
+      u32x4 o;
+      o.x = (__float_as_uint(f[0]) >> 16) | (__float_as_uint(f[1]) & 0xFFFF0000u);
+      o.y = (__float_as_uint(f[2]) >> 16) | (__float_as_uint(f[3]) & 0xFFFF0000u);
+      o.z = (__float_as_uint(f[4]) >> 16) | (__float_as_uint(f[5]) & 0xFFFF0000u);
+      o.w = (__float_as_uint(f[6]) >> 16) | (__float_as_uint(f[7]) & 0xFFFF0000u);
+      reinterpret_cast<u32x4*>(x)[i] = o;
+    } else {
+      reinterpret_cast<f32x4*>(x)[2 * i] = f32x4{f[0], f[1], f[2], f[3]};
+      reinterpret_cast<f32x4*>(x)[2 * i + 1] = f32x4{f[4], f[5], f[6], f[7]};
+    }
+  }
+}
+
+template <typename T>
+hipError_t launch_quantize(const void* x, int64_t rows, int cols, uint8_t* codes, uint8_t* scales,
+                           hipStream_t stream) {
+  const unsigned tiles = (unsigned)((cols + kQCols - 1) / kQCols);
+  uint32_t* const c = reinterpret_cast<uint32_t*>(codes);
+  uint32_t* const s = reinterpret_cast<uint32_t*>(scales);
+  const T* const in = reinterpret_cast<const T*>(x);
+  if (quantize_rows(rows, cols) == kQuantRows)
+    hipLaunchKernelGGL((quantize_kernel<T, kQuantRows>),
+                       dim3((unsigned)((rows + kQuantRows - 1) / kQuantRows), tiles),
+                       dim3(kQWaves * kWave), 0, stream, in, rows, cols, c, s);
+  else
+    hipLaunchKernelGGL((quantize_kernel<T, kQuantFewRows>),
+                       dim3((unsigned)((rows + kQuantFewRows - 1) / kQuantFewRows), tiles),
+                       dim3(kQWaves * kWave), 0, stream, in, rows, cols, c, s);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t rows, int cols, uint8_t* codes,
+                               uint8_t* scales, hipStream_t stream) {
+  return dtype == 1 ? launch_quantize<uint16_t>(x, rows, cols, codes, scales, stream)
+                    : launch_quantize<float>(x, rows, cols, codes, scales, stream);
+}
+
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype,
+                                 int64_t rows, int cols, void* x, hipStream_t stream) {
+  int64_t blocks = (rows * (cols / 8) + 255) / 256;
+  if (blocks > kMaxStrideBlocks) blocks = kMaxStrideBlocks;  // the loop strides over the rest
+  const uint32_t* const c = reinterpret_cast<const uint32_t*>(codes);
+  if (dtype == 1)
+    hipLaunchKernelGGL(dequantize_kernel<uint16_t>, dim3((unsigned)blocks), dim3(256), 0, stream,
+                       c, scales, rows, cols, reinterpret_cast<uint16_t*>(x));
+  else
+    hipLaunchKernelGGL(dequantize_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, stream, c,
+                       scales, rows, cols, reinterpret_cast<float*>(x));
+  return hipGetLastError();
+}
+
+}  // namespace sdm

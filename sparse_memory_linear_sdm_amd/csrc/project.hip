@@ -29,12 +29,12 @@
 // [B, H, T] (token m = b*T + t), fp32, so no layout pass follows.
 #include "device_common.h"
 #include "internal.h"
+#include "project_store.h"
 
 namespace sdm {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kPBM = kProjTile, kPBN = kProjTile;  // output tile
 constexpr int kPBK = 64;                            // K per stage (bf16 elements)
@@ -52,15 +52,10 @@ static_assert(kPLoads == 4 && kPSegs == 8, "the slot numbering assumes 4 loads o
 struct ProjArgs {
   const uint16_t* X;   // [M, K] bf16
   const uint16_t* Wt;  // [Ncols, K] bf16, Ncols = H * P
-  int64_t M;
   int K;
-  int H, P, n, d_v, T;
-  int64_t Ncols;
-  float *s1, *s2, *q1, *q2, *v, *alpha, *beta;
   int nbm, nbn;
+  ProjOut out;
 };
-
-__device__ __forceinline__ float sigmoidf_(float y) { return 1.0f / (1.0f + expf(-y)); }
 
 // position of 16-byte segment `seg` in row `row` of a stage
 __device__ __forceinline__ int seg_pos(int row, int seg) { return seg ^ ((row >> 1) & 7); }
@@ -104,8 +99,8 @@ __global__ __launch_bounds__(kPThreads) void project_kernel(ProjArgs A) {
 #pragma unroll
   for (int q = 0; q < kPLoads; ++q) {
     const int s = (q * 8 + w) * kWave + lane, row = s / kPSegs, seg = seg_pos(row, s % kPSegs);
-    const int64_t gm = m0 + row < A.M ? m0 + row : A.M - 1;
-    const int64_t gn = n0 + row < A.Ncols ? n0 + row : A.Ncols - 1;
+    const int64_t gm = m0 + row < A.out.M ? m0 + row : A.out.M - 1;
+    const int64_t gn = n0 + row < A.out.Ncols ? n0 + row : A.out.Ncols - 1;
     srcA[q] = A.X + gm * A.K + seg * 8;
     srcB[q] = A.Wt + gn * A.K + seg * 8;
   }
@@ -179,54 +174,14 @@ __global__ __launch_bounds__(kPThreads) void project_kernel(ProjArgs A) {
 
   // epilogue: lane l, accumulator r of block (i, j) holds C[row][col] with
   // row = 8*(r/4) + 4*(l/32) + r%4 and col = l%32 within the 32 x 32 block
-  const int64_t HT = (int64_t)A.H * A.T;
 #pragma unroll
   for (int j = 0; j < kPTN; ++j) {
     const int64_t col = n0 + (wn * kPTN + j) * 32 + lr;
-    if (col >= A.Ncols) continue;
-    const int h = (int)(col / A.P), p = (int)(col % A.P);
-    float* dst;
-    int64_t stride;  // elements per token of the destination
-    int off;
-    bool gate = false;
-    if (p < 4 * A.n) {
-      const int part = p / A.n;
-      dst = part == 0 ? A.s1 : part == 1 ? A.s2 : part == 2 ? A.q1 : A.q2;
-      stride = A.n;
-      off = p - part * A.n;
-    } else if (p < 4 * A.n + A.d_v) {
-      dst = A.v;
-      stride = A.d_v;
-      off = p - 4 * A.n;
-    } else {
-      dst = p == 4 * A.n + A.d_v ? A.alpha : A.beta;
-      stride = 1;
-      off = 0;
-      gate = true;
-    }
+    if (col >= A.out.Ncols) continue;
+    const ProjColumn c = project_column(A.out, col);
 #pragma unroll
-    for (int i = 0; i < kPTM; ++i) {
-      // this lane's rows in block i: rb + 8*(r/4) + r%4, r = 0..15; the
-      // token (b, t) of rb by one division (tokens < 2^32), then stepped
-      const int64_t rb = m0 + (wm * kPTM + i) * 32 + 4 * lh;
-      if (rb >= A.M) continue;
-      uint32_t b = (uint32_t)rb / (uint32_t)A.T, t = (uint32_t)rb - b * (uint32_t)A.T;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        if (r > 0) {
-          t += (r & 3) ? 1 : 5;  // the row offsets run 0,1,2,3, 8,9,10,11, 16,...
-          while (t >= (uint32_t)A.T) {
-            t -= (uint32_t)A.T;
-            ++b;
-          }
-        }
-        const int64_t row = rb + 8 * (r >> 2) + (r & 3);
-        if (row >= A.M) break;
-        const int64_t tok = (int64_t)b * HT + (int64_t)h * A.T + t;  // ((b*H + h)*T + t)
-        const float y = acc[i][j][r];
-        dst[tok * stride + off] = gate ? sigmoidf_(y) : y;
-      }
-    }
+    for (int i = 0; i < kPTM; ++i)
+      project_store_block(A.out, c, m0 + (wm * kPTM + i) * 32 + 4 * lh, acc[i][j]);
   }
 }
 
@@ -238,25 +193,12 @@ hipError_t launch_project(const uint16_t* X, const uint16_t* Wt, int B, int T, i
   ProjArgs A;
   A.X = X;
   A.Wt = Wt;
-  A.M = (int64_t)B * T;
   A.K = d_model;
-  A.H = H;
-  A.P = 4 * n + d_v + 2;
-  A.n = n;
-  A.d_v = d_v;
-  A.T = T;
-  A.Ncols = (int64_t)H * A.P;
-  A.s1 = s1;
-  A.s2 = s2;
-  A.q1 = q1;
-  A.q2 = q2;
-  A.v = v;
-  A.alpha = alpha;
-  A.beta = beta;
-  if (A.M == 0) return hipSuccess;
-  A.nbm = (int)((A.M + kPBM - 1) / kPBM);
-  A.nbn = (int)((A.Ncols + kPBN - 1) / kPBN);
-  const int64_t blocks = project_blocks(A.M, A.Ncols);
+  A.out = project_out(B, T, H, n, d_v, s1, s2, q1, q2, v, alpha, beta);
+  if (A.out.M == 0) return hipSuccess;
+  A.nbm = (int)((A.out.M + kPBM - 1) / kPBM);
+  A.nbn = (int)((A.out.Ncols + kPBN - 1) / kPBN);
+  const int64_t blocks = project_blocks(A.out.M, A.out.Ncols);
   hipLaunchKernelGGL(project_kernel, dim3((unsigned)blocks), dim3(kPThreads), 0, stream, A);
   return hipGetLastError();
 }

@@ -1,0 +1,100 @@
+"""The microscaled calls refuse bad arguments before any launch: the C entry
+points by status and message, the binding by ValueError (CPU tensors; no
+kernel is reached)."""
+import pytest
+import torch
+
+import sparse_memory_linear_sdm_amd as sdm
+
+FAKE = 1 << 20  # a non-null, aligned address that is never dereferenced
+u8, f32 = torch.uint8, torch.float32
+
+
+def _err():
+    return sdm.lib().sdm_last_error().decode()
+
+
+def _each(fn, ok, bad):
+    for at, value, status, word in bad:
+        a = list(ok)
+        a[at] = value
+        assert fn(*a) == status, (at, value, _err())
+        assert word in _err(), _err()
+
+
+def test_mx4_entry_points():
+    L = sdm.lib()
+    ok = (FAKE, 0, 10, 256, FAKE, FAKE, None)  # x, dtype, rows, cols, codes, scales, stream
+    _each(L.sdm_mx4_quantize, ok, [
+        (0, None, 1, "x is NULL"), (0, FAKE + 4, 1, "16-byte"), (1, 2, 1, "dtype"),
+        (2, -1, 1, "rows"), (2, 1 << 31, 2, "tiles"), (3, 96, 2, "multiple of 128"),
+        (3, 0, 2, "multiple of 128"), (3, 65536 + 128, 2, "multiple of 128"),
+        (4, None, 1, "codes"), (4, FAKE + 8, 1, "16-byte"), (5, None, 1, "scales"),
+        (5, FAKE + 2, 1, "4-byte")])
+    assert L.sdm_mx4_quantize(None, 0, 0, 256, None, None, None) == 0
+    # one tile of 512 columns per 32 rows: 2^24 - 1 tiles is the largest grid
+    assert L.sdm_mx4_quantize(FAKE, 0, 1 << 30, 512, FAKE, FAKE, None) == 2 and "tiles" in _err()
+    ok = (FAKE, FAKE, 0, 10, 256, FAKE, None)  # codes, scales, dtype, rows, cols, x, stream
+    _each(L.sdm_mx4_dequantize, ok, [
+        (0, None, 1, "codes"), (1, None, 1, "codes and scales"), (2, 2, 1, "dtype"),
+        (3, -1, 1, "rows"), (4, 64, 2, "multiple of 128"), (5, None, 1, "x is NULL"),
+        (5, FAKE + 2, 1, "16-byte")])
+    assert L.sdm_mx4_dequantize(None, None, 1, 0, 128, None, None) == 0
+
+
+def test_project_mx4_entry_point():
+    L = sdm.lib()
+    ok = (FAKE,) * 4 + (2, 100, 256, 2, 64, 16) + (FAKE,) * 7 + (None,)
+    _each(L.sdm_project_mx4, ok, [
+        (0, None, 1, "NULL"), (1, None, 1, "NULL"), (2, None, 1, "NULL"), (3, None, 1, "NULL"),
+        (0, FAKE + 8, 1, "16-byte"), (2, FAKE + 4, 1, "16-byte"), (1, FAKE + 2, 1, "4-byte"),
+        (3, FAKE + 1, 1, "4-byte"), (4, -1, 1, "B and T"), (6, 64, 2, "multiple of 128"),
+        (6, 192, 2, "multiple of 128"), (6, 65536 + 128, 2, "multiple of 128"),
+        (7, 0, 1, "H, n and d_v"), (8, 0, 1, "H, n and d_v"), (14, None, 1, "v is NULL"),
+        (10, FAKE + 2, 1, "s1 must be 4-byte")])
+    a = list(ok)
+    a[4] = a[5] = 1 << 30
+    assert L.sdm_project_mx4(*a) == 2 and "tiles" in _err()
+    a = list(ok)
+    a[7] = a[8] = 1 << 20
+    assert L.sdm_project_mx4(*a) == 2 and "2^31" in _err()
+    assert L.sdm_project_mx4(*[None] * 4, 0, 100, 256, 2, 64, 16, *[None] * 8) == 0
+
+
+def _expect(match, fn, *a, **kw):
+    with pytest.raises(ValueError, match=match):
+        fn(*a, **kw)
+
+
+def _z(*shape, dtype=u8):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def test_mx4_binding():
+    x = _z(3, 5, 256, dtype=f32)
+    _expect("on the GPU", sdm.mx4_quantize, x)
+    _expect("float32 or bfloat16", sdm.mx4_quantize, x.half())
+    _expect("last dimension", sdm.mx4_quantize, torch.zeros(()))
+    _expect("contiguous", sdm.mx4_quantize, x.transpose(0, 1))
+    _expect("codes must have shape", sdm.mx4_quantize, x, out=(_z(3, 5, 127), _z(2, 15, 4)))
+    _expect("scales must have shape", sdm.mx4_quantize, x, out=(_z(3, 5, 128), _z(2, 14, 4)))
+    _expect("scales must be", sdm.mx4_quantize, x, out=(_z(3, 5, 128), _z(2, 15, 4, dtype=f32)))
+    codes, scales = _z(3, 5, 128), _z(2, 15, 4)
+    _expect("on the GPU", sdm.mx4_dequantize, codes, scales)
+    _expect("scales must have shape", sdm.mx4_dequantize, codes, _z(15, 2, 4))
+    _expect("float32 or bfloat16", sdm.mx4_dequantize, codes, scales, torch.float64)
+    _expect("out must have shape", sdm.mx4_dequantize, codes, scales, out=_z(15, 256, dtype=f32))
+    _expect("out must be", sdm.mx4_dequantize, codes, scales, torch.bfloat16, out=x)
+
+
+def test_project_mx4_binding():
+    B, T, d, H, n, d_v = 2, 5, 256, 3, 8, 16
+    P = 4 * n + d_v + 2
+    xq, xs, wq, ws = _z(B, T, d // 2), _z(2, B * T, 4), _z(H, P, d // 2), _z(2, H * P, 4)
+    _expect("on the GPU", sdm.project_mx4, xq, xs, wq, ws, n)
+    _expect("Xq must be", sdm.project_mx4, xq.view(B * T, -1), xs, wq, ws, n)
+    _expect("Xs must have shape", sdm.project_mx4, xq, xs[:1], wq, ws, n)
+    _expect("Wq must have shape", sdm.project_mx4, xq, xs, _z(H, P, d), ws, n)
+    _expect("Ws must be", sdm.project_mx4, xq, xs, wq, ws.int(), n)
+    _expect("too few", sdm.project_mx4, xq, xs, wq, ws, P)
+    _expect("7 tensors", sdm.project_mx4, xq, xs, wq, ws, n, out=(xq,))
