@@ -333,6 +333,46 @@ int sdm_scan_backward_noalloc(int B, int H, int64_t N, int d_v, int64_t T, int W
                               float* dv, float* dwk, float* drw, float* dalpha, float* dbeta,
                               const uint64_t* first, void* stream);
 
+/* ---- The training tape in 8 bits: about a quarter of its memory and traffic
+ * (17 GB -> 4.6 GB for 2^18 head-tokens of W = R = 64 rows of 128 values), and
+ * four times the steps per call.  Blocks of 16 columns of a row share one
+ * scale, a power of two 2^(b - 127) held as the byte b:
+ *   b - 127 = the smallest integer >= -125 with |round(x / 2^(b - 127))| <= 127
+ *   over the block, rounding to nearest even; the codes are those rounded
+ *   whole numbers, so a value is off by at most half a scale.  A block with a
+ *   NaN or an infinity in it gets b = 255 and codes 0, and reads as NaN.
+ *   tape        [B, H, d_v/16, T, W + R, 16] int8, 16-byte aligned: slot j of
+ *               step t as in sdm_scan_train's tape, per block of 16 columns.
+ *   tape_scale  [B, H, d_v/16, T, W + R] bytes. */
+
+/* sdm_scan_train with that tape: M and out are its, bit for bit; the tape
+ * holds its rows, rounded.  Slots of rows outside [0, N) are not written.
+ * One memory's tape, T*(W+R)*d_v bytes, must be below 2 GiB. */
+int sdm_scan_train8(void* M, int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
+                    const int32_t* widx, const float* wk, const int32_t* ridx, const float* rw,
+                    const float* v, const float* alpha, const float* beta, float* out,
+                    int8_t* tape, uint8_t* tape_scale, void* stream);
+
+/* The rows of an 8-bit tape of S = W + R slots per step (1..128):
+ *   rows  [B, H, T, S, d_v] fp32 (dtype SDM_F32) or bf16 bits (SDM_BF16),
+ *         exact in both, 16-byte aligned.
+ * T = 0 is a valid no-op (the arrays may then be NULL). */
+int sdm_tape8_read(const int8_t* tape, const uint8_t* tape_scale, int B, int H, int d_v,
+                   int64_t T, int S, int dtype, void* rows, void* stream);
+
+/* sdm_scan_backward from an 8-bit tape: the gradients of the step at the
+ * tape's rounded rows, every result that sdm_scan_backward gives for the fp32
+ * rows of sdm_tape8_read (bit for bit while no product under- or overflows).
+ * Other arguments, modes, workspace and limits as there, the tape's size
+ * limit as for sdm_scan_train8. */
+int sdm_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
+                       const int32_t* widx, const float* wk, const int32_t* ridx,
+                       const float* rw, const float* v, const float* alpha, const float* beta,
+                       const int8_t* tape, const uint8_t* tape_scale, const float* dout, float* G,
+                       float* dv, float* dwk, float* drw, float* dalpha, float* dbeta,
+                       const uint64_t* first, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
 /* Gradient of the selection weights back to the halves ("Meccanismo Core",
  * item 2: slot f = a*n + b scores x1[a] + x2[b]), selections held fixed.
  *   idx, weight  [units, K] from sdm_select;  dweight [units, K] fp32 in.

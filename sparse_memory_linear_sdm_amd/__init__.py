@@ -20,6 +20,9 @@ Training (fp32 state; selections held fixed):
   scan_train(M, widx, wk, ridx, rw, v, alpha, beta) -> (out, tape)
   scan_backward(widx, wk, ridx, rw, v, alpha, beta, tape, dout, G) -> dict
   scan_backward_noalloc(..., G, out) -> out   (no workspace, no allocation)
+  scan_train8(M, widx, wk, ridx, rw, v, alpha, beta) -> (out, (codes, scales))
+  tape8_read((codes, scales), dtype) -> tape  (the 8-bit tape's rows)
+  scan_backward8(widx, wk, ridx, rw, v, alpha, beta, (codes, scales), dout, G) -> dict
 Planned scan (fp32 state; few memories, long sequences):
   scan_plan(widx, wk, ridx, rw, N, d_v) -> workspace
   scan_planned(M, v, alpha, beta, workspace) -> out       (M updated in place)
@@ -46,7 +49,8 @@ STATUS = {0: "SDM_OK", 1: "SDM_ERR_INVALID", 2: "SDM_ERR_UNSUPPORTED", 3: "SDM_E
 EXPORTS = ("sdm_project", "sdm_mx4_quantize", "sdm_mx4_dequantize", "sdm_project_mx4", "sdm_select", "sdm_state_init", "sdm_scan", "sdm_step_decode", "sdm_scan_train",
            "sdm_scan_backward_workspace_size", "sdm_scan_backward", "sdm_scan_backward_noalloc",
            "sdm_select_backward", "sdm_scan_plan_workspace_size", "sdm_scan_plan",
-           "sdm_scan_planned", "sdm_state_init_backward", "sdm_touch_prepare", "sdm_status_string", "sdm_last_error",
+           "sdm_scan_planned", "sdm_state_init_backward", "sdm_touch_prepare", "sdm_scan_train8", "sdm_tape8_read",
+           "sdm_scan_backward8", "sdm_status_string", "sdm_last_error",
            "sdm_abi_version")
 
 _lib = None
@@ -81,6 +85,10 @@ def lib():
         L.sdm_scan_backward.argtypes = ([i32, i32, i64, i32, i64, i32, i32] + [p] * 17 +
                                         [ctypes.c_size_t, p])
         L.sdm_scan_backward_noalloc.argtypes = [i32, i32, i64, i32, i64, i32, i32] + [p] * 17
+        L.sdm_scan_train8.argtypes = [p, i32, i32, i64, i32, i64, i32, i32] + [p] * 11
+        L.sdm_tape8_read.argtypes = [p, p, i32, i32, i32, i64, i32, i32, p, p]
+        L.sdm_scan_backward8.argtypes = ([i32, i32, i64, i32, i64, i32, i32] + [p] * 18 +
+                                         [ctypes.c_size_t, p])
         L.sdm_touch_prepare.argtypes = [i32, i32, i64, i64, i32, i32, p, p, p, p, p]
         L.sdm_scan_plan_workspace_size.argtypes = [i32, i32, i32, i64]
         L.sdm_scan_plan_workspace_size.restype = ctypes.c_size_t
@@ -93,7 +101,8 @@ def lib():
                   "sdm_abi_version", "sdm_scan_train", "sdm_scan_backward",
                   "sdm_scan_backward_noalloc",
                   "sdm_select_backward", "sdm_state_init_backward", "sdm_touch_prepare",
-                  "sdm_scan_plan", "sdm_scan_planned"):
+                  "sdm_scan_plan", "sdm_scan_planned", "sdm_scan_train8", "sdm_tape8_read",
+                  "sdm_scan_backward8"):
             getattr(L, f).restype = ctypes.c_int
         L.sdm_status_string.argtypes = [i32]
         L.sdm_status_string.restype = ctypes.c_char_p
@@ -515,6 +524,86 @@ def scan_backward_noalloc(widx, wk, ridx, rw, v, alpha, beta, tape, dout, G, out
     af = None if first is None else _arg(first, torch.int64, (B, H, T, 2), "first")
     ptrs = _gpu(*ins, af)
     _check(lib().sdm_scan_backward_noalloc(B, H, N, d_v, T, W, R, *ptrs, _stream(stream)))
+    return out
+
+
+def _tape8_args(tape, B, H, T, S, d_v):
+    import torch
+
+    codes, scales = tape
+    return [_arg(codes, torch.int8, (B, H, d_v // 16, T, S, 16), "tape codes"),
+            _arg(scales, torch.uint8, (B, H, d_v // 16, T, S), "tape scales")]
+
+
+def scan_train8(M, widx, wk, ridx, rw, v, alpha, beta, out=None, tape=None, stream=None):
+    """scan_train() with its tape in 8 bits: returns (out [B,H,T,d_v],
+    (codes int8 [B,H,d_v/16,T,W+R,16], scales uint8 [B,H,d_v/16,T,W+R])).
+    M and out are scan_train()'s bit for bit."""
+    import torch
+
+    f32 = torch.float32
+    B, H, N, d_v, T, W, R = _scan_shapes(M, widx, ridx)
+    am = _arg(M, f32, (B, H, N, d_v), "M")
+    ins = _scan_args(B, H, T, W, R, d_v, widx, wk, ridx, rw, v, alpha, beta)
+    if out is None:
+        out = torch.empty((B, H, T, d_v), dtype=f32, device=M.device)
+    if tape is None:
+        tape = (torch.empty((B, H, d_v // 16, T, W + R, 16), dtype=torch.int8, device=M.device),
+                torch.empty((B, H, d_v // 16, T, W + R), dtype=torch.uint8, device=M.device))
+    pm, *ptrs = _gpu(am, *ins, _arg(out, f32, (B, H, T, d_v), "out"),
+                     *_tape8_args(tape, B, H, T, W + R, d_v))
+    with _on(M, stream) as st:
+        _check(lib().sdm_scan_train8(pm, B, H, N, d_v, T, W, R, *ptrs, st))
+    return out, tuple(tape)
+
+
+def tape8_read(tape, dtype=None, out=None, stream=None):
+    """The rows [B,H,T,W+R,d_v] (float32 unless dtype or out says bfloat16;
+    exact in both) of an 8-bit tape."""
+    import torch
+
+    codes, scales = tape
+    if codes.dim() != 6:
+        raise ValueError("tape codes must be [B, H, d_v/16, T, W+R, 16]")
+    B, H, nb, T, S = codes.shape[:5]
+    shape = (B, H, T, S, 16 * nb)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32 if dtype is None else dtype,
+                          device=codes.device)
+    elif dtype is not None and dtype != out.dtype:
+        raise ValueError(f"out must be {dtype}, got {out.dtype}")
+    dt = _value_dtype(out.dtype)
+    pc, ps, po = _gpu(*_tape8_args(tape, B, H, T, S, 16 * nb), _arg(out, out.dtype, shape, "out"))
+    with _on(codes, stream) as st:
+        _check(lib().sdm_tape8_read(pc, ps, B, H, 16 * nb, T, S, dt, po, st))
+    return out
+
+
+def scan_backward8(widx, wk, ridx, rw, v, alpha, beta, tape, dout, G, workspace=None, first=None,
+                   out=None, stream=None):
+    """scan_backward() from the 8-bit tape (codes, scales) of scan_train8.
+    out = a dict of dv, dwk, drw, dalpha, dbeta writes into caller tensors;
+    with it and a workspace the call allocates nothing."""
+    import torch
+
+    f32 = torch.float32
+    B, H, N, d_v, T, W, R = _scan_shapes(G, widx, ridx)
+    ins = _scan_args(B, H, T, W, R, d_v, widx, wk, ridx, rw, v, alpha, beta)
+    ins += _tape8_args(tape, B, H, T, W + R, d_v)
+    ins += [_arg(dout, f32, (B, H, T, d_v), "dout"), _arg(G, f32, (B, H, N, d_v), "G")]
+    shapes = {"dv": (B, H, T, d_v), "dwk": (B, H, T, W), "drw": (B, H, T, R),
+              "dalpha": (B, H, T), "dbeta": (B, H, T)}
+    if out is None:
+        out = {k: torch.empty(shp, dtype=f32, device=G.device) for k, shp in shapes.items()}
+    ins += [_arg(out[k], f32, shp, k) for k, shp in shapes.items()]
+    af = None if first is None else _arg(first, torch.int64, (B, H, T, 2), "first")
+    if workspace is None:
+        need = int(lib().sdm_scan_backward_workspace_size(B, H, d_v, T, W, R))
+        workspace = torch.empty((max(need, 16) + 3) // 4, dtype=f32, device=G.device)
+    ptrs = _gpu(*ins, af, _arg(workspace, None, None, "workspace"))
+    nbytes = workspace.numel() * workspace.element_size()
+    with _on(G, stream) as st:
+        _check(lib().sdm_scan_backward8(B, H, N, d_v, T, W, R, *ptrs, nbytes, st))
     return out
 
 

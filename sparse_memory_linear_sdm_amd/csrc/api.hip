@@ -60,8 +60,6 @@ bool n_supported(int n) {
   return (n >= 1 && n <= 64) || n == 128 || n == 256 || n == 512 || n == 1024 || n == 2048;
 }
 
-bool dv_supported(int d) { return d == 16 || d == 32 || d == 64 || d == 128 || d == 256; }
-
 int check_n_k(int n, int K, const char* kname) {
   if (n < 1) return fail(SDM_ERR_INVALID, "n must be >= 1 (got %d)", n);
   if (K < 1 || K > n) return fail(SDM_ERR_INVALID, "%s must be in [1, n] (got %s=%d, n=%d)",
@@ -104,10 +102,11 @@ int check_project_sizes(int B, int T, int H, int n, int d_v) {
   if (B < 0 || T < 0) return fail(SDM_ERR_INVALID, "B and T must be >= 0 (got %d, %d)", B, T);
   if (H < 1 || n < 1 || d_v < 1)
     return fail(SDM_ERR_INVALID, "H, n and d_v must be >= 1 (got %d, %d, %d)", H, n, d_v);
-  const int64_t P = 4 * (int64_t)n + d_v + 2, cols = (int64_t)H * P, M = (int64_t)B * T;
-  if (cols >= ((int64_t)1 << 31))
-    return fail(SDM_ERR_UNSUPPORTED, "H*(4n + d_v + 2) must be below 2^31 (got %lld)",
-                (long long)cols);
+  const int64_t P = 4 * (int64_t)n + d_v + 2, limit = (int64_t)1 << 31;
+  if (P >= limit || (int64_t)H * P >= limit)  // the product of P < 2^31 and H fits 62 bits
+    return fail(SDM_ERR_UNSUPPORTED, "H*(4n + d_v + 2) must be below 2^31 (got %d * %lld)", H,
+                (long long)P);
+  const int64_t cols = (int64_t)H * P, M = (int64_t)B * T;
   if (M > 0 && sdm::project_blocks(M, cols) > sdm::kMaxStrideBlocks)
     return fail(SDM_ERR_UNSUPPORTED, "more than 2^24 - 1 output tiles of 256 x 256 (B*T=%lld, "
                 "H*P=%lld); split the tokens over several calls", (long long)M, (long long)cols);
@@ -197,7 +196,8 @@ int sdm_state_init(void* M, int dtype, const float* M0, int B, int H, int64_t N,
 
 }  // extern "C"
 
-namespace {
+namespace sdm {
+namespace api {
 
 int check_scan_args(const void* M, int dtype, int B, int H, int64_t N, int d_v, int64_t T, int W,
                     int R, const int32_t* widx, const float* wk, const int32_t* ridx,
@@ -231,7 +231,8 @@ int check_scan_args(const void* M, int dtype, int B, int H, int64_t N, int d_v, 
   return SDM_OK;
 }
 
-}  // namespace
+}  // namespace api
+}  // namespace sdm
 
 extern "C" {
 
@@ -278,14 +279,15 @@ size_t sdm_scan_backward_workspace_size(int B, int H, int d_v, int64_t T, int W,
 
 }  // extern "C"
 
-namespace {
+namespace sdm {
+namespace api {
 
-// Validation shared by sdm_scan_backward and sdm_scan_backward_noalloc; on
-// success *need is the workspace the reverse pass uses, in bytes.
+// Validation shared by the reverse passes; on success *need is the workspace
+// they use, in bytes.
 int check_backward_args(int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
                         const int32_t* widx, const float* wk, const int32_t* ridx,
                         const float* rw, const float* v, const float* alpha, const float* beta,
-                        const float* tape, const float* dout, float* G, float* dv, float* dwk,
+                        const void* tape, int tape_elem, const float* dout, float* G, float* dv, float* dwk,
                         float* drw, float* dalpha, float* dbeta, const uint64_t* first,
                         size_t* need) {
   int rc;
@@ -304,16 +306,19 @@ int check_backward_args(int B, int H, int64_t N, int d_v, int64_t T, int W, int 
   if ((int64_t)B * H * T > sdm::kMaxWaveUnits)
     return fail(SDM_ERR_UNSUPPORTED,
                 "B*H*T must be at most 2^26 - 4 (one finishing wavefront per memory and step)");
-  if (T * (W + R) * d_v * 4 >= ((int64_t)1 << 31))
-    return fail(SDM_ERR_UNSUPPORTED, "one memory's tape (T*(W+R)*d_v*4 bytes) must be below 2 GiB; "
-                "split the sequence into consecutive calls");
-  if (!sdm::ranges::scan_backward_ok(N, d_v, T, W, R))
+  if (T * (W + R) * d_v * tape_elem >= ((int64_t)1 << 31))
+    return fail(SDM_ERR_UNSUPPORTED, "one memory's tape (T*(W+R)*d_v*%d bytes) must be below 2 GiB; "
+                "split the sequence into consecutive calls", tape_elem);
+  if (tape_elem == 4 ? !sdm::ranges::scan_backward_ok(N, d_v, T, W, R)
+                     : !sdm::ranges::scan_ok(N, d_v, 4, T, W, R, false) ||
+                           !sdm::ranges::tape8_ok(d_v, T, W, R))
     return fail(SDM_ERR_UNSUPPORTED, "a gradient or tape tile's buffer range does not fit 31 bits");
   *need = sdm::scan_backward_workspace_bytes(B * H, d_v, T, W, R);
   return SDM_OK;
 }
 
-}  // namespace
+}  // namespace api
+}  // namespace sdm
 
 extern "C" {
 
@@ -325,7 +330,7 @@ int sdm_scan_backward(int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
                       void* workspace, size_t workspace_bytes, void* stream) {
   int rc;
   size_t need = 0;
-  if ((rc = check_backward_args(B, H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha, beta, tape,
+  if ((rc = check_backward_args(B, H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha, beta, tape, 4,
                                 dout, G, dv, dwk, drw, dalpha, dbeta, first, &need)))
     return rc;
   if (T > 0 && !workspace) return fail(SDM_ERR_INVALID, "workspace is NULL");
@@ -349,7 +354,7 @@ int sdm_scan_backward_noalloc(int B, int H, int64_t N, int d_v, int64_t T, int W
                               const uint64_t* first, void* stream) {
   int rc;
   size_t need = 0;
-  if ((rc = check_backward_args(B, H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha, beta, tape,
+  if ((rc = check_backward_args(B, H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha, beta, tape, 4,
                                 dout, G, dv, dwk, drw, dalpha, dbeta, first, &need)))
     return rc;
   if (need > sdm::kStaticScratchBytes)

@@ -3,6 +3,7 @@
 #include "../../include/sdm.h"
 #include "api_common.h"
 #include "internal.h"
+#include "ranges.h"
 
 namespace {
 
@@ -74,6 +75,78 @@ int sdm_project_mx4(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, con
   return finish("sdm_project_mx4",
                 sdm::launch_project_mx4(Xq, Xs, Wq, Ws, B, T, d_model, H, n, d_v, s1, s2, q1, q2,
                                         v, alpha, beta, s), s);
+}
+
+int sdm_scan_train8(void* M, int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
+                    const int32_t* widx, const float* wk, const int32_t* ridx, const float* rw,
+                    const float* v, const float* alpha, const float* beta, float* out,
+                    int8_t* tape, uint8_t* tape_scale, void* stream) {
+  int rc;
+  if ((rc = check_scan_args(M, SDM_F32, B, H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha,
+                            beta, out)))
+    return rc;
+  if (T > 0 && (!tape || !tape_scale))
+    return fail(SDM_ERR_INVALID, "tape and tape_scale must not be NULL");
+  if (!aligned(tape, 16)) return fail(SDM_ERR_INVALID, "tape must be 16-byte aligned");
+  if (T * (W + R) * d_v >= ((int64_t)1 << 31))
+    return fail(SDM_ERR_UNSUPPORTED, "one memory's tape (T*(W+R)*d_v bytes) must be below 2 GiB; "
+                "split the sequence into consecutive calls");
+  if (!sdm::ranges::tape8_ok(d_v, T, W, R))
+    return fail(SDM_ERR_UNSUPPORTED, "a tape buffer range does not fit 31 bits");
+  hipStream_t s = (hipStream_t)stream;
+  return finish("sdm_scan_train8",
+                sdm::launch_scan_train8(reinterpret_cast<float*>(M), B, H, N, d_v, T, W, R, widx,
+                                        wk, ridx, rw, v, alpha, beta, out, tape, tape_scale, s),
+                s);
+}
+
+int sdm_tape8_read(const int8_t* tape, const uint8_t* tape_scale, int B, int H, int d_v,
+                   int64_t T, int S, int dtype, void* rows, void* stream) {
+  if (B < 1 || H < 1) return fail(SDM_ERR_INVALID, "B and H must be >= 1");
+  if ((int64_t)B * H > sdm::kMaxMemories)
+    return fail(SDM_ERR_UNSUPPORTED, "B*H must be at most 2^20 memories per call");
+  if (!dv_supported(d_v))
+    return fail(SDM_ERR_UNSUPPORTED, "d_v=%d not compiled (16, 32, 64, 128, 256)", d_v);
+  if (dtype != SDM_F32 && dtype != SDM_BF16)
+    return fail(SDM_ERR_INVALID, "dtype must be SDM_F32 or SDM_BF16 (got %d)", dtype);
+  if (T < 0) return fail(SDM_ERR_INVALID, "T must be >= 0");
+  if (S < 1 || S > 128) return fail(SDM_ERR_INVALID, "S (rows per step, W + R) must be in [1, 128]");
+  if (T >= ((int64_t)1 << 31) || T * S * d_v >= ((int64_t)1 << 31))
+    return fail(SDM_ERR_UNSUPPORTED, "one memory's tape (T*S*d_v bytes) must be below 2 GiB");
+  hipStream_t s = (hipStream_t)stream;
+  if (T == 0) return finish("sdm_tape8_read", hipSuccess, s);  // the arrays may be NULL
+  if (!tape || !tape_scale || !rows)
+    return fail(SDM_ERR_INVALID, "tape, tape_scale and rows must not be NULL");
+  if (!aligned(tape, 16) || !aligned(rows, 16))
+    return fail(SDM_ERR_INVALID, "tape and rows must be 16-byte aligned");
+  return finish("sdm_tape8_read",
+                sdm::launch_tape8_read(tape, tape_scale, dtype, B * H, d_v, T * S, rows, s), s);
+}
+
+int sdm_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
+                       const int32_t* widx, const float* wk, const int32_t* ridx,
+                       const float* rw, const float* v, const float* alpha, const float* beta,
+                       const int8_t* tape, const uint8_t* tape_scale, const float* dout, float* G,
+                       float* dv, float* dwk, float* drw, float* dalpha, float* dbeta,
+                       const uint64_t* first, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  int rc;
+  size_t need = 0;
+  if ((rc = check_backward_args(B, H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha, beta, tape, 1,
+                                dout, G, dv, dwk, drw, dalpha, dbeta, first, &need)))
+    return rc;
+  if (T > 0 && !tape_scale) return fail(SDM_ERR_INVALID, "tape_scale is NULL");
+  if (T > 0 && !workspace) return fail(SDM_ERR_INVALID, "workspace is NULL");
+  if (!aligned(workspace, 16)) return fail(SDM_ERR_INVALID, "workspace must be 16-byte aligned");
+  if (workspace_bytes < need)
+    return fail(SDM_ERR_INVALID, "workspace of %zu bytes is below the %zu required",
+                workspace_bytes, need);
+  hipStream_t s = (hipStream_t)stream;
+  return finish("sdm_scan_backward8",
+                sdm::launch_scan_backward8(B, H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha,
+                                           beta, tape, tape_scale, dout, G, dv, dwk, drw, dalpha,
+                                           dbeta, first, reinterpret_cast<float*>(workspace), s),
+                s);
 }
 
 }  // extern "C"

@@ -71,6 +71,16 @@ hipError_t launch_scan(void* M, int dtype, int B, int H, int64_t N, int d_v, int
                        const float* rw, const float* v, const float* alpha, const float* beta,
                        float* out, void* tape, hipStream_t stream);
 
+// The training forward with its tape in 8 bits (scan.hip) and reading that
+// tape back (tape8.hip): S row records per memory and 16-column block.
+hipError_t launch_scan_train8(float* M, int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
+                              const int32_t* widx, const float* wk, const int32_t* ridx,
+                              const float* rw, const float* v, const float* alpha,
+                              const float* beta, float* out, int8_t* tape, uint8_t* tape_scale,
+                              hipStream_t stream);
+hipError_t launch_tape8_read(const int8_t* tape, const uint8_t* tape_scale, int dtype, int n_mem,
+                             int d_v, int64_t S, void* rows, hipStream_t stream);
+
 hipError_t launch_step_decode(void* M, int dtype, int B, int H, int n, int d_v, int W, int R,
                               const float* s1, const float* s2, const float* q1,
                               const float* q2, const float* v, const float* alpha,
@@ -86,6 +96,14 @@ hipError_t launch_scan_backward(int B, int H, int64_t N, int d_v, int64_t T, int
                                 const float* dout, float* G, float* dv, float* dwk, float* drw,
                                 float* dalpha, float* dbeta, const uint64_t* first, float* ws,
                                 hipStream_t stream);
+
+hipError_t launch_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
+                                 const int32_t* widx, const float* wk, const int32_t* ridx,
+                                 const float* rw, const float* v, const float* alpha,
+                                 const float* beta, const int8_t* tape,
+                                 const uint8_t* tape_scale, const float* dout, float* G,
+                                 float* dv, float* dwk, float* drw, float* dalpha, float* dbeta,
+                                 const uint64_t* first, float* ws, hipStream_t stream);
 
 // The library's per-GPU scratch buffer (scratch.hip), for callers that cannot
 // allocate: kStaticScratchBytes of device memory, aligned to 256 bytes, held

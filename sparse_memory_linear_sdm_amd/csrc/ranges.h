@@ -81,6 +81,14 @@ constexpr bool scan_ok(int64_t N, int d_v, int elem_bytes, int64_t T, int W, int
   return true;
 }
 
+// The 8-bit tape of one memory: d_v/16 * T * (W + R) records of 16 code bytes
+// and as many scale bytes.
+constexpr bool tape8_ok(int d_v, int64_t T, int W, int R) {
+  const int64_t recs = (int64_t)(d_v / 16) * T * (W + R);
+  return T == 0 || (span_ok(table_range(recs, 16, 0, 16), table_end(recs, 16, 16)) &&
+                    span_ok(recs, recs));
+}
+
 // sdm_scan_backward (fp32): the gradient table G [N, d_v] and the tape
 // [T * (W + R), d_v] of every memory, 16- or 32-column tiles.
 constexpr bool scan_backward_ok(int64_t N, int d_v, int64_t T, int W, int R) {

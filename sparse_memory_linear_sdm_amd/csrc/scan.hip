@@ -58,6 +58,7 @@
 // The two waves meet at one workgroup barrier per chunk.
 #include "device_common.h"
 #include "internal.h"
+#include "mx.h"
 #include "ranges.h"
 #include "scan_rows.h"
 
@@ -134,7 +135,9 @@ struct ScanArgs {
   const float* beta;
   float* out;
   void* tape;  // training forward: [n_mem, T, W + R, d_v] in the state type: per step the
-              // W pre-write rows, then the R rows the read used
+              // W pre-write rows, then the R rows the read used; or, in 8 bits,
+              // [n_mem, d_v/16, T, W + R, 16] codes
+  uint8_t* tape_scale;  // 8-bit tape: [n_mem, d_v/16, T, W + R] scale bytes
   int ntiles;
   int shards;  // 1, or 2: rows split between two workgroups by row_shard()
 };
@@ -338,17 +341,27 @@ struct Producer {
 
 // ---------------------------------------------------------------- consumer
 
-template <typename DT, int COLS, int D, bool SAVE>
+// What the training forward keeps of the rows a step uses.
+enum { kSaveNone = 0, kSaveRows = 1, kSave8 = 2 };
+
+template <typename DT, int COLS, int D, int SAVE>
 struct Consumer {
   using TL = Tile<DT, COLS>;
   static constexpr int NI = TL::NI, EPL = TL::EPL, LPR = TL::LPR, RPI = TL::RPI;
+  // stores of a step: the write rows, and with a tape the W and R rows kept
+  // (8 bits: a code and a scale store per 4 instructions' rows of each)
+  static constexpr int kStores = SAVE == kSaveRows ? 3 * NI : SAVE == kSave8 ? 2 * NI : NI;
 
   u32x4v wv[D + 1][NI];
   u32x4v rv[D + 1][NI];
   __amdgpu_buffer_rsrc_t mres;  // this memory's tile column, range = the memory slice
   __amdgpu_buffer_rsrc_t tres;  // SAVE: this memory's tape slice, shifted to the tile column
+  __amdgpu_buffer_rsrc_t sres;  // kSave8: this memory's scale bytes
+  uint32_t block0;               // kSave8: row records before the tile's first 16-column block
+  uint32_t block_rows;           // kSave8: row records of one block, T * (W + R)
+  uint32_t step_rows;            // kSave8: W + R
   uint32_t tape_step;            // SAVE: bytes of one step's W + R tape rows
-  uint32_t read_base;            // SAVE: bytes before a step's first read row (W rows)
+  uint32_t read_base;            // SAVE: bytes (kSave8: records) before a step's first read row
   uint32_t row_bytes;            // SAVE: bytes of one full row
   uint32_t lane_off;             // lc * 16
   bool accumulate;               // rows split over two workgroups: add into out
@@ -416,6 +429,41 @@ struct Consumer {
     }
   }
 
+  // The 8-bit tape (kSave8): 64 row slots' tile rows as blocks of 16 columns
+  // (mx.h, 8-bit form).  The four lanes of a quad hold one block of a row;
+  // they agree on its scale, pack their four codes into a word each, and
+  // exchange words so that lane q of the quad ends with the whole records
+  // (16 code bytes and the scale byte) of row slots (4 g + q) * RPI + lr: one
+  // 16-byte and one 1-byte store per lane and 4 RPI rows, whose lanes write
+  // neighbouring records.  ofs: the slots' state offsets (out of range: not
+  // kept); row0: the step's first record of these rows in a block.
+  __device__ __forceinline__ void keep8(const u32x4v (&rows)[NI], const uint32_t (&ofs)[NI],
+                                        uint32_t row0) const {
+    const int lane = lane_id(), q = lane & 3, lr = lane / LPR;
+    const uint32_t block = block0 + (uint32_t)((lane % LPR) / 4) * block_rows;
+#pragma unroll
+    for (int g = 0; g < NI / 4; ++g) {
+      uint32_t w[4], sc = 0, at = kOffNone;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = 4 * g + i;
+        float x[4];
+        unpack<float>(rows[k], x);
+        uint32_t m = umax(umax(mag_bits(x[0]), mag_bits(x[1])), umax(mag_bits(x[2]), mag_bits(x[3])));
+        const uint32_t b = int8_scale(quad_max(m));
+        w[i] = int8_pack4(x, b);
+        sc = q == i ? b : sc;
+        at = q == i ? ofs[k] : at;
+      }
+      quad_transpose(w);
+      const uint32_t rec = block + row0 + (uint32_t)((4 * g + q) * RPI + lr);
+      const bool none = at >= kOffNone;
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4v{w[0], w[1], w[2], w[3]}, tres,
+                                             none ? kOffNone : rec * 16u, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)sc, sres, none ? kOffNone : rec, 0, 0);
+    }
+  }
+
   template <int SLOT>
   __device__ __forceinline__ void step(ScanShared<DT, COLS, D>& sh, float* out_mem, int d_v,
                                        int64_t T, int tile, int lr, int lc, int64_t u) {
@@ -441,7 +489,8 @@ struct Consumer {
         if (src) wv[SLOT][k] = lds_u4(sh.upd[(src - 1) >> 6][((src - 1) & 63) * LPR + lc]);
       }
     }
-    if constexpr (SAVE) {  // the pre-write rows, as stored, for the reverse pass
+    if constexpr (SAVE == kSave8) keep8(wv[SLOT], wo, (uint32_t)u * step_rows);
+    if constexpr (SAVE == kSaveRows) {  // the pre-write rows, as stored, for the reverse pass
 #pragma unroll
       for (int k = 0; k < NI; ++k) {
         const uint32_t to = p.wofs[lr * NI + k] == kOffNone
@@ -487,7 +536,13 @@ struct Consumer {
         if (src) rv[SLOT][k] = lds_u4(sh.upd[(src - 1) >> 6][((src - 1) & 63) * LPR + lc]);
       }
     }
-    if constexpr (SAVE) {  // the rows the read uses, for the reverse pass
+    if constexpr (SAVE == kSave8) {
+      uint32_t ro[NI];
+#pragma unroll
+      for (int k = 0; k < NI; ++k) ro[k] = p.rofs[lr * NI + k];
+      keep8(rv[SLOT], ro, (uint32_t)u * step_rows + read_base);
+    }
+    if constexpr (SAVE == kSaveRows) {  // the rows the read uses, for the reverse pass
 #pragma unroll
       for (int k = 0; k < NI; ++k) {
         const uint32_t to = p.rofs[lr * NI + k] == kOffNone
@@ -533,7 +588,7 @@ struct Consumer {
       issue<S>(sh, lr, S, T);
       const u32x4v zero = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int k = 0; k < (SAVE ? 3 : 1) * NI; ++k)  // distinct offsets: identical stores would be merged
+      for (int k = 0; k < kStores; ++k)  // distinct offsets: identical stores would be merged
         __builtin_amdgcn_raw_buffer_store_b128(zero, mres, kOffNone + (uint32_t)(S * 3 * NI + k) * 16u,
                                                0, 0);
       prologue<S + 1>(sh, lr, T);
@@ -563,7 +618,7 @@ struct Consumer {
   }
 };
 
-template <typename DT, int COLS, int D, bool SAVE>
+template <typename DT, int COLS, int D, int SAVE>
 __global__ __launch_bounds__(2 * kWave) void scan_kernel(DT* __restrict__ M, ScanArgs A) {
   using TL = Tile<DT, COLS>;
   __shared__ ScanShared<DT, COLS, D> sh;
@@ -620,7 +675,19 @@ __global__ __launch_bounds__(2 * kWave) void scan_kernel(DT* __restrict__ M, Sca
   cs.accumulate = A.shards > 1;
   // descriptor ranges from ranges.h (checked on the host before the launch)
   const int64_t row_bytes = (int64_t)d_v * (int64_t)sizeof(DT);
-  if constexpr (SAVE) {
+  if constexpr (SAVE == kSave8) {
+    const int64_t recs = (int64_t)(d_v / 16) * T * (A.W + A.R);  // row records of one memory
+    cs.step_rows = (uint32_t)(A.W + A.R);
+    cs.read_base = (uint32_t)A.W;
+    cs.block_rows = (uint32_t)(T * (A.W + A.R));
+    cs.block0 = (uint32_t)(tile * (COLS / 16)) * cs.block_rows;
+    cs.tres = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<uint8_t*>(A.tape) + (int64_t)mem * recs * 16, 0,
+        (int)ranges::table_range(recs, 16, 0, 16), kBufWord3);
+    cs.sres = __builtin_amdgcn_make_buffer_rsrc(A.tape_scale + (int64_t)mem * recs, 0, (int)recs,
+                                                kBufWord3);
+  }
+  if constexpr (SAVE == kSaveRows) {
     const int64_t tape_rows = T * (A.W + A.R);  // rows of one memory's tape
     cs.tape_step = (uint32_t)((A.W + A.R) * row_bytes);
     cs.read_base = (uint32_t)(A.W * row_bytes);
@@ -644,13 +711,15 @@ __global__ __launch_bounds__(256) void zero_kernel(float4* __restrict__ p, int64
     p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-template <typename DT, int COLS, int D, bool SAVE>
+template <typename DT, int COLS, int D, int SAVE>
 hipError_t launch(void* M, ScanArgs A, hipStream_t stream) {
   static_assert(D >= 1 && D <= kChunk, "prefetch depth");
-  static_assert((SAVE ? 5 : 3) * Tile<DT, COLS>::NI * D <= 63,
+  static_assert((2 * Tile<DT, COLS>::NI + Consumer<DT, COLS, D, SAVE>::kStores) * D <= 63,
                 "outstanding vector memory operations");
   A.ntiles = A.d_v / COLS;
-  if (!ranges::scan_tiles_ok(A.N, A.d_v, (int)sizeof(DT), A.T, A.W, A.R, COLS, SAVE))
+  if (!ranges::scan_tiles_ok(A.N, A.d_v, (int)sizeof(DT), A.T, A.W, A.R, COLS,
+                             SAVE == kSaveRows) ||
+      (SAVE == kSave8 && !ranges::tape8_ok(A.d_v, A.T, A.W, A.R)))
     return hipErrorInvalidValue;  // never taken: the C-ABI layer checked every tile width
   const int groups = (A.n_mem + 7) / 8;
   const int64_t blocks = (int64_t)groups * A.shards * A.ntiles * 8;
@@ -686,7 +755,8 @@ hipError_t launch_scan(void* M, int dtype, int B, int H, int64_t N, int d_v, int
                        const float* rw, const float* v, const float* alpha, const float* beta,
                        float* out, void* tape, hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  ScanArgs A{B * H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha, beta, out, tape, 0, 1};
+  ScanArgs A{B * H, N,    d_v,   T,   W,    R,       widx, wk, ridx,
+             rw,    v,    alpha, beta, out, tape, nullptr, 0,    1};
   // Tile width and prefetch depth, measured on the mid (64 memories) and
   // long-stream (16 memories) workloads.  Each workgroup walks its steps at a
   // rate set by the latency of a step's gathers, so with few memories the
@@ -703,23 +773,42 @@ hipError_t launch_scan(void* M, int dtype, int B, int H, int64_t N, int d_v, int
   const bool narrow = d_v == 16 || (int64_t)A.n_mem * (d_v / 16) <= cus;
   if (dtype != 2 && narrow && 2 * (int64_t)A.n_mem * (d_v / 16) <= cus) A.shards = 2;
   if (tape) {  // training forward (fp32 state): also keep the pre-write and the read rows
-    if (!narrow) return launch<float, 32, 1, true>(M, A, stream);
-    if (A.shards == 2) return launch<float, 16, 3, true>(M, A, stream);
-    return launch<float, 16, 2, true>(M, A, stream);
+    if (!narrow) return launch<float, 32, 1, kSaveRows>(M, A, stream);
+    if (A.shards == 2) return launch<float, 16, 3, kSaveRows>(M, A, stream);
+    return launch<float, 16, 2, kSaveRows>(M, A, stream);
   }
   if (dtype == 0) {
-    if (!narrow) return launch<float, 32, 1, false>(M, A, stream);
-    if (A.shards == 2) return launch<float, 16, 3, false>(M, A, stream);
-    return launch<float, 16, 2, false>(M, A, stream);
+    if (!narrow) return launch<float, 32, 1, kSaveNone>(M, A, stream);
+    if (A.shards == 2) return launch<float, 16, 3, kSaveNone>(M, A, stream);
+    return launch<float, 16, 2, kSaveNone>(M, A, stream);
   }
   if (dtype == 2) {  // fp8 E4M3: 32-column tiles (32-byte rows)
     const bool few = (int64_t)A.n_mem * (d_v / 32) < cus;
-    if (!few) return launch<fp8e4m3, 32, 1, false>(M, A, stream);
+    if (!few) return launch<fp8e4m3, 32, 1, kSaveNone>(M, A, stream);
     if (2 * (int64_t)A.n_mem * (d_v / 32) <= cus) A.shards = 2;
-    return launch<fp8e4m3, 32, 3, false>(M, A, stream);
+    return launch<fp8e4m3, 32, 3, kSaveNone>(M, A, stream);
   }
-  if (!narrow) return launch<uint16_t, 32, 1, false>(M, A, stream);
-  return launch<uint16_t, 16, 3, false>(M, A, stream);
+  if (!narrow) return launch<uint16_t, 32, 1, kSaveNone>(M, A, stream);
+  return launch<uint16_t, 16, 3, kSaveNone>(M, A, stream);
+}
+
+hipError_t launch_scan_train8(float* M, int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
+                              const int32_t* widx, const float* wk, const int32_t* ridx,
+                              const float* rw, const float* v, const float* alpha,
+                              const float* beta, float* out, int8_t* tape, uint8_t* tape_scale,
+                              hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  ScanArgs A{B * H, N,    d_v,   T,   W,    R,          widx, wk, ridx,
+             rw,    v,    alpha, beta, out, tape, tape_scale, 0,    1};
+  // the tile widths and depths of the other scans
+  const int cus = compute_units();
+  const bool narrow = d_v == 16 || (int64_t)A.n_mem * (d_v / 16) <= cus;
+  if (!narrow) return launch<float, 32, 1, kSave8>(M, A, stream);
+  if (2 * (int64_t)A.n_mem * (d_v / 16) <= cus) {
+    A.shards = 2;
+    return launch<float, 16, 3, kSave8>(M, A, stream);
+  }
+  return launch<float, 16, 2, kSave8>(M, A, stream);
 }
 
 }  // namespace sdm

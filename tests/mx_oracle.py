@@ -67,3 +67,46 @@ def int8_values(codes, scales):
     out = np.ldexp(codes.astype(np.float64), (b - 127)[..., None])
     out[b == 255] = np.nan
     return out
+
+
+# --------------------------------------------- the step on one memory, in float64
+
+def forward(M, widx, wk, ridx, rw, v, alpha, beta):
+    """T steps on M [N, d_v] (updated): out [T, d_v] and the tape rows
+    [T, W + R, d_v] (write rows before the step's write, read rows after it).
+    Row numbers outside [0, N) are skipped."""
+    out, tape = [], []
+    N = M.shape[0]
+    for t in range(len(v)):
+        wv, rv = (widx[t] >= 0) & (widx[t] < N), (ridx[t] >= 0) & (ridx[t] < N)
+        pre = np.where(wv[:, None], M[np.where(wv, widx[t], 0)], 0.0)
+        k = (beta[t] * wk[t])[:, None]
+        M[widx[t][wv]] = (alpha[t] * (1 - k) * pre + k * v[t])[wv]
+        read = np.where(rv[:, None], M[np.where(rv, ridx[t], 0)], 0.0)
+        out.append((rw[t][:, None] * read).sum(0))
+        tape.append(np.concatenate([pre, read]))
+    return np.array(out), np.array(tape)
+
+
+def backward(G, widx, wk, ridx, rw, v, alpha, beta, tape, dout):
+    """Gradients at the tape's rows; G [N, d_v] in: of the state after the last
+    step, out: before the first."""
+    T, W = wk.shape
+    N = G.shape[0]
+    g = {"dv": np.zeros(v.shape), "dwk": np.zeros(wk.shape), "drw": np.zeros(rw.shape),
+         "dalpha": np.zeros(T), "dbeta": np.zeros(T)}
+    for t in reversed(range(T)):
+        wv, rv = (widx[t] >= 0) & (widx[t] < N), (ridx[t] >= 0) & (ridx[t] < N)
+        pre = np.where(wv[:, None], tape[t, :W], 0.0)
+        read = np.where(rv[:, None], tape[t, W:], 0.0)
+        g["drw"][t] = read @ dout[t]
+        G[ridx[t][rv]] += np.outer(rw[t], dout[t])[rv]
+        gr = np.where(wv[:, None], G[np.where(wv, widx[t], 0)], 0.0)
+        k = beta[t] * wk[t]
+        d = (gr * (v[t] - alpha[t] * pre)).sum(1)
+        g["dv"][t] = k @ gr
+        g["dalpha"][t] = ((1 - k) * (gr * pre).sum(1)).sum()
+        g["dwk"][t] = beta[t] * d
+        g["dbeta"][t] = wk[t] @ d
+        G[widx[t][wv]] = ((alpha[t] * (1 - k))[:, None] * gr)[wv]
+    return g

@@ -98,3 +98,82 @@ def test_project_mx4_binding():
     _expect("Ws must be", sdm.project_mx4, xq, xs, wq, ws.int(), n)
     _expect("too few", sdm.project_mx4, xq, xs, wq, ws, P)
     _expect("7 tensors", sdm.project_mx4, xq, xs, wq, ws, n, out=(xq,))
+
+
+# ------------------------------------------------------------- 8-bit tape
+
+def test_train8_entry_point():
+    L = sdm.lib()
+    # M, B, H, N, d_v, T, W, R, 7 inputs, out, tape, tape_scale, stream
+    ok = [FAKE, 1, 1, 4096, 16, 8, 8, 8] + [FAKE] * 10 + [None]
+    _each(L.sdm_scan_train8, ok, [
+        (0, None, 1, "M is NULL"), (1, 0, 1, "B and H"), (3, 4, 1, "exceed N"),
+        (4, 24, 2, "d_v=24"), (5, -1, 1, "T must"), (6, 65, 2, "64"), (8, None, 1, "NULL"),
+        (15, FAKE + 8, 1, "16-byte"), (16, None, 1, "tape"), (16, FAKE + 4, 1, "tape"),
+        (17, None, 1, "tape_scale")])
+    a = list(ok)
+    a[4], a[5], a[6], a[7] = 128, 1 << 17, 64, 64  # exactly 2 GiB of codes
+    assert L.sdm_scan_train8(*a) == 2 and "2 GiB" in _err()
+    a[4], a[5], a[6], a[7] = 16, 1 << 32, 1, 1
+    assert L.sdm_scan_train8(*a) == 2
+    assert L.sdm_scan_train8(FAKE, 1, 1, 4096, 16, 0, 8, 8, *[None] * 11) == 0
+
+
+def test_tape8_read_entry_point():
+    L = sdm.lib()
+    ok = [FAKE, FAKE, 2, 3, 64, 10, 12, 0, FAKE, None]  # codes, scales, B, H, d_v, T, S, dtype, rows
+    _each(L.sdm_tape8_read, ok, [
+        (0, None, 1, "NULL"), (1, None, 1, "NULL"), (8, None, 1, "NULL"), (0, FAKE + 8, 1, "16-byte"),
+        (8, FAKE + 8, 1, "16-byte"), (2, 0, 1, "B and H"), (2, 1 << 20, 2, "2^20"),
+        (4, 48, 2, "d_v=48"), (5, -1, 1, "T must"), (5, 1 << 40, 2, "2 GiB"), (6, 0, 1, "S (rows"),
+        (6, 129, 1, "S (rows"), (7, 2, 1, "dtype")])
+    assert L.sdm_tape8_read(None, None, 1, 1, 16, 0, 2, 1, None, None) == 0
+
+
+def test_backward8_entry_point():
+    L = sdm.lib()
+    ws = L.sdm_scan_backward_workspace_size(1, 1, 16, 8, 8, 8)
+    # B, H, N, d_v, T, W, R, 7 inputs, tape, tape_scale, dout, G, dv, dwk, drw, dalpha, dbeta,
+    # first, workspace, bytes, stream
+    ok = [1, 1, 4096, 16, 8, 8, 8] + [FAKE] * 18 + [ws, None]
+    _each(L.sdm_scan_backward8, ok, [
+        (14, None, 1, "NULL"), (14, FAKE + 4, 1, "16-byte"), (15, None, 1, "tape_scale"),
+        (16, None, 1, "NULL"), (17, None, 1, "M is NULL"), (23, FAKE + 4, 1, "first"),
+        (24, None, 1, "workspace"), (24, FAKE + 4, 1, "workspace"), (25, ws - 4, 1, "workspace"),
+        (4, 1 << 26, 2, "2^26"), (3, 24, 2, "d_v=24"), (6, 65, 2, "64")])
+    a = list(ok)
+    a[3], a[4], a[5], a[6] = 128, 1 << 17, 64, 64
+    assert L.sdm_scan_backward8(*a) == 2 and "2 GiB" in _err()
+    args = [1, 1, 4096, 16, 0, 8, 8] + [None] * 10 + [FAKE] + [None] * 7 + [0, None]
+    assert L.sdm_scan_backward8(*args) == 0
+
+
+def test_tape8_binding():
+    B, H, N, d_v, T, W, R = 2, 3, 64, 32, 5, 4, 3
+    i32, i8 = torch.int32, torch.int8
+    step = dict(widx=_z(B, H, T, W, dtype=i32), wk=_z(B, H, T, W, dtype=f32),
+                ridx=_z(B, H, T, R, dtype=i32), rw=_z(B, H, T, R, dtype=f32),
+                v=_z(B, H, T, d_v, dtype=f32), alpha=_z(B, H, T, dtype=f32),
+                beta=_z(B, H, T, dtype=f32))
+    M = _z(B, H, N, d_v, dtype=f32)
+    codes, scales = _z(B, H, 2, T, W + R, 16, dtype=i8), _z(B, H, 2, T, W + R)
+    _expect("on the GPU", sdm.scan_train8, M, **step)
+    _expect("M must be", sdm.scan_train8, M.bfloat16(), **step)
+    _expect("wk must have shape", sdm.scan_train8, M, **{**step, "wk": step["rw"]})
+    _expect("tape codes must be", sdm.scan_train8, M, **step, tape=(codes.view(u8), scales))
+    _expect("tape scales must have shape", sdm.scan_train8, M, **step, tape=(codes, scales[:, :, :1]))
+    _expect("out must have shape", sdm.scan_train8, M, **step, out=_z(B, H, T, 16, dtype=f32))
+    _expect("on the GPU", sdm.tape8_read, (codes, scales))
+    _expect("tape codes must be", sdm.tape8_read, (codes[0], scales))
+    _expect("tape codes must have shape", sdm.tape8_read, (codes[..., :8].contiguous(), scales))
+    _expect("float32 or bfloat16", sdm.tape8_read, (codes, scales), torch.float16)
+    _expect("out must have shape", sdm.tape8_read, (codes, scales), out=M)
+    dout = step["v"]
+    _expect("on the GPU", sdm.scan_backward8, **step, tape=(codes, scales), dout=dout, G=M)
+    _expect("tape scales must have shape", sdm.scan_backward8, **step, tape=(codes, scales[:1]),
+            dout=dout, G=M)
+    _expect("first must be", sdm.scan_backward8, **step, tape=(codes, scales), dout=dout, G=M,
+            first=_z(B, H, T, 2, dtype=i32))
+    bad = dict(dv=step["v"], dwk=step["wk"], drw=step["wk"], dalpha=step["alpha"], dbeta=step["beta"])
+    _expect("drw must have shape", sdm.scan_backward8, **step, tape=(codes, scales), dout=dout, G=M,
+            out=bad)

@@ -61,3 +61,37 @@ def test_zero_and_tiny_blocks_take_the_smallest_scale():
         assert np.all(scales == 2) and not codes.any()
     q, b = O.int8_quantize(np.full((1, 16), 2.0 ** -126))
     assert b[0] == 2 and np.all(q == 0)  # half of 2^-125: ties to even
+
+
+def test_plain_backward_against_differences():
+    """The plain reverse pass (unrounded tape) against central differences of
+    the plain forward, in every input.  The forward is a polynomial in each
+    input, so with h = 1e-4 the differences are within h^2 of third derivatives
+    of order one, plus 2^-52 / h of rounding: 1e-7 holds both."""
+    rng = np.random.default_rng(7)
+    N, d_v, T, W, R = 10, 3, 6, 4, 3
+    widx = np.array([rng.permutation(N)[:W] for _ in range(T)])
+    ridx = np.array([rng.permutation(N)[:R] for _ in range(T)])
+    widx[2, 1], ridx[3, 0], ridx[4, 2] = -1, N, 1 << 30  # skipped rows
+    x = dict(M=rng.standard_normal((N, d_v)), wk=rng.random((T, W)), rw=rng.random((T, R)),
+             v=rng.standard_normal((T, d_v)), alpha=rng.random(T), beta=rng.random(T))
+    dout, dM = rng.standard_normal((T, d_v)), rng.standard_normal((N, d_v))
+
+    def run(y):
+        M = y["M"].copy()
+        out, tape = O.forward(M, widx, y["wk"], ridx, y["rw"], y["v"], y["alpha"], y["beta"])
+        return M, out, tape
+
+    def loss(y):
+        M, out, _ = run(y)
+        return (out * dout).sum() + (M * dM).sum()
+
+    G = dM.copy()
+    g = O.backward(G, widx, x["wk"], ridx, x["rw"], x["v"], x["alpha"], x["beta"], run(x)[2], dout)
+    want = dict(M=G, wk=g["dwk"], rw=g["drw"], v=g["dv"], alpha=g["dalpha"], beta=g["dbeta"])
+    for name, grad in want.items():
+        for i in np.ndindex(grad.shape):
+            up, down = ({k: v.copy() for k, v in x.items()} for _ in range(2))
+            up[name][i] += 1e-4
+            down[name][i] -= 1e-4
+            assert abs((loss(up) - loss(down)) / 2e-4 - grad[i]) <= 1e-7, (name, i)
