@@ -32,7 +32,6 @@ Planned scan (fp32 state; few memories, long sequences):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -139,6 +138,11 @@ def _arg(t, dtype, shape, name):
     strided buffer must never reach them.  Every argument of a call passes
     these checks before any device check, so a call fails on the first bad
     shape whatever device its tensors are on."""
+    try:  # the common case first: small calls cost about as much as their checks
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return (name, t)
+    except AttributeError:
+        pass
     import torch
 
     if not isinstance(t, torch.Tensor):
@@ -174,20 +178,23 @@ def _gpu(*args):
     return ptrs
 
 
-@contextlib.contextmanager
-def _on(t, stream):
-    """The stream handle for a call on tensor t's GPU, with that GPU current
-    while the call runs: the caller's stream, or t's GPU's current one.  A
-    stream of another GPU is refused."""
+def _call(fn, t, stream, *args):
+    """fn(*args, stream handle) for a call on tensor t's GPU, with that GPU
+    current while the call runs: on the caller's stream, or on t's GPU's
+    current one.  A stream of another GPU is refused."""
     import torch
 
-    if isinstance(stream, torch.cuda.Stream) and stream.device != t.device:
-        raise ValueError(f"the stream is on {stream.device}, the call's tensors on {t.device}")
-    if t.device.index == torch.cuda.current_device():
-        yield _stream(stream)
+    index = t.get_device()
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _call(fn, t, stream, *args)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
     else:
-        with torch.cuda.device(t.device):
-            yield _stream(stream)
+        if isinstance(stream, torch.cuda.Stream) and stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the call's tensors on {t.device}")
+        handle = _stream(stream)
+    _check(fn(*args, handle))
 
 
 def _state_dtype(M):
@@ -291,8 +298,7 @@ def mx4_quantize(x, out=None, stream=None):
                torch.empty((cols // 128, rows, 4), dtype=torch.uint8, device=x.device))
     codes, scales = out
     px, pc, ps = _gpu(_arg(x, x.dtype, shape, "x"), *_mx4_args(codes, scales, shape))
-    with _on(x, stream) as st:
-        _check(lib().sdm_mx4_quantize(px, dtype, rows, cols, pc, ps, st))
+    _call(lib().sdm_mx4_quantize, x, stream, px, dtype, rows, cols, pc, ps)
     return codes, scales
 
 
@@ -311,8 +317,7 @@ def mx4_dequantize(codes, scales, dtype=None, out=None, stream=None):
         raise ValueError(f"out must be {dtype}, got {out.dtype}")
     dt = _value_dtype(out.dtype)
     pc, ps, px = _gpu(*_mx4_args(codes, scales, shape), _arg(out, out.dtype, shape, "out"))
-    with _on(codes, stream) as st:
-        _check(lib().sdm_mx4_dequantize(pc, ps, dt, _units(shape[:-1]), shape[-1], px, st))
+    _call(lib().sdm_mx4_dequantize, codes, stream, pc, ps, dt, _units(shape[:-1]), shape[-1], px)
     return out
 
 
@@ -329,8 +334,7 @@ def project_mx4(Xq, Xs, Wq, Ws, n: int, out=None, stream=None):
     out, outs = _project_out(B, T, H, P, n, "Wq", out, Xq.device)
     ptrs = _gpu(*_mx4_args(Xq, Xs, (B, T, d_model), ("Xq", "Xs")),
                 *_mx4_args(Wq, Ws, (H, P, d_model), ("Wq", "Ws")), *outs)
-    with _on(Xq, stream) as st:
-        _check(lib().sdm_project_mx4(*ptrs[:4], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[4:], st))
+    _call(lib().sdm_project_mx4, Xq, stream, *ptrs[:4], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[4:])
     return out
 
 
@@ -552,8 +556,7 @@ def scan_train8(M, widx, wk, ridx, rw, v, alpha, beta, out=None, tape=None, stre
                 torch.empty((B, H, d_v // 16, T, W + R), dtype=torch.uint8, device=M.device))
     pm, *ptrs = _gpu(am, *ins, _arg(out, f32, (B, H, T, d_v), "out"),
                      *_tape8_args(tape, B, H, T, W + R, d_v))
-    with _on(M, stream) as st:
-        _check(lib().sdm_scan_train8(pm, B, H, N, d_v, T, W, R, *ptrs, st))
+    _call(lib().sdm_scan_train8, M, stream, pm, B, H, N, d_v, T, W, R, *ptrs)
     return out, tuple(tape)
 
 
@@ -574,8 +577,7 @@ def tape8_read(tape, dtype=None, out=None, stream=None):
         raise ValueError(f"out must be {dtype}, got {out.dtype}")
     dt = _value_dtype(out.dtype)
     pc, ps, po = _gpu(*_tape8_args(tape, B, H, T, S, 16 * nb), _arg(out, out.dtype, shape, "out"))
-    with _on(codes, stream) as st:
-        _check(lib().sdm_tape8_read(pc, ps, B, H, 16 * nb, T, S, dt, po, st))
+    _call(lib().sdm_tape8_read, codes, stream, pc, ps, B, H, 16 * nb, T, S, dt, po)
     return out
 
 
@@ -602,8 +604,7 @@ def scan_backward8(widx, wk, ridx, rw, v, alpha, beta, tape, dout, G, workspace=
         workspace = torch.empty((max(need, 16) + 3) // 4, dtype=f32, device=G.device)
     ptrs = _gpu(*ins, af, _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()
-    with _on(G, stream) as st:
-        _check(lib().sdm_scan_backward8(B, H, N, d_v, T, W, R, *ptrs, nbytes, st))
+    _call(lib().sdm_scan_backward8, G, stream, B, H, N, d_v, T, W, R, *ptrs, nbytes)
     return out
 
 

@@ -174,15 +174,13 @@ __global__ __launch_bounds__(kPThreads) void project_kernel(ProjArgs A) {
 
   // epilogue: lane l, accumulator r of block (i, j) holds C[row][col] with
   // row = 8*(r/4) + 4*(l/32) + r%4 and col = l%32 within the 32 x 32 block
+  ProjColumn c[kPTN];
 #pragma unroll
-  for (int j = 0; j < kPTN; ++j) {
-    const int64_t col = n0 + (wn * kPTN + j) * 32 + lr;
-    if (col >= A.out.Ncols) continue;
-    const ProjColumn c = project_column(A.out, col);
+  for (int j = 0; j < kPTN; ++j)
+    c[j] = project_column(A.out, (uint32_t)(n0 + (wn * kPTN + j) * 32 + lr));
 #pragma unroll
-    for (int i = 0; i < kPTM; ++i)
-      project_store_block(A.out, c, m0 + (wm * kPTM + i) * 32 + 4 * lh, acc[i][j]);
-  }
+  for (int i = 0; i < kPTM; ++i)
+    project_store_blocks(A.out, c, m0 + (wm * kPTM + i) * 32, acc[i]);
 }
 
 }  // namespace

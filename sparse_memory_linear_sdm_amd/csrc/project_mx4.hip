@@ -78,6 +78,14 @@ __device__ __forceinline__ f32x16 mfma32(const i32x4& a, const i32x4& b, const f
                                                          sa, SEL, sb);
 }
 
+// A wavefront's fragments of 64 columns, and its scale words of 128.
+struct Frags {
+  i32x4 a[kXTM], b[kXTN];
+};
+struct Scales {
+  int a[kXTM], b[kXTN];
+};
+
 __global__ __launch_bounds__(kXThreads) void project_mx4_kernel(Mx4Args A) {
   __shared__ __align__(16) uint8_t lds[2 * kXStage];
   const int tid = threadIdx.x, lane = lane_id();
@@ -96,43 +104,50 @@ __global__ __launch_bounds__(kXThreads) void project_mx4_kernel(Mx4Args A) {
 
   // Direct loads.  Codes: load q of wavefront w fills the 64 consecutive
   // 16-byte slots (q * 8 + w) * 64 + lane; slot s is position s % 8 of row
-  // s / 8.  Scales: thread i < 256 (>= 256) loads row i % 256's word of the
-  // stage's first (second) 128 columns.  Rows past the matrix read its last
-  // row (their products land only in outputs that are never stored).
-  const uint8_t *srcA[kXLoads], *srcB[kXLoads];
-  int seg_of[kXLoads];
-#pragma unroll
-  for (int q = 0; q < kXLoads; ++q) {
-    const int s = (q * 8 + w) * kWave + lane, row = s / kXSegs;
-    seg_of[q] = seg_pos(row, s % kXSegs);
-    const int64_t gm = m0 + row < M ? m0 + row : M - 1;
-    const int64_t gn = n0 + row < Ncols ? n0 + row : Ncols - 1;
-    srcA[q] = A.Xq + gm * (A.K / 2) + seg_of[q] * 16;
-    srcB[q] = A.Wq + gn * (A.K / 2) + seg_of[q] * 16;
-  }
-  const int srow = tid & 255, sgrp = tid >> 8;
-  const int64_t sm = m0 + srow < M ? m0 + srow : M - 1;
-  const int64_t sn = n0 + srow < Ncols ? n0 + srow : Ncols - 1;
+  // s / 8, whose swizzle is the same for every q.  Scales: thread i < 256
+  // (>= 256) loads row i % 256's word of the stage's first (second) 128
+  // columns.  Rows past the matrix read its last row (their products land
+  // only in outputs that are never stored).  Offsets are from the tile's
+  // first row: 32 bits (256 rows of at most 32 KiB).
   const int nk = (A.K + kXBK - 1) / kXBK;
   const bool half = A.K % kXBK != 0;  // the last stage holds 128 columns
-  auto issue = [&](int kt, int buf) __attribute__((always_inline)) {
-    uint8_t* base = lds + buf * kXStage;
-    // in a half stage the second half's slots repeat the first (not read)
+  const uint32_t row_bytes = (uint32_t)A.K / 2;
+  const int mrows = (int)(M - m0 < kXBM ? M - m0 : kXBM);
+  const int nrows = (int)(Ncols - n0 < kXBN ? Ncols - n0 : kXBN);
+  const int row0 = w * 8 + lane / kXSegs, seg = seg_pos(row0, lane % kXSegs);
+  uint32_t srcA[kXLoads], srcB[kXLoads];
+#pragma unroll
+  for (int q = 0; q < kXLoads; ++q) {
+    const int row = q * 64 + row0;
+    srcA[q] = (uint32_t)(row < mrows ? row : mrows - 1) * row_bytes + seg * 16;
+    srcB[q] = (uint32_t)(row < nrows ? row : nrows - 1) * row_bytes + seg * 16;
+  }
+  const uint8_t *tileA = A.Xq + m0 * row_bytes, *tileB = A.Wq + n0 * row_bytes;
+  const int srow = tid & 255, g0 = w >> 2;
+  const uint32_t sA = (uint32_t)(srow < mrows ? srow : mrows - 1) * 4;
+  const uint32_t sB = (uint32_t)(srow < nrows ? srow : nrows - 1) * 4;
+  const uint8_t *tileXs = A.Xs + m0 * 4, *tileWs = A.Ws + n0 * 4;
+  // Load stage kt into its buffer (past the last stage: the last one again,
+  // into a buffer no longer read, so that the loop has no branch).  In a half
+  // stage the second half's slots repeat the first (not read).
+  auto issue = [&](int kt) __attribute__((always_inline)) {
+    uint8_t* base = lds + (kt & 1) * kXStage;
+    kt = kt < nk ? kt : nk - 1;
     const bool cut = half && kt == nk - 1;
+    const uint32_t back = cut && seg >= kXSegs / 2 ? kXRow / 2 : 0;
+    const uint8_t *pa = tileA + (int64_t)kt * kXRow, *pb = tileB + (int64_t)kt * kXRow;
 #pragma unroll
     for (int q = 0; q < kXLoads; ++q) {
-      const int64_t back = cut && seg_of[q] >= kXSegs / 2 ? kXRow / 2 : 0;
-      const int64_t at = (int64_t)kt * kXRow - back;
-      __builtin_amdgcn_global_load_lds((const void*)(srcA[q] + at),
+      __builtin_amdgcn_global_load_lds((const void*)(pa + (srcA[q] - back)),
                                        (void*)(base + (q * 8 + w) * kWave * 16), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((const void*)(srcB[q] + at),
+      __builtin_amdgcn_global_load_lds((const void*)(pb + (srcB[q] - back)),
                                        (void*)(base + kXBM * kXRow + (q * 8 + w) * kWave * 16),
                                        16, 0, 0);
     }
-    const int64_t g = 2 * (int64_t)kt + (cut ? 0 : sgrp);
-    __builtin_amdgcn_global_load_lds((const void*)(A.Xs + (g * M + sm) * 4),
+    const int64_t g = 2 * (int64_t)kt + (cut ? 0 : g0);
+    __builtin_amdgcn_global_load_lds((const void*)(tileXs + g * M * 4 + sA),
                                      (void*)(base + kXCodes + w * kWave * 4), 4, 0, 0);
-    __builtin_amdgcn_global_load_lds((const void*)(A.Ws + (g * Ncols + sn) * 4),
+    __builtin_amdgcn_global_load_lds((const void*)(tileWs + g * Ncols * 4 + sB),
                                      (void*)(base + kXCodes + (kXThreads + w * kWave) * 4), 4, 0,
                                      0);
   };
@@ -142,20 +157,12 @@ __global__ __launch_bounds__(kXThreads) void project_mx4_kernel(Mx4Args A) {
   // Fragment of 64 columns: lane l holds columns 32 * (l / 32) .. + 31 of row
   // l % 32, i.e. segment 2 * kk + l / 32 of the stage's row; its scale is
   // byte 2 * (kk % 2) + l / 32 of word kk / 2, taken after a shift by l / 32
-  // bytes as byte 2 * (kk % 2) of every lane.
-  int offA[kXTM], offB[kXTN], scA[kXTM], scB[kXTN];
-#pragma unroll
-  for (int i = 0; i < kXTM; ++i) {
-    const int row = (wm * kXTM + i) * 32 + lr;
-    offA[i] = row * kXRow + seg_pos(row, lh) * 16;
-    scA[i] = kXCodes + row * 4;
-  }
-#pragma unroll
-  for (int j = 0; j < kXTN; ++j) {
-    const int row = (wn * kXTN + j) * 32 + lr;
-    offB[j] = kXBM * kXRow + row * kXRow + seg_pos(row, lh) * 16;
-    scB[j] = kXCodes + kXThreads * 4 + row * 4;
-  }
+  // bytes as byte 2 * (kk % 2) of every lane.  The next 32 rows lie 4096
+  // bytes on (the swizzle repeats every 16 rows).
+  const int rowA = wm * kXTM * 32 + lr, rowB = wn * kXTN * 32 + lr;
+  const int offA = rowA * kXRow + seg_pos(rowA, lh) * 16;
+  const int offB = kXBM * kXRow + rowB * kXRow + seg_pos(rowB, lh) * 16;
+  const int scA = kXCodes + rowA * 4, scB = kXCodes + kXThreads * 4 + rowB * 4;
   f32x16 acc[kXTM][kXTN];
 #pragma unroll
   for (int i = 0; i < kXTM; ++i)
@@ -164,53 +171,92 @@ __global__ __launch_bounds__(kXThreads) void project_mx4_kernel(Mx4Args A) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  issue(0, 0);
-  for (int kt = 0; kt < nk; ++kt) {
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));  // this wavefront's loads of stage kt are in
-    stage_barrier();  // every wavefront's part of stage kt is in; stage kt-1 is read
-    if (kt + 1 < nk) issue(kt + 1, (kt + 1) & 1);
+  // Two sets of fragments: while the matrix cores take one, the next 64
+  // columns' are read from LDS into the other, across the stage boundary too.
+  Frags fr[2];
+  Scales sc[2];
+  auto read = [&](int kt, int kk) __attribute__((always_inline)) {
     const uint8_t* base = lds + (kt & 1) * kXStage;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      if (g == 1 && half && kt == nk - 1) break;
-      int sa[kXTM], sb[kXTN];
-#pragma unroll
-      for (int i = 0; i < kXTM; ++i)
-        sa[i] = *reinterpret_cast<const int*>(base + scA[i] + g * 1024) >> (8 * lh);
+    const uint8_t *pa = base + (offA ^ (kk * 32)), *pb = base + (offB ^ (kk * 32));
+    Frags& f = fr[kk & 1];
+    if (kk % 2 == 0) {
+      Scales& s = sc[kk / 2];
 #pragma unroll
       for (int j = 0; j < kXTN; ++j)
-        sb[j] = *reinterpret_cast<const int*>(base + scB[j] + g * 1024) >> (8 * lh);
+        s.b[j] = *reinterpret_cast<const int*>(base + scB + (kk / 2) * 1024 + j * 128);
 #pragma unroll
-      for (int k2 = 0; k2 < 2; ++k2) {
-        const int kk = 2 * g + k2;
-        i32x4 a[kXTM], b[kXTN];
-#pragma unroll
-        for (int i = 0; i < kXTM; ++i)
-          a[i] = *reinterpret_cast<const i32x4*>(base + (offA[i] ^ (kk * 32)));
-#pragma unroll
-        for (int j = 0; j < kXTN; ++j)
-          b[j] = *reinterpret_cast<const i32x4*>(base + (offB[j] ^ (kk * 32)));
-#pragma unroll
-        for (int i = 0; i < kXTM; ++i)
-#pragma unroll
-          for (int j = 0; j < kXTN; ++j)
-            acc[i][j] = k2 == 0 ? mfma32<0>(a[i], b[j], acc[i][j], sa[i], sb[j])
-                                : mfma32<2>(a[i], b[j], acc[i][j], sa[i], sb[j]);
-      }
+      for (int i = 0; i < kXTM; ++i)
+        s.a[i] = *reinterpret_cast<const int*>(base + scA + (kk / 2) * 1024 + i * 128);
     }
+#pragma unroll
+    for (int j = 0; j < kXTN; ++j) f.b[j] = *reinterpret_cast<const i32x4*>(pb + j * 32 * kXRow);
+#pragma unroll
+    for (int i = 0; i < kXTM; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(pa + i * 32 * kXRow);
+  };
+  auto mul = [&](int kk) __attribute__((always_inline)) {
+    const Frags& f = fr[kk & 1];
+    Scales& s = sc[kk / 2];
+    if (kk % 2 == 0) {
+#pragma unroll
+      for (int j = 0; j < kXTN; ++j) s.b[j] >>= 8 * lh;
+#pragma unroll
+      for (int i = 0; i < kXTM; ++i) s.a[i] >>= 8 * lh;
+    }
+#pragma unroll
+    for (int i = 0; i < kXTM; ++i)
+#pragma unroll
+      for (int j = 0; j < kXTN; ++j)
+        acc[i][j] = kk % 2 == 0 ? mfma32<0>(f.a[i], f.b[j], acc[i][j], s.a[i], s.b[j])
+                                : mfma32<2>(f.a[i], f.b[j], acc[i][j], s.a[i], s.b[j]);
+  };
+  // One phase: the next fragments' reads go out, then the matrix
+  // instructions of the present ones.  (Left to itself the compiler gathers
+  // the reads of a whole stage in front, which does not fit the registers.)
+  auto phase = [&](int kk, int kt_next, int kk_next) __attribute__((always_inline)) {
+    read(kt_next, kk_next);
+    __builtin_amdgcn_sched_barrier(0);
+    mul(kk);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  issue(0);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  stage_barrier();
+  issue(1);
+  read(0, 0);
+  for (int kt = 0; kt < nk - 1; ++kt) {
+    phase(0, kt, 1);
+    phase(1, kt, 2);
+    phase(2, kt, 3);
+    // stage kt + 1 is in, and stage kt's last fragments are in registers, for
+    // this wavefront; after the barrier for all of them
+    __builtin_amdgcn_s_waitcnt(0);
+    stage_barrier();
+    issue(kt + 2);
+    phase(3, kt + 1, 0);
   }
+  if (!half) {
+    phase(0, nk - 1, 1);
+    phase(1, nk - 1, 2);
+    phase(2, nk - 1, 3);
+    mul(3);
+  } else {
+    phase(0, nk - 1, 1);
+    mul(1);
+  }
+
+  // no load may reach LDS after the workgroup has left it
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
 
   // lane l, accumulator r of block (i, j) holds C[row][col] with
   // row = 8*(r/4) + 4*(l/32) + r%4 and col = l%32 within the 32 x 32 block
+  ProjColumn c[kXTN];
 #pragma unroll
-  for (int j = 0; j < kXTN; ++j) {
-    const int64_t col = n0 + (wn * kXTN + j) * 32 + lr;
-    if (col >= Ncols) continue;
-    const ProjColumn c = project_column(A.out, col);
+  for (int j = 0; j < kXTN; ++j)
+    c[j] = project_column(A.out, (uint32_t)(n0 + (wn * kXTN + j) * 32 + lr));
 #pragma unroll
-    for (int i = 0; i < kXTM; ++i)
-      project_store_block(A.out, c, m0 + (wm * kXTM + i) * 32 + 4 * lh, acc[i][j]);
-  }
+  for (int i = 0; i < kXTM; ++i)
+    project_store_blocks(A.out, c, m0 + (wm * kXTM + i) * 32, acc[i]);
 }
 
 // Few tokens: at most 16 * MT of them against every column.  The weights are
@@ -301,7 +347,8 @@ __global__ __launch_bounds__(kFewWaves* kWave) void project_mx4_few(Mx4Args A) {
 #pragma unroll
       for (int k = 0; k < kFewWaves; ++k) y += part[q][k][l][r];
       const int64_t row = 16 * i + 4 * (l >> 4) + r, col = n0 + 16 * j + (l & 15);
-      if (row < M && col < Ncols) project_store_one(A.out, project_column(A.out, col), row, y);
+      if (row < M && col < Ncols) project_store_one(A.out, project_column(A.out, (uint32_t)col),
+                                                     project_token(A.out, (uint32_t)row), y);
     }
   }
 }
