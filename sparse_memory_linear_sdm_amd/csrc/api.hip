@@ -107,8 +107,8 @@ int check_project_sizes(int B, int T, int H, int n, int d_v) {
     return fail(SDM_ERR_UNSUPPORTED, "H*(4n + d_v + 2) must be below 2^31 (got %d * %lld)", H,
                 (long long)P);
   const int64_t cols = (int64_t)H * P, M = (int64_t)B * T;
-  if (M > 0 && sdm::project_blocks(M, cols) > sdm::kMaxStrideBlocks)
-    return fail(SDM_ERR_UNSUPPORTED, "more than 2^24 - 1 output tiles of 256 x 256 (B*T=%lld, "
+  if (M > 0 && sdm::project_blocks(M, cols) > sdm::kMaxProjTiles)
+    return fail(SDM_ERR_UNSUPPORTED, "more than 2^23 - 1 output tiles of 256 x 256 (B*T=%lld, "
                 "H*P=%lld); split the tokens over several calls", (long long)M, (long long)cols);
   return SDM_OK;
 }

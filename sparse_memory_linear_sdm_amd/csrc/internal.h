@@ -26,12 +26,16 @@ constexpr int64_t kMaxMemorySteps = (int64_t)1 << 40;
 //   256 threads and loop over the rest.
 constexpr int64_t kMaxStrideBlocks = ((int64_t)1 << 24) - 1;
 
+// Compute units of the current device (cached per device; scan.hip).
+int compute_units();
+
 hipError_t launch_select(const float* x1, const float* x2, int64_t units, int n, int K,
                          int32_t* idx, float* score, float* weight, hipStream_t stream);
 
 // Token projections (project.hip): one workgroup per kProjTile x kProjTile
 // tile of the [tokens, H*P] output, d_model a multiple of 64.
 constexpr int kProjTile = 256;
+constexpr int64_t kMaxProjTiles = ((int64_t)1 << 23) - 1;  // workgroups of 512 threads
 inline int64_t project_blocks(int64_t M, int64_t Ncols) {
   return ((M + kProjTile - 1) / kProjTile) * ((Ncols + kProjTile - 1) / kProjTile);
 }
@@ -55,9 +59,7 @@ hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t rows, int cols,
 hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype,
                                  int64_t rows, int cols, void* x, hipStream_t stream);
 
-// Projections from 4-bit operands (project_mx4.hip): up to this many tokens
-// the weights are streamed once per call; from there on 256 x 256 tiles.
-constexpr int64_t kProjFewTokens = 64;
+// Projections from 4-bit operands (project_mx4.hip).
 hipError_t launch_project_mx4(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq,
                               const uint8_t* Ws, int B, int T, int d_model, int H, int n, int d_v,
                               float* s1, float* s2, float* q1, float* q2, float* v, float* alpha,

@@ -7,16 +7,23 @@
 //
 // Many tokens: project_mx4_kernel, a 256 x 256 tile of tokens x columns per
 // 512-thread workgroup, 2 x 4 wavefronts of 128 x 64, each 4 x 2 blocks of
-// v_mfma_scale_f32_32x32x64_f8f6f4.  K is taken 256 at a time (128 bytes of
-// codes and two 4-byte scale words per row) through two LDS stages filled by
-// direct global-to-LDS loads; the 16-byte segments of a row are swizzled so
-// that the fragment reads are free of bank conflicts.  Tiles are numbered so
-// that each XCD gets a contiguous range, grouped along M.
+// v_mfma_scale_f32_32x32x64_f8f6f4.  K is taken 128 at a time (64 bytes of
+// codes and a 4-byte scale word per row) through a ring of four LDS stages
+// filled by direct global-to-LDS loads, three of them in flight; the 16-byte
+// segments of a row are swizzled so that the fragment reads are free of bank
+// conflicts.  Tiles are numbered so that each XCD gets a contiguous range,
+// grouped 8 deep along M.  Per compute unit and 128 of K the matrix cores need
+// 1024 cycles, LDS about as many (the reads of eight wavefronts and the 34 KB
+// that arrive), so the order inside a stage decides: a matrix instruction, then
+// two fragment reads or a load, and so on, against all reads first, is 8.1
+// against 9.3 ms without the outputs.  32768 tokens x 33808 columns at d_model
+// 16384: 9.1-9.6 ms, 3.8-4.0 PFLOP/s (bf16 tiles: 33 ms).  What bounds it: with
+// no loads in flight the same loop reaches 5.9, bare matrix instructions on
+// random codes 6.3 (8.8 on zeros: the card's power limit sets the clock), and
+// the outputs' 4.4 GB take 1.0 ms that nothing overlaps.
 //
 // Few tokens (a decode step): project_mx4_few, bound by streaming the weights
 // once.  See there.
-#include <type_traits>
-
 #include "internal.h"
 #include "mx.h"
 #include "project_store.h"
@@ -28,20 +35,34 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kXBM = kProjTile, kXBN = kProjTile;  // output tile
-constexpr int kXBK = 256;                           // K per stage
+constexpr int kXBK = 128;                           // K per stage
+constexpr int kXStages = 4;
 constexpr int kXRow = kXBK / 2;                     // code bytes of a row in a stage
 constexpr int kXThreads = 512;                      // 8 wavefronts
 constexpr int kXWavesM = 2;                         // wavefront grid 2 (M) x 4 (N)
 constexpr int kXTM = 4, kXTN = 2;                   // 32 x 32 blocks per wavefront
 constexpr int kXSegs = kXRow / 16;                  // 16-byte segments per row
 constexpr int kXCodes = (kXBM + kXBN) * kXRow;      // code bytes per stage
-constexpr int kXScales = 2 * (kXBM + kXBN) * 4;     // scale bytes per stage: 2 words per row
+constexpr int kXScales = (kXBM + kXBN) * 4;         // scale bytes per stage: a word per row
 constexpr int kXStage = kXCodes + kXScales;
 constexpr int kXLoads = kXBM * kXSegs / kXThreads;  // 16-byte loads per thread, operand, stage
+constexpr int kXIssued = 2 * kXLoads + 1;           // loads per wavefront and stage
 constexpr int kXGroupM = 8;
-static_assert(kXLoads == 4 && kXSegs == 8, "the slot numbering assumes 4 loads of 8 segments");
-static_assert(kXScales == 2 * kXThreads * 4, "two scale words per thread and stage");
-static_assert(2 * kXStage <= 160 * 1024, "two stages in LDS");
+static_assert(kXLoads == 2 && kXSegs == 4, "the slot numbering assumes 2 loads of 4 segments");
+static_assert(kXScales == kXThreads * 4, "a scale word per thread and stage");
+static_assert(kXStages * kXStage <= 160 * 1024, "the stages in LDS");
+
+// Scheduling of one half stage: a matrix instruction, then one LDS read and
+// one memory load while it runs.
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < kXTM * kXTN; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS read
+    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // memory load
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
 
 struct Mx4Args {
   const uint8_t *Xq, *Xs, *Wq, *Ws;
@@ -51,10 +72,12 @@ struct Mx4Args {
 };
 
 // position of 16-byte segment `seg` in row `row` of a stage
-__device__ __forceinline__ int seg_pos(int row, int seg) { return seg ^ ((row >> 1) & 7); }
+__device__ __forceinline__ int seg_pos(int row, int seg) { return seg ^ ((row >> 2) & 3); }
 
 // s_waitcnt with only the vector-memory count limited: vmcnt(n), n < 16
 constexpr int waitcnt_vm(int n) { return (n & 15) | (7 << 4) | (15 << 8); }
+// the same, and every LDS access done
+constexpr int waitcnt_vm_lgkm0(int n) { return (n & 15) | (7 << 4); }
 
 // a workgroup barrier without a memory fence (the direct loads are waited for
 // by count just before it); the empty asm keeps LDS accesses on their side
@@ -87,7 +110,7 @@ struct Scales {
 };
 
 __global__ __launch_bounds__(kXThreads) void project_mx4_kernel(Mx4Args A) {
-  __shared__ __align__(16) uint8_t lds[2 * kXStage];
+  __shared__ __align__(16) uint8_t lds[kXStages * kXStage];
   const int tid = threadIdx.x, lane = lane_id();
   const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int64_t M = A.out.M, Ncols = A.out.Ncols;
@@ -103,66 +126,57 @@ __global__ __launch_bounds__(kXThreads) void project_mx4_kernel(Mx4Args A) {
   const int64_t m0 = pm * kXBM, n0 = pn * kXBN;
 
   // Direct loads.  Codes: load q of wavefront w fills the 64 consecutive
-  // 16-byte slots (q * 8 + w) * 64 + lane; slot s is position s % 8 of row
-  // s / 8, whose swizzle is the same for every q.  Scales: thread i < 256
-  // (>= 256) loads row i % 256's word of the stage's first (second) 128
-  // columns.  Rows past the matrix read its last row (their products land
-  // only in outputs that are never stored).  Offsets are from the tile's
-  // first row: 32 bits (256 rows of at most 32 KiB).
-  const int nk = (A.K + kXBK - 1) / kXBK;
-  const bool half = A.K % kXBK != 0;  // the last stage holds 128 columns
+  // 16-byte slots (q * 8 + w) * 64 + lane; slot s is position s % 4 of row
+  // s / 4, whose swizzle is the same for every q.  Scales: thread i < 256
+  // (>= 256) loads token (column) i % 256's word.  Rows past the matrix read
+  // its last row (their products land only in outputs that are never stored).
+  // Offsets are from the tile's first row: 32 bits (256 rows of at most 32 KiB).
+  const int nk = A.K / kXBK;
   const uint32_t row_bytes = (uint32_t)A.K / 2;
   const int mrows = (int)(M - m0 < kXBM ? M - m0 : kXBM);
   const int nrows = (int)(Ncols - n0 < kXBN ? Ncols - n0 : kXBN);
-  const int row0 = w * 8 + lane / kXSegs, seg = seg_pos(row0, lane % kXSegs);
+  const int lrow = w * 16 + lane / kXSegs, seg = seg_pos(lrow, lane % kXSegs);
   uint32_t srcA[kXLoads], srcB[kXLoads];
 #pragma unroll
   for (int q = 0; q < kXLoads; ++q) {
-    const int row = q * 64 + row0;
+    const int row = q * 128 + lrow;
     srcA[q] = (uint32_t)(row < mrows ? row : mrows - 1) * row_bytes + seg * 16;
     srcB[q] = (uint32_t)(row < nrows ? row : nrows - 1) * row_bytes + seg * 16;
   }
   const uint8_t *tileA = A.Xq + m0 * row_bytes, *tileB = A.Wq + n0 * row_bytes;
-  const int srow = tid & 255, g0 = w >> 2;
-  const uint32_t sA = (uint32_t)(srow < mrows ? srow : mrows - 1) * 4;
-  const uint32_t sB = (uint32_t)(srow < nrows ? srow : nrows - 1) * 4;
-  const uint8_t *tileXs = A.Xs + m0 * 4, *tileWs = A.Ws + n0 * 4;
+  const int srow = tid & 255, slim = w < 4 ? mrows : nrows;
+  const uint32_t srcS = (uint32_t)(srow < slim ? srow : slim - 1) * 4;
+  const uint8_t* const tileS = w < 4 ? A.Xs + m0 * 4 : A.Ws + n0 * 4;
+  const int64_t stepS = (w < 4 ? M : Ncols) * 4;
   // Load stage kt into its buffer (past the last stage: the last one again,
-  // into a buffer no longer read, so that the loop has no branch).  In a half
-  // stage the second half's slots repeat the first (not read).
+  // into a buffer no longer read, so that the loop has no branch).
   auto issue = [&](int kt) __attribute__((always_inline)) {
-    uint8_t* base = lds + (kt & 1) * kXStage;
+    uint8_t* base = lds + (kt % kXStages) * kXStage;
     kt = kt < nk ? kt : nk - 1;
-    const bool cut = half && kt == nk - 1;
-    const uint32_t back = cut && seg >= kXSegs / 2 ? kXRow / 2 : 0;
     const uint8_t *pa = tileA + (int64_t)kt * kXRow, *pb = tileB + (int64_t)kt * kXRow;
 #pragma unroll
     for (int q = 0; q < kXLoads; ++q) {
-      __builtin_amdgcn_global_load_lds((const void*)(pa + (srcA[q] - back)),
+      __builtin_amdgcn_global_load_lds((const void*)(pa + srcA[q]),
                                        (void*)(base + (q * 8 + w) * kWave * 16), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((const void*)(pb + (srcB[q] - back)),
+      __builtin_amdgcn_global_load_lds((const void*)(pb + srcB[q]),
                                        (void*)(base + kXBM * kXRow + (q * 8 + w) * kWave * 16),
                                        16, 0, 0);
     }
-    const int64_t g = 2 * (int64_t)kt + (cut ? 0 : g0);
-    __builtin_amdgcn_global_load_lds((const void*)(tileXs + g * M * 4 + sA),
+    __builtin_amdgcn_global_load_lds((const void*)(tileS + kt * stepS + srcS),
                                      (void*)(base + kXCodes + w * kWave * 4), 4, 0, 0);
-    __builtin_amdgcn_global_load_lds((const void*)(tileWs + g * Ncols * 4 + sB),
-                                     (void*)(base + kXCodes + (kXThreads + w * kWave) * 4), 4, 0,
-                                     0);
   };
 
   const int wm = w % kXWavesM, wn = w / kXWavesM;  // this wavefront's 128 x 64 part of the tile
   const int lr = lane & 31, lh = lane >> 5;
   // Fragment of 64 columns: lane l holds columns 32 * (l / 32) .. + 31 of row
   // l % 32, i.e. segment 2 * kk + l / 32 of the stage's row; its scale is
-  // byte 2 * (kk % 2) + l / 32 of word kk / 2, taken after a shift by l / 32
-  // bytes as byte 2 * (kk % 2) of every lane.  The next 32 rows lie 4096
-  // bytes on (the swizzle repeats every 16 rows).
+  // byte 2 * kk + l / 32 of the row's word, taken after a shift by l / 32
+  // bytes as byte 2 * kk of every lane.  The next 32 rows lie 2048 bytes on
+  // (the swizzle repeats every 16 rows).
   const int rowA = wm * kXTM * 32 + lr, rowB = wn * kXTN * 32 + lr;
   const int offA = rowA * kXRow + seg_pos(rowA, lh) * 16;
   const int offB = kXBM * kXRow + rowB * kXRow + seg_pos(rowB, lh) * 16;
-  const int scA = kXCodes + rowA * 4, scB = kXCodes + kXThreads * 4 + rowB * 4;
+  const int scA = kXCodes + rowA * 4, scB = kXCodes + kXBM * 4 + rowB * 4;
   f32x16 acc[kXTM][kXTN];
 #pragma unroll
   for (int i = 0; i < kXTM; ++i)
@@ -171,32 +185,30 @@ __global__ __launch_bounds__(kXThreads) void project_mx4_kernel(Mx4Args A) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  // Two sets of fragments: while the matrix cores take one, the next 64
-  // columns' are read from LDS into the other, across the stage boundary too.
+  // Two sets of fragments and scales: while the matrix cores take one, the
+  // next 64 columns' are read from LDS into the other, across the stage
+  // boundary too.
   Frags fr[2];
   Scales sc[2];
-  auto read = [&](int kt, int kk) __attribute__((always_inline)) {
-    const uint8_t* base = lds + (kt & 1) * kXStage;
+  auto read = [&](int kt, int kk, int set) __attribute__((always_inline)) {
+    const uint8_t* base = lds + (kt % kXStages) * kXStage;
     const uint8_t *pa = base + (offA ^ (kk * 32)), *pb = base + (offB ^ (kk * 32));
-    Frags& f = fr[kk & 1];
-    if (kk % 2 == 0) {
-      Scales& s = sc[kk / 2];
+    Frags& f = fr[kk];
+    if (kk == 0) {
 #pragma unroll
-      for (int j = 0; j < kXTN; ++j)
-        s.b[j] = *reinterpret_cast<const int*>(base + scB + (kk / 2) * 1024 + j * 128);
+      for (int j = 0; j < kXTN; ++j) sc[set].b[j] = *reinterpret_cast<const int*>(base + scB + j * 128);
 #pragma unroll
-      for (int i = 0; i < kXTM; ++i)
-        s.a[i] = *reinterpret_cast<const int*>(base + scA + (kk / 2) * 1024 + i * 128);
+      for (int i = 0; i < kXTM; ++i) sc[set].a[i] = *reinterpret_cast<const int*>(base + scA + i * 128);
     }
 #pragma unroll
     for (int j = 0; j < kXTN; ++j) f.b[j] = *reinterpret_cast<const i32x4*>(pb + j * 32 * kXRow);
 #pragma unroll
     for (int i = 0; i < kXTM; ++i) f.a[i] = *reinterpret_cast<const i32x4*>(pa + i * 32 * kXRow);
   };
-  auto mul = [&](int kk) __attribute__((always_inline)) {
-    const Frags& f = fr[kk & 1];
-    Scales& s = sc[kk / 2];
-    if (kk % 2 == 0) {
+  auto mul = [&](int kk, int set) __attribute__((always_inline)) {
+    const Frags& f = fr[kk];
+    Scales& s = sc[set];
+    if (kk == 0) {
 #pragma unroll
       for (int j = 0; j < kXTN; ++j) s.b[j] >>= 8 * lh;
 #pragma unroll
@@ -206,44 +218,36 @@ __global__ __launch_bounds__(kXThreads) void project_mx4_kernel(Mx4Args A) {
     for (int i = 0; i < kXTM; ++i)
 #pragma unroll
       for (int j = 0; j < kXTN; ++j)
-        acc[i][j] = kk % 2 == 0 ? mfma32<0>(f.a[i], f.b[j], acc[i][j], s.a[i], s.b[j])
-                                : mfma32<2>(f.a[i], f.b[j], acc[i][j], s.a[i], s.b[j]);
+        acc[i][j] = kk == 0 ? mfma32<0>(f.a[i], f.b[j], acc[i][j], s.a[i], s.b[j])
+                            : mfma32<2>(f.a[i], f.b[j], acc[i][j], s.a[i], s.b[j]);
   };
-  // One phase: the next fragments' reads go out, then the matrix
-  // instructions of the present ones.  (Left to itself the compiler gathers
-  // the reads of a whole stage in front, which does not fit the registers.)
-  auto phase = [&](int kk, int kt_next, int kk_next) __attribute__((always_inline)) {
-    read(kt_next, kk_next);
-    __builtin_amdgcn_sched_barrier(0);
-    mul(kk);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-
-  issue(0);
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-  stage_barrier();
-  issue(1);
-  read(0, 0);
-  for (int kt = 0; kt < nk - 1; ++kt) {
-    phase(0, kt, 1);
-    phase(1, kt, 2);
-    phase(2, kt, 3);
+  // One stage: the next fragments' reads go out, then the matrix instructions
+  // of the present ones, twice.  (Left to itself the compiler gathers the
+  // reads in front, which does not fit the registers.)
+  auto stage = [&](int kt, int set) __attribute__((always_inline)) {
+    issue(kt + kXStages - 1);  // into the buffer of stage kt - 1, read before the last barrier
+    read(kt, 1, set);
+    mul(0, set);
+    interleave();
     // stage kt + 1 is in, and stage kt's last fragments are in registers, for
     // this wavefront; after the barrier for all of them
-    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((kXStages - 2) * kXIssued));
     stage_barrier();
-    issue(kt + 2);
-    phase(3, kt + 1, 0);
+    read(kt + 1, 0, set ^ 1);
+    mul(1, set);
+    interleave();
+  };
+#pragma unroll
+  for (int kt = 0; kt < kXStages - 1; ++kt) issue(kt);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm((kXStages - 2) * kXIssued));
+  stage_barrier();
+  read(0, 0, 0);
+  int kt = 0;
+  for (; kt + 1 < nk; kt += 2) {
+    stage(kt, 0);
+    stage(kt + 1, 1);
   }
-  if (!half) {
-    phase(0, nk - 1, 1);
-    phase(1, nk - 1, 2);
-    phase(2, nk - 1, 3);
-    mul(3);
-  } else {
-    phase(0, nk - 1, 1);
-    mul(1);
-  }
+  if (kt < nk) stage(kt, 0);
 
   // no load may reach LDS after the workgroup has left it
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
@@ -259,40 +263,70 @@ __global__ __launch_bounds__(kXThreads) void project_mx4_kernel(Mx4Args A) {
     project_store_blocks(A.out, c, m0 + (wm * kXTM + i) * 32, acc[i]);
 }
 
-// Few tokens: at most 16 * MT of them against every column.  The weights are
-// read once, straight into registers (no LDS: each code is used by one
-// wavefront only); the tokens' codes come from L2.  A workgroup owns 16 * CT
-// columns and its kFewWaves wavefronts split K in turns of 128 columns, so
-// together they walk each weight row in runs of kFewWaves * 64 bytes; each
-// keeps kFewAhead turns of loads in flight.  v_mfma_scale_f32_16x16x128_f8f6f4:
-// lane l holds columns 32 * (l / 16) .. + 31 of the 128 of row l % 16.  The
-// wavefronts' sums meet in LDS and are added in wavefront order (the same
-// result every time).
-constexpr int kFewWaves = 8;
-constexpr int kFewAhead = 4;
+// Few tokens: 16 * MT tokens (MT = 4: blocks of 64) against 16 * CT columns
+// per workgroup, whose wavefronts split K in turns of 128 columns, so that
+// together they walk each row in runs of 512 (256) bytes; no barrier until
+// their sums meet in LDS, where they are added in wavefront order (the same
+// result every time).  v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds columns
+// 32 * (l / 16) .. + 31 of the 128 of row l % 16.
+//
+// Bound by memory (each weight is read once per 64 tokens), and below that by
+// the rate of load instructions: a fragment loaded as the matrix cores want
+// it has 16 bytes of another row on every lane, 64 requests, and took 145 us
+// for 64 tokens at d_model 16384 x 33808 columns.  So four neighbouring lanes
+// load 64 bytes of a row, the turn's fragments pass through the wavefront's own
+// piece of LDS (16-byte segments swizzled as in the tiles), and the turn after
+// it is in flight in registers: 90 us, floor 63; one token 57-59 us.
+template <int MT, int CT>
+constexpr int few_waves() {  // the accumulators of 4 x 7 blocks and up leave room for four
+  return MT * CT >= 28 ? 4 : 8;
+}
 
 template <int MT, int CT>
-__global__ __launch_bounds__(kFewWaves* kWave) void project_mx4_few(Mx4Args A) {
-  constexpr int kBlocks = MT * CT;                     // 16 x 16 output blocks
-  constexpr int kTurn = kBlocks < 4 ? kBlocks : 4;     // of them summed at a time
-  __shared__ f32x4 part[kTurn][kFewWaves][kWave];
+__global__ __launch_bounds__((few_waves<MT, CT>() * kWave)) void project_mx4_few(Mx4Args A) {
+  constexpr int kWaves = few_waves<MT, CT>();
+  constexpr int NF = MT + CT;                       // fragments of a turn
+  constexpr int kBlocks = MT * CT;                  // 16 x 16 output blocks
+  constexpr int kTurn = kBlocks % 4 == 0 ? 4 : kBlocks % 3 == 0 ? 3 : kBlocks % 2 == 0 ? 2 : 1;
+  constexpr int kMine = NF * 1024 + NF * 64;        // a wavefront's LDS: codes, scale words
+  constexpr int kSums = kTurn * kWaves * kWave * 16;
+  constexpr int kLoadsW = (16 * CT + kWave - 1) / kWave;  // scale-word loads of the columns
+  __shared__ __align__(16) uint8_t lds[kWaves * kMine > kSums ? kWaves * kMine : kSums];
   const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lr = lane & 15, lh = lane >> 4;
   const int64_t M = A.out.M, Ncols = A.out.Ncols;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * CT);
-  const uint8_t *xq[MT], *xs[MT], *wq[CT], *ws[CT];
+  // blocks are dealt to the 8 XCDs in turn: the token blocks of a column block
+  // follow each other on one of them, so its weights come from that L2
+  const int x = blockIdx.x & 7, rest = blockIdx.x >> 3;
+  const int64_t m0 = (int64_t)(rest % A.nbm) * (16 * MT);
+  const int64_t n0 = ((int64_t)(rest / A.nbm) * 8 + x) * (16 * CT);
+  if (n0 >= Ncols) return;  // whole workgroup leaves together
+
+  // Loads: lane l takes segment (l % 4) ^ swizzle of row l / 4 of a fragment's
+  // 16; rows past the end repeat the last one (not stored).  Offsets are from
+  // the workgroup's first rows: 32 bits (at most 144 rows of 32 KiB).
+  const uint32_t row_bytes = (uint32_t)A.K / 2;
+  const int row = lane >> 2, seg = seg_pos(row, lane & 3);
+  const int mrows = (int)(M - m0 < 16 * MT ? M - m0 : 16 * MT);
+  const int nrows = (int)(Ncols - n0 < 16 * CT ? Ncols - n0 : 16 * CT);
+  uint32_t src[NF], srcWs[kLoadsW];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {  // rows past the end repeat the last one (not stored)
-    const int64_t r = 16 * i + lr < M ? 16 * i + lr : M - 1;
-    xq[i] = A.Xq + r * (A.K / 2) + lh * 16;
-    xs[i] = A.Xs + r * 4 + lh;
+  for (int f = 0; f < NF; ++f) {
+    const int r = 16 * (f < MT ? f : f - MT) + row, last = (f < MT ? mrows : nrows) - 1;
+    src[f] = (uint32_t)(r < last ? r : last) * row_bytes + seg * 16;
   }
+  const uint32_t srcXs = (uint32_t)(lane < mrows ? lane : mrows - 1) * 4;
 #pragma unroll
-  for (int j = 0; j < CT; ++j) {
-    const int64_t c = n0 + 16 * j + lr < Ncols ? n0 + 16 * j + lr : Ncols - 1;
-    wq[j] = A.Wq + c * (A.K / 2) + lh * 16;
-    ws[j] = A.Ws + c * 4 + lh;
+  for (int z = 0; z < kLoadsW; ++z) {
+    const int c = z * kWave + lane;
+    srcWs[z] = (uint32_t)(c < nrows ? c : nrows - 1) * 4;
   }
+  const uint8_t *xq = A.Xq + m0 * row_bytes, *wq = A.Wq + n0 * row_bytes;
+  const uint8_t *xs = A.Xs + m0 * 4, *ws = A.Ws + n0 * 4;
+  uint8_t* const mine = lds + w * kMine;
+  uint32_t* const sx = reinterpret_cast<uint32_t*>(mine + NF * 1024);
+  uint32_t* const sw = sx + 16 * MT;
+  const int frag = lr * 64 + seg_pos(lr, lh) * 16;
   f32x4 acc[MT][CT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -300,64 +334,120 @@ __global__ __launch_bounds__(kFewWaves* kWave) void project_mx4_few(Mx4Args A) {
     for (int j = 0; j < CT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int G = A.K / 128;
-  auto turns = [&](int g, auto count) __attribute__((always_inline)) {
-    constexpr int U = decltype(count)::value;
-    i32x4 a[U][MT], b[U][CT];
-    int sa[U][MT], sb[U][CT];
+  i32x4 next[NF];
+  uint32_t nextXs, nextWs[kLoadsW];
+  auto load = [&](int g) __attribute__((always_inline)) {
+    const int64_t gu = g < G ? g : G - 1;  // past the end: again, not used
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t gu = g + u * kFewWaves;
+    for (int f = 0; f < NF; ++f)
+      next[f] = *reinterpret_cast<const i32x4*>((f < MT ? xq : wq) + gu * 64 + src[f]);
+    nextXs = *reinterpret_cast<const uint32_t*>(xs + gu * M * 4 + srcXs);
 #pragma unroll
-      for (int j = 0; j < CT; ++j) {
-        b[u][j] = *reinterpret_cast<const i32x4*>(wq[j] + gu * 64);
-        sb[u][j] = ws[j][gu * Ncols * 4];
-      }
+    for (int z = 0; z < kLoadsW; ++z)
+      nextWs[z] = *reinterpret_cast<const uint32_t*>(ws + gu * Ncols * 4 + srcWs[z]);
+  };
+  load(w);
+  for (int g = w; g < G; g += kWaves) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        a[u][i] = *reinterpret_cast<const i32x4*>(xq[i] + gu * 64);
-        sa[u][i] = xs[i][gu * M * 4];
-      }
+    for (int f = 0; f < NF; ++f) *reinterpret_cast<i32x4*>(mine + f * 1024 + lane * 16) = next[f];
+    if (lane < 16 * MT) sx[lane] = nextXs;
+#pragma unroll
+    for (int z = 0; z < kLoadsW; ++z)
+      if (z * kWave + lane < 16 * CT) sw[z * kWave + lane] = nextWs[z];
+    load(g + kWaves);
+    wave_sync();
+    i32x4 a[MT];
+    int sa[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      a[i] = *reinterpret_cast<const i32x4*>(mine + i * 1024 + frag);
+      sa[i] = reinterpret_cast<const uint8_t*>(sx + 16 * i + lr)[lh];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int j = 0; j < CT; ++j) {
+      const i32x4 b = *reinterpret_cast<const i32x4*>(mine + (MT + j) * 1024 + frag);
+      const int sb = reinterpret_cast<const uint8_t*>(sw + 16 * j + lr)[lh];
 #pragma unroll
       for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < CT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              widen(a[u][i]), widen(b[u][j]), acc[i][j], kFp4, kFp4, 0, sa[u][i], 0, sb[u][j]);
-  };
-  int g = w;
-  for (; g + (kFewAhead - 1) * kFewWaves < G; g += kFewAhead * kFewWaves)
-    turns(g, std::integral_constant<int, kFewAhead>{});
-  for (; g < G; g += kFewWaves) turns(g, std::integral_constant<int, 1>{});
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            widen(a[i]), widen(b), acc[i][j], kFp4, kFp4, 0, sa[i], 0, sb);
+    }
+    wave_sync();
+  }
 
   // lane l, value r of block (i, j): token 16 i + 4 (l / 16) + r, column 16 j + l % 16
+  f32x4* const part = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
   for (int t = 0; t < kBlocks; t += kTurn) {
-    if (t > 0) __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kTurn; ++q) part[q][w][lane] = acc[(t + q) / CT][(t + q) % CT];
     __syncthreads();
-    for (int e = threadIdx.x; e < kTurn * 256; e += kFewWaves * kWave) {
+#pragma unroll
+    for (int q = 0; q < kTurn; ++q)
+      part[(q * kWaves + w) * kWave + lane] = acc[(t + q) / CT][(t + q) % CT];
+    __syncthreads();
+    for (int e = threadIdx.x; e < kTurn * 256; e += kWaves * kWave) {
       // element e: block q, value r of lane l; consecutive threads take consecutive columns
       const int q = e / 256, l = (e & 15) | ((e >> 2) & 48), r = (e >> 4) & 3;
       const int i = (t + q) / CT, j = (t + q) % CT;
       float y = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kFewWaves; ++k) y += part[q][k][l][r];
-      const int64_t row = 16 * i + 4 * (l >> 4) + r, col = n0 + 16 * j + (l & 15);
-      if (row < M && col < Ncols) project_store_one(A.out, project_column(A.out, (uint32_t)col),
-                                                     project_token(A.out, (uint32_t)row), y);
+      for (int k = 0; k < kWaves; ++k) y += part[(q * kWaves + k) * kWave + l][r];
+      const int tok = 16 * i + 4 * (l >> 4) + r, col = 16 * j + (l & 15);
+      if (tok < mrows && col < nrows)
+        project_store_one(A.out, project_column(A.out, (uint32_t)(n0 + col)),
+                          project_token(A.out, (uint32_t)(m0 + tok)), y);
     }
   }
 }
 
 template <int MT, int CT>
-void launch_few(const Mx4Args& A, hipStream_t stream) {
-  const int64_t blocks = (A.out.Ncols + 16 * CT - 1) / (16 * CT);
-  hipLaunchKernelGGL((project_mx4_few<MT, CT>), dim3((unsigned)blocks), dim3(kFewWaves * kWave), 0,
-                     stream, A);
+void launch_few(Mx4Args A, hipStream_t stream) {
+  A.nbm = (int)((A.out.M + 16 * MT - 1) / (16 * MT));
+  const int64_t cols = (A.out.Ncols + 16 * CT - 1) / (16 * CT);
+  hipLaunchKernelGGL((project_mx4_few<MT, CT>), dim3((unsigned)((cols + 7) / 8 * 8 * A.nbm)),
+                     dim3(few_waves<MT, CT>() * kWave), 0, stream, A);
+}
+
+template <int MT>
+void launch_few_columns(const Mx4Args& A, int ct, hipStream_t stream) {
+  if (ct == 1) return launch_few<MT, 1>(A, stream);
+  if (ct == 2) return launch_few<MT, 2>(A, stream);
+  if (ct == 3) return launch_few<MT, 3>(A, stream);
+  if (ct == 5) return launch_few<MT, 5>(A, stream);
+  return launch_few<MT, 9>(A, stream);
+}
+
+// Which kernel, and how many columns a few-token workgroup takes.
+//
+// Columns: the compute units work through their workgroups side by side, so
+// a call lasts as long as the unit with the most of them.  As measured (ns), a
+// workgroup costs 31 for each of its CT + MT fragments and turn of 128 columns
+// (a single token's fragment, the same bytes on every lane, next to nothing)
+// and 200 for each block it adds up; the CT of least cost over the rounds was
+// within 5% of the best of CT = 1..9 at 1, 16, 32 and 64 tokens x 16904 and
+// 33808 columns.  64 tokens at d_model 8192 x 16904 columns: 22 us with CT = 5
+// (one round), 38 with 4 (two), 62 with 1.
+//
+// Kernel: a round of tiles takes 13000 + 900 per turn, a few-token call 5000
+// beside its workgroups.  64 tokens at d_model 16384 x 33808 columns: 79 us
+// against 130 in tiles; 128: 147 against 131; 300 at 2048 x 4360: 12 against
+// 28; 1024: 39 against 28.  CT = 9 leaves a unit one workgroup of four
+// wavefronts, so it is for one block of tokens.
+int pick_few(const Mx4Args& A) {
+  const int64_t M = A.out.M, Ncols = A.out.Ncols, G = A.K / 128, cus = compute_units();
+  const int MT = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  const int64_t tokens = (M + 16 * MT - 1) / (16 * MT);
+  int64_t best = 0;
+  int pick = 0;
+  for (int ct : {1, 2, 3, 5, 9}) {
+    if (ct == 9 && tokens > 1) break;
+    const int64_t wgs = (Ncols + 16 * ct - 1) / (16 * ct) * tokens;
+    if (wgs > kMaxProjTiles - 8 * tokens) continue;  // work-items of a launch: 32 bits
+    const int64_t each = (ct + (M == 1 ? 0 : MT)) * G * 31 + 200 * ct * MT;
+    const int64_t cost = (wgs + cus - 1) / cus * each;
+    if (!pick || cost < best) best = cost, pick = ct;
+  }
+  const int64_t tiles = project_blocks(M, Ncols), rounds = (tiles + cus - 1) / cus;
+  return best + 5000 < rounds * (13000 + 900 * G) ? pick : 0;
 }
 
 }  // namespace
@@ -374,14 +464,13 @@ hipError_t launch_project_mx4(const uint8_t* Xq, const uint8_t* Xs, const uint8_
   A.K = d_model;
   A.out = project_out(B, T, H, n, d_v, s1, s2, q1, q2, v, alpha, beta);
   if (A.out.M == 0) return hipSuccess;
-  if (A.out.M <= kProjFewTokens) {
-    const int mt = (int)((A.out.M + 15) / 16);
-    if (mt == 1)
-      launch_few<1, 1>(A, stream);
-    else if (mt == 2)
-      launch_few<2, 2>(A, stream);
+  if (const int ct = pick_few(A)) {
+    if (A.out.M <= 16)
+      launch_few_columns<1>(A, ct, stream);
+    else if (A.out.M <= 32)
+      launch_few_columns<2>(A, ct, stream);
     else
-      launch_few<4, 4>(A, stream);
+      launch_few_columns<4>(A, ct, stream);
     return hipGetLastError();
   }
   A.nbm = (int)((A.out.M + kXBM - 1) / kXBM);

@@ -734,6 +734,8 @@ hipError_t launch(void* M, ScanArgs A, hipStream_t stream) {
   return hipGetLastError();
 }
 
+}  // namespace
+
 // Compute units of the current device (cached per device).
 int compute_units() {
   static int cached[64] = {0};
@@ -747,8 +749,6 @@ int compute_units() {
   }
   return cached[dev];
 }
-
-}  // namespace
 
 hipError_t launch_scan(void* M, int dtype, int B, int H, int64_t N, int d_v, int64_t T, int W,
                        int R, const int32_t* widx, const float* wk, const int32_t* ridx,

@@ -177,3 +177,11 @@ def test_tape8_binding():
     bad = dict(dv=step["v"], dwk=step["wk"], drw=step["wk"], dalpha=step["alpha"], dbeta=step["beta"])
     _expect("drw must have shape", sdm.scan_backward8, **step, tape=(codes, scales), dout=dout, G=M,
             out=bad)
+
+
+def test_projection_launches_stay_below_2_to_the_32_work_items():
+    """Tiles are workgroups of 512 threads, so 2^23 - 1 of them at most."""
+    L = sdm.lib()
+    for call, ptrs in ((L.sdm_project, 2), (L.sdm_project_mx4, 4)):
+        a = [FAKE] * ptrs + [1 << 15, 1 << 16, 256, 1, 64, 16] + [FAKE] * 7 + [None]
+        assert call(*a) == 2 and "2^23 - 1" in _err()  # 2^23 row tiles x 2
