@@ -360,11 +360,17 @@ int sdm_scan_train8(void* M, int B, int H, int64_t N, int d_v, int64_t T, int W,
 int sdm_tape8_read(const int8_t* tape, const uint8_t* tape_scale, int B, int H, int d_v,
                    int64_t T, int S, int dtype, void* rows, void* stream);
 
+/* Bytes of workspace sdm_scan_backward8 needs for these sizes (0 if they are
+ * not supported): about 1.3 KB per memory and step, and 4*(W + 1) for each 16
+ * columns. */
+size_t sdm_scan_backward8_workspace_size(int B, int H, int d_v, int64_t T, int W, int R);
+
 /* sdm_scan_backward from an 8-bit tape: the gradients of the step at the
- * tape's rounded rows, every result that sdm_scan_backward gives for the fp32
- * rows of sdm_tape8_read (bit for bit while no product under- or overflows).
- * Other arguments, modes, workspace and limits as there, the tape's size
- * limit as for sdm_scan_train8. */
+ * tape's rounded rows.  G as sdm_scan_backward leaves it, bit for bit (it does
+ * not depend on the rows); the per-step sums are sdm_scan_backward's for the
+ * fp32 rows of sdm_tape8_read up to the order of their fp32 additions, which
+ * is fixed.  Other arguments, modes and limits as there, the tape's size limit
+ * as for sdm_scan_train8, and B*H*(T + 8) <= 2^26 - 4. */
 int sdm_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
                        const int32_t* widx, const float* wk, const int32_t* ridx,
                        const float* rw, const float* v, const float* alpha, const float* beta,

@@ -49,7 +49,7 @@ EXPORTS = ("sdm_project", "sdm_mx4_quantize", "sdm_mx4_dequantize", "sdm_project
            "sdm_scan_backward_workspace_size", "sdm_scan_backward", "sdm_scan_backward_noalloc",
            "sdm_select_backward", "sdm_scan_plan_workspace_size", "sdm_scan_plan",
            "sdm_scan_planned", "sdm_state_init_backward", "sdm_touch_prepare", "sdm_scan_train8", "sdm_tape8_read",
-           "sdm_scan_backward8", "sdm_status_string", "sdm_last_error",
+           "sdm_scan_backward8", "sdm_scan_backward8_workspace_size", "sdm_status_string", "sdm_last_error",
            "sdm_abi_version")
 
 _lib = None
@@ -86,6 +86,8 @@ def lib():
         L.sdm_scan_backward_noalloc.argtypes = [i32, i32, i64, i32, i64, i32, i32] + [p] * 17
         L.sdm_scan_train8.argtypes = [p, i32, i32, i64, i32, i64, i32, i32] + [p] * 11
         L.sdm_tape8_read.argtypes = [p, p, i32, i32, i32, i64, i32, i32, p, p]
+        L.sdm_scan_backward8_workspace_size.argtypes = [i32, i32, i32, i64, i32, i32]
+        L.sdm_scan_backward8_workspace_size.restype = ctypes.c_size_t
         L.sdm_scan_backward8.argtypes = ([i32, i32, i64, i32, i64, i32, i32] + [p] * 18 +
                                          [ctypes.c_size_t, p])
         L.sdm_touch_prepare.argtypes = [i32, i32, i64, i64, i32, i32, p, p, p, p, p]
@@ -600,7 +602,7 @@ def scan_backward8(widx, wk, ridx, rw, v, alpha, beta, tape, dout, G, workspace=
     ins += [_arg(out[k], f32, shp, k) for k, shp in shapes.items()]
     af = None if first is None else _arg(first, torch.int64, (B, H, T, 2), "first")
     if workspace is None:
-        need = int(lib().sdm_scan_backward_workspace_size(B, H, d_v, T, W, R))
+        need = int(lib().sdm_scan_backward8_workspace_size(B, H, d_v, T, W, R))
         workspace = torch.empty((max(need, 16) + 3) // 4, dtype=f32, device=G.device)
     ptrs = _gpu(*ins, af, _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()

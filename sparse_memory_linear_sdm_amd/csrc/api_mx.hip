@@ -123,6 +123,12 @@ int sdm_tape8_read(const int8_t* tape, const uint8_t* tape_scale, int B, int H, 
                 sdm::launch_tape8_read(tape, tape_scale, dtype, B * H, d_v, T * S, rows, s), s);
 }
 
+size_t sdm_scan_backward8_workspace_size(int B, int H, int d_v, int64_t T, int W, int R) {
+  if (B < 1 || H < 1 || T < 0 || W < 1 || W > 64 || R < 1 || R > 64 || !dv_supported(d_v)) return 0;
+  if ((int64_t)B * H > sdm::kMaxMemories || T > sdm::kMaxWaveUnits) return 0;
+  return sdm::scan_backward8_workspace_bytes(B * H, d_v, T, W);
+}
+
 int sdm_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
                        const int32_t* widx, const float* wk, const int32_t* ridx,
                        const float* rw, const float* v, const float* alpha, const float* beta,
@@ -131,10 +137,14 @@ int sdm_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, int W, int R
                        const uint64_t* first, void* workspace, size_t workspace_bytes,
                        void* stream) {
   int rc;
-  size_t need = 0;
+  size_t need = 0;  // of the other reverse pass
   if ((rc = check_backward_args(B, H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha, beta, tape, 1,
                                 dout, G, dv, dwk, drw, dalpha, dbeta, first, &need)))
     return rc;
+  if ((int64_t)B * H * (T + sdm::kBackward8Pad) > sdm::kMaxWaveUnits)
+    return fail(SDM_ERR_UNSUPPORTED,
+                "B*H*(T + 8) must be at most 2^26 - 4 (one wavefront per memory and step)");
+  need = T > 0 ? sdm::scan_backward8_workspace_bytes(B * H, d_v, T, W) : 0;
   if (T > 0 && !tape_scale) return fail(SDM_ERR_INVALID, "tape_scale is NULL");
   if (T > 0 && !workspace) return fail(SDM_ERR_INVALID, "workspace is NULL");
   if (!aligned(workspace, 16)) return fail(SDM_ERR_INVALID, "workspace must be 16-byte aligned");
@@ -145,7 +155,7 @@ int sdm_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, int W, int R
   return finish("sdm_scan_backward8",
                 sdm::launch_scan_backward8(B, H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha,
                                            beta, tape, tape_scale, dout, G, dv, dwk, drw, dalpha,
-                                           dbeta, first, reinterpret_cast<float*>(workspace), s),
+                                           dbeta, first, workspace, s),
                 s);
 }
 

@@ -37,7 +37,6 @@
 // sequence selects.  Nothing here is a dense contraction: no MFMA.
 #include "device_common.h"
 #include "internal.h"
-#include "mx.h"
 #include "ranges.h"
 
 namespace sdm {
@@ -67,8 +66,6 @@ struct BwdArgs {
   float* ws;
   int ntiles;
   const uint64_t* first;  // optional: per step, the slots that are their row's last touch
-  const int8_t* tape8;    // 8-bit tape (tape is then unused): [n_mem, d_v/16, T, W + R, 16]
-  const uint8_t* tape_scale;  // codes and [n_mem, d_v/16, T, W + R] scale bytes
 };
 
 __device__ __forceinline__ uint32_t hash_slot(uint32_t row) {
@@ -108,29 +105,7 @@ __device__ __forceinline__ float col_sum(float x) {
   return x;
 }
 
-// One group of four wave instructions' rows of the 8-bit tape, as loaded: lane
-// q of a quad holds the record (16 code bytes, scale byte) of the group's
-// row slot q * RPI + lr in the quad's 16-column block.
-struct Records8 {
-  u32x4 codes;
-  uint32_t scale;
-};
-
-// Word i, after the exchange within the quad, is this lane's four columns of
-// row slot i * RPI + lr; its scale comes from lane i of the quad.
-__device__ __forceinline__ void spread8(const Records8& r, uint32_t (&w)[4], float (&s)[4]) {
-  w[0] = r.codes.x;
-  w[1] = r.codes.y;
-  w[2] = r.codes.z;
-  w[3] = r.codes.w;
-  quad_transpose(w);
-  s[0] = __uint_as_float(dpp_mov<0x00>(r.scale) << 23);
-  s[1] = __uint_as_float(dpp_mov<0x55>(r.scale) << 23);
-  s[2] = __uint_as_float(dpp_mov<0xAA>(r.scale) << 23);
-  s[3] = __uint_as_float(dpp_mov<0xFF>(r.scale) << 23);
-}
-
-template <int COLS, bool TAPE8>
+template <int COLS>
 __global__ __launch_bounds__(kWave) void scan_bwd_kernel(BwdArgs A) {
   constexpr int LPR = COLS / 4;      // lanes per tile row (16 bytes each)
   constexpr int RPI = kWave / LPR;   // rows per wave instruction
@@ -158,20 +133,9 @@ __global__ __launch_bounds__(kWave) void scan_bwd_kernel(BwdArgs A) {
       A.G + (int64_t)mem * mem_elems + tile * COLS, 0,
       (int)ranges::table_range(N, (int64_t)d_v * 4, tile, COLS * 4), kBufWord3);
   const int64_t tape_rows = T * (W + R);  // per step: W pre-write rows, R read rows
-  const int64_t recs = (int64_t)(d_v / 16) * tape_rows;  // 8-bit tape: row records of one memory
-  const __amdgpu_buffer_rsrc_t tres =
-      TAPE8 ? __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(A.tape8) + (int64_t)mem * recs * 16,
-                                                0, (int)ranges::table_range(recs, 16, 0, 16), kBufWord3)
-            : __builtin_amdgcn_make_buffer_rsrc(
-                  const_cast<float*>(A.tape) + (int64_t)mem * tape_rows * d_v + tile * COLS, 0,
-                  (int)ranges::table_range(tape_rows, (int64_t)d_v * 4, tile, COLS * 4), kBufWord3);
-  const __amdgpu_buffer_rsrc_t sres = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(A.tape_scale) + (int64_t)mem * (TAPE8 ? recs : 0), 0, TAPE8 ? (int)recs : 0,
-      kBufWord3);
-  // TAPE8: this lane's first record in the tile's blocks (see Records8)
-  const int q = lane & 3;
-  const uint32_t rec0 =
-      (uint32_t)(tile * (COLS / 16) + lc / 4) * (uint32_t)tape_rows + (uint32_t)(q * RPI + lr);
+  const __amdgpu_buffer_rsrc_t tres = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(A.tape) + (int64_t)mem * tape_rows * d_v + tile * COLS, 0,
+      (int)ranges::table_range(tape_rows, (int64_t)d_v * 4, tile, COLS * 4), kBufWord3);
   const uint32_t row_bytes = (uint32_t)d_v * 4u;
   const uint32_t lane_off = (uint32_t)lc * 16u;
 
@@ -244,36 +208,14 @@ __global__ __launch_bounds__(kWave) void scan_bwd_kernel(BwdArgs A) {
 
     // ---- gathers (all issued before any is used)
     u32x4 Mg[NI], Gg[NI], Gf[NI], P[NI];
-    Records8 M8[NI / 4], P8[NI / 4];
-    if constexpr (TAPE8) {
 #pragma unroll
-      for (int g = 0; g < NI / 4; ++g) {
-        uint32_t ws = kOffNone, rs = kOffNone;  // slot (4 g + q) * RPI + lr: out of range if unused
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ws = q == i ? wo[4 * g + i] : ws;
-          rs = q == i ? ro[4 * g + i] : rs;
-        }
-        const bool wv = ws < kOffNone, rv = rs < kOffNone;
-        const uint32_t aw = rec0 + (uint32_t)t * (uint32_t)(W + R) + (uint32_t)(4 * g * RPI);
-        const uint32_t ar = aw + (uint32_t)W;
-        M8[g].codes = __builtin_amdgcn_raw_buffer_load_b128(tres, rv ? ar * 16u : kOffNone, 0, 0);
-        M8[g].scale = __builtin_amdgcn_raw_buffer_load_b8(sres, rv ? ar : kOffNone, 0, 0);
-        P8[g].codes = __builtin_amdgcn_raw_buffer_load_b128(tres, wv ? aw * 16u : kOffNone, 0, 0);
-        P8[g].scale = __builtin_amdgcn_raw_buffer_load_b8(sres, wv ? aw : kOffNone, 0, 0);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < NI; ++k) Mg[k] = __builtin_amdgcn_raw_buffer_load_b128(tres, tr[k], 0, 0);
-    }
+    for (int k = 0; k < NI; ++k) Mg[k] = __builtin_amdgcn_raw_buffer_load_b128(tres, tr[k], 0, 0);
 #pragma unroll
     for (int k = 0; k < NI; ++k) Gg[k] = __builtin_amdgcn_raw_buffer_load_b128(gres, rlo[k], 0, 0);
 #pragma unroll
     for (int k = 0; k < NI; ++k) Gf[k] = __builtin_amdgcn_raw_buffer_load_b128(gres, wlo[k], 0, 0);
-    if constexpr (!TAPE8) {
 #pragma unroll
-      for (int k = 0; k < NI; ++k) P[k] = __builtin_amdgcn_raw_buffer_load_b128(tres, to[k], 0, 0);
-    }
+    for (int k = 0; k < NI; ++k) P[k] = __builtin_amdgcn_raw_buffer_load_b128(tres, to[k], 0, 0);
 
     // ---- step t-1's metadata, in flight with the gathers
     const int64_t tn = t > 0 ? t - 1 : 0;
@@ -319,32 +261,12 @@ __global__ __launch_bounds__(kWave) void scan_bwd_kernel(BwdArgs A) {
 #pragma unroll
     for (int k = 0; k < NI; ++k) mw[k] = match[k] >= 0 ? rws[match[k]] : 0.0f;
 
-    // ---- read part: dr_j and G[g_j] += r_j * do.  The 8-bit tape's rows stay
-    // whole numbers c and their block's scale s, a power of two, multiplies
-    // the sums: s * (do . c) rounds as do . (s c) does.
-    float m8[NI / 4][4], p8[NI / 4][4];  // TAPE8: scales of the read and the pre-write rows
-    if constexpr (TAPE8) {
-#pragma unroll
-      for (int g = 0; g < NI / 4; ++g) {
-        uint32_t wm[4], wp[4];
-        spread8(M8[g], wm, m8[g]);
-        spread8(P8[g], wp, p8[g]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x[4];
-          int8_unpack4(wm[i], x);
-          Mg[4 * g + i] = as_u4(f32x4{x[0], x[1], x[2], x[3]});
-          int8_unpack4(wp[i], x);
-          P[4 * g + i] = as_u4(f32x4{x[0], x[1], x[2], x[3]});
-        }
-      }
-    }
+    // ---- read part: dr_j and G[g_j] += r_j * do
     float drp[NI];
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
       const f32x4 m = as_f4(Mg[k]);
       drp[k] = dd.x * m.x + dd.y * m.y + dd.z * m.z + dd.w * m.w;
-      if constexpr (TAPE8) drp[k] *= m8[k / 4][k % 4];
       f32x4 g = as_f4(Gg[k]);
       g.x = fmaf(rwk[k], dd.x, g.x);
       g.y = fmaf(rwk[k], dd.y, g.y);
@@ -369,15 +291,10 @@ __global__ __launch_bounds__(kWave) void scan_bwd_kernel(BwdArgs A) {
       dva.y = fmaf(bk, g.y, dva.y);
       dva.z = fmaf(bk, g.z, dva.z);
       dva.w = fmaf(bk, g.w, dva.w);
-      float gp = g.x * p.x + g.y * p.y + g.z * p.z + g.w * p.w;
-      float ap = a;  // times the row's scale
-      if constexpr (TAPE8) {
-        gp *= p8[k / 4][k % 4];
-        ap *= p8[k / 4][k % 4];
-      }
+      const float gp = g.x * p.x + g.y * p.y + g.z * p.z + g.w * p.w;
       dap = fmaf(1.0f - bk, gp, dap);
-      dbk[k] = g.x * (vv.x - ap * p.x) + g.y * (vv.y - ap * p.y) + g.z * (vv.z - ap * p.z) +
-               g.w * (vv.w - ap * p.w);
+      dbk[k] = g.x * (vv.x - a * p.x) + g.y * (vv.y - a * p.y) + g.z * (vv.z - a * p.z) +
+               g.w * (vv.w - a * p.w);
       const float c = a * (1.0f - bk);
       Gf[k] = as_u4(f32x4{c * g.x, c * g.y, c * g.z, c * g.w});
     }
@@ -669,38 +586,6 @@ size_t scan_backward_workspace_bytes(int n_mem, int d_v, int64_t T, int W, int R
   return (size_t)n_mem * (size_t)T * (size_t)(d_v / cols) * (size_t)(W + R + 1) * sizeof(float);
 }
 
-namespace {
-
-// The reverse scan and its finishing pass.
-template <bool TAPE8>
-hipError_t run_backward(BwdArgs A, float* dwk, float* drw, float* dalpha, float* dbeta,
-                        hipStream_t stream) {
-  // Tile width (measured at mid): the dense mode gathers every G row at
-  // random, so whole 128-byte lines (32 columns, one wave per compute unit)
-  // are fastest (14.1 ms against 17.3 with 16 columns).  In the sparse mode
-  // most G gathers are dropped and the tape rows are read in order, so twice
-  // the wavefronts with half the arithmetic each win (16 columns: 11.5 ms
-  // against 13.4).
-  const int cols = A.first ? (A.d_v < 16 ? A.d_v : 16) : (A.d_v < 32 ? A.d_v : 32);
-  A.ntiles = A.d_v / cols;
-  const int groups = (A.n_mem + 7) / 8;
-  const int64_t blocks = (int64_t)groups * A.ntiles * 8;
-  if (cols == 32)
-    hipLaunchKernelGGL((scan_bwd_kernel<32, TAPE8>), dim3((unsigned)blocks), dim3(kWave), 0,
-                       stream, A);
-  else
-    hipLaunchKernelGGL((scan_bwd_kernel<16, TAPE8>), dim3((unsigned)blocks), dim3(kWave), 0,
-                       stream, A);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int64_t units = (int64_t)A.n_mem * A.T;
-  hipLaunchKernelGGL(scan_bwd_finish, dim3((unsigned)((units + 3) / 4)), dim3(256), 0, stream, A,
-                     dwk, drw, dalpha, dbeta);
-  return hipGetLastError();
-}
-
-}  // namespace
-
 hipError_t launch_scan_backward(int B, int H, int64_t N, int d_v, int64_t T, int W,
                                 int R, const int32_t* widx, const float* wk,
                                 const int32_t* ridx, const float* rw, const float* v,
@@ -709,23 +594,27 @@ hipError_t launch_scan_backward(int B, int H, int64_t N, int d_v, int64_t T, int
                                 float* dalpha, float* dbeta, const uint64_t* first, float* ws,
                                 hipStream_t stream) {
   if (T == 0) return hipSuccess;
-  return run_backward<false>(BwdArgs{B * H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha, beta,
-                                     dout, tape, G, dv, ws, 0, first, nullptr, nullptr},
-                             dwk, drw, dalpha, dbeta, stream);
-}
-
-hipError_t launch_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
-                                 const int32_t* widx, const float* wk, const int32_t* ridx,
-                                 const float* rw, const float* v, const float* alpha,
-                                 const float* beta, const int8_t* tape,
-                                 const uint8_t* tape_scale, const float* dout, float* G,
-                                 float* dv, float* dwk, float* drw, float* dalpha, float* dbeta,
-                                 const uint64_t* first, float* ws, hipStream_t stream) {
-  if (T == 0) return hipSuccess;
-  if (!ranges::tape8_ok(d_v, T, W, R)) return hipErrorInvalidValue;  // checked by the C-ABI layer
-  return run_backward<true>(BwdArgs{B * H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha, beta,
-                                    dout, nullptr, G, dv, ws, 0, first, tape, tape_scale},
-                            dwk, drw, dalpha, dbeta, stream);
+  // Tile width (measured at mid): the dense mode gathers every G row at
+  // random, so whole 128-byte lines (32 columns, one wave per compute unit)
+  // are fastest (14.1 ms against 17.3 with 16 columns).  In the sparse mode
+  // most G gathers are dropped and the tape rows are read in order, so twice
+  // the wavefronts with half the arithmetic each win (16 columns: 11.5 ms
+  // against 13.4).
+  const int cols = first ? (d_v < 16 ? d_v : 16) : (d_v < 32 ? d_v : 32);
+  BwdArgs A{B * H, N, d_v, T, W, R, widx, wk, ridx, rw, v, alpha, beta, dout, tape, G, dv, ws,
+            d_v / cols, first};
+  const int groups = (A.n_mem + 7) / 8;
+  const int64_t blocks = (int64_t)groups * A.ntiles * 8;
+  if (cols == 32)
+    hipLaunchKernelGGL((scan_bwd_kernel<32>), dim3((unsigned)blocks), dim3(kWave), 0, stream, A);
+  else
+    hipLaunchKernelGGL((scan_bwd_kernel<16>), dim3((unsigned)blocks), dim3(kWave), 0, stream, A);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t units = (int64_t)A.n_mem * T;
+  hipLaunchKernelGGL(scan_bwd_finish, dim3((unsigned)((units + 3) / 4)), dim3(256), 0, stream, A,
+                     dwk, drw, dalpha, dbeta);
+  return hipGetLastError();
 }
 
 hipError_t launch_select_backward(const int32_t* idx, const float* w, const float* dw,

@@ -105,7 +105,10 @@ hipError_t launch_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, in
                                  const float* beta, const int8_t* tape,
                                  const uint8_t* tape_scale, const float* dout, float* G,
                                  float* dv, float* dwk, float* drw, float* dalpha, float* dbeta,
-                                 const uint64_t* first, float* ws, hipStream_t stream);
+                                 const uint64_t* first, void* ws, hipStream_t stream);
+size_t scan_backward8_workspace_bytes(int n_mem, int d_v, int64_t T, int W);
+// Steps of a memory are padded to at most this many more (one wavefront each).
+constexpr int64_t kBackward8Pad = 8;
 
 // The library's per-GPU scratch buffer (scratch.hip), for callers that cannot
 // allocate: kStaticScratchBytes of device memory, aligned to 256 bytes, held

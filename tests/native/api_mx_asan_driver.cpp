@@ -132,8 +132,11 @@ hipError_t launch_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, in
                                  const int32_t*, const float*, const int32_t*, const float*,
                                  const float*, const float*, const float*, const int8_t*,
                                  const uint8_t*, const float*, float*, float*, float*, float*,
-                                 float*, float*, const uint64_t*, float*, hipStream_t) {
+                                 float*, float*, const uint64_t*, void*, hipStream_t) {
   return record(B, H, N, d_v, T, W, R);
+}
+size_t scan_backward8_workspace_bytes(int n_mem, int d_v, int64_t T, int W) {
+  return (size_t)n_mem * (size_t)T * (size_t)(1296 + d_v / 16 * (W + 1) * 4);
 }
 }  // namespace sdm
 
@@ -164,7 +167,7 @@ int main() {
   CHECK(g_last[2] == 4096 && g_last[4] == 100 && g_last[6] == 5);
   CHECK(read8(2, 3, 256, 100, 128) == SDM_OK && g_launches == ++n);
   CHECK(g_last[1] == 6 && g_last[3] == 12800);
-  const size_t ws = sdm_scan_backward_workspace_size(2, 3, 128, 100, 64, 5);
+  const size_t ws = sdm_scan_backward8_workspace_size(2, 3, 128, 100, 64, 5);
   CHECK(backward8(2, 3, 4096, 128, 100, 64, 5, ws) == SDM_OK && g_launches == ++n);
   CHECK(backward8(2, 3, 4096, 128, 100, 64, 5, ws - 1) == SDM_ERR_INVALID);
   // the largest tape below 2 GiB, and the first one at it

@@ -132,7 +132,13 @@ def test_tape8_read_entry_point():
 
 def test_backward8_entry_point():
     L = sdm.lib()
-    ws = L.sdm_scan_backward_workspace_size(1, 1, 16, 8, 8, 8)
+    size = L.sdm_scan_backward8_workspace_size
+    # 16 padded steps' records of 5 x 64 + 4 words, and 8 steps' sums of W + 1
+    ws = size(1, 1, 16, 8, 8, 8)
+    assert ws == 16 * 1296 + 8 * 9 * 4 and size(2, 3, 128, 7, 64, 1) == 6 * (8 * 1296 + 7 * 8 * 65 * 4)
+    for bad in ((0, 1, 16, 8, 8, 8), (1, 1, 24, 8, 8, 8), (1, 1, 16, -1, 8, 8), (1, 1, 16, 8, 65, 8),
+                (1, 1, 16, 8, 8, 0), (1 << 11, 1 << 10, 16, 8, 8, 8), (1, 1, 16, 1 << 40, 8, 8)):
+        assert size(*bad) == 0, bad
     # B, H, N, d_v, T, W, R, 7 inputs, tape, tape_scale, dout, G, dv, dwk, drw, dalpha, dbeta,
     # first, workspace, bytes, stream
     ok = [1, 1, 4096, 16, 8, 8, 8] + [FAKE] * 18 + [ws, None]
@@ -144,6 +150,9 @@ def test_backward8_entry_point():
     a = list(ok)
     a[3], a[4], a[5], a[6] = 128, 1 << 17, 64, 64
     assert L.sdm_scan_backward8(*a) == 2 and "2 GiB" in _err()
+    a = list(ok)
+    a[0], a[1], a[4], a[25] = 1 << 10, 1 << 10, 63, 1 << 50  # padded: 2^20 * 64 wavefronts
+    assert L.sdm_scan_backward8(*a) == 2 and "T + 8" in _err()
     args = [1, 1, 4096, 16, 0, 8, 8] + [None] * 10 + [FAKE] + [None] * 7 + [0, None]
     assert L.sdm_scan_backward8(*args) == 0
 
