@@ -38,8 +38,10 @@ constexpr uint32_t kOffNone = ranges::kOffNone;
 constexpr int kChunk = 8;  // records per LDS chunk
 constexpr int kRing = 3;
 
-// A step's record.  Row entries are transposed for the tile width in use:
-// entry lr * NI + k is row slot k * RPI + lr.  Offsets are multiples of 64
+// A step's record.  Row entries are transposed for the tile width in use (COLS
+// columns, RPI = 256 / COLS rows per wave instruction, NI = COLS / 4
+// instructions for 64): entry lr * NI + k is row slot k * RPI + lr, so a lane
+// reads its rows contiguously.  Offsets are multiples of 64
 // (whole rows); bit 0 marks a row whose gradient is still zero (sparse mode:
 // its last touch in time), which is stored but not gathered.
 struct Record {
@@ -84,15 +86,26 @@ struct Bwd8Args {
 
 // ---------------------------------------------------------------- prepare
 
+// A set of rows as bits: three bits of one of kSetWords words per row (word
+// and bits from two multiplicative hashes).  Of 128 rows in the set, an absent
+// row is found about once in 10^4.
+constexpr int kSetWords = 512;
+__device__ __forceinline__ uint32_t set_word(uint32_t row) { return (row * 2654435761u) >> 23; }
+__device__ __forceinline__ uint32_t set_bits(uint32_t row) {
+  const uint32_t h = row * 0x85EBCA77u;
+  return (1u << (h >> 27)) | (1u << ((h >> 22) & 31u)) | (1u << ((h >> 17) & 31u));
+}
+
 __global__ __launch_bounds__(256) void prepare_kernel(Bwd8Args A) {
+  __shared__ uint32_t sets[4][2][kSetWords];
   const int64_t Tp = padded_steps(A.T);
-  const int64_t unit = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
   if (unit >= (int64_t)A.n_mem * Tp) return;  // whole wavefront leaves together
   const int64_t mem = unit / Tp, u = unit - mem * Tp, t = A.T - 1 - u;
   const int lane = lane_id(), W = A.W, R = A.R;
   Record& out = A.rec[unit];
-  const int lpr = A.cols / 4, rpi = kWave / lpr, ni = 64 / rpi;
-  const int at = (lane % rpi) * ni + lane / rpi;  // this lane's slot in the record
+  const int rpi = 256 / A.cols, at = (lane % rpi) * (A.cols / 4) + lane / rpi;  // slot in the record
   if (t < 0) {
     out.wofs[at] = kOffNone;
     out.rofs[at] = kOffNone;
@@ -107,32 +120,49 @@ __global__ __launch_bounds__(256) void prepare_kernel(Bwd8Args A) {
     return r < N ? r : ~0u;
   };
   const uint32_t w = row(A.widx, W, step), r = row(A.ridx, R, step);
+  uint32_t w1 = ~0u, r1 = ~0u;  // step t + 1's
+  if (u > 0) {
+    w1 = row(A.widx, W, step + 1);
+    r1 = row(A.ridx, R, step + 1);
+  }
   const float wk = lane < W ? A.wk[step * W + lane] : 0.0f;
   const float rw = lane < R ? A.rw[step * R + lane] : 0.0f;
   const uint64_t fw = A.first ? A.first[step * 2] : 0ull, fr = A.first ? A.first[step * 2 + 1] : 0ull;
 
-  // the read weight that falls on a write row
+  // Which rows to look at exactly: write rows in the set of this step's read
+  // rows, and any row in the set of the rows of step t + 1.
+  uint32_t (&reads)[kSetWords] = sets[wave][0], (&later)[kSetWords] = sets[wave][1];
+#pragma unroll
+  for (int i = 0; i < 2 * kSetWords / 4 / kWave; ++i)
+    reinterpret_cast<uint4*>(reads)[i * kWave + lane] = make_uint4(0, 0, 0, 0);  // both
+  wave_sync();
+  if (r != ~0u) atomicOr(&reads[set_word(r)], set_bits(r));
+  if (w1 != ~0u) atomicOr(&later[set_word(w1)], set_bits(w1));
+  if (r1 != ~0u) atomicOr(&later[set_word(r1)], set_bits(r1));
+  wave_sync();
+  const uint32_t bw = set_bits(w), br = set_bits(r);
+  uint64_t match = __ballot(w != ~0u && (reads[set_word(w)] & bw) == bw);
+  const uint64_t aw = __ballot(w != ~0u && (later[set_word(w)] & bw) == bw);
+  const uint64_t ar = __ballot(r != ~0u && (later[set_word(r)] & br) == br);
+  // the read weight that falls on a write row (read rows are distinct)
   float mw = 0.0f;
-  for (int l = 0; l < R; ++l) {
-    const uint32_t s = (uint32_t)__builtin_amdgcn_readlane((int)r, l);
-    const float x = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(rw), l));
-    if (w == s) mw = x;
+  for (; match; match &= match - 1) {
+    const int l = __builtin_ctzll(match);
+    const uint64_t hit = __ballot(r == (uint32_t)__builtin_amdgcn_readlane((int)w, l));
+    const float x = __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
+        (int)__float_as_uint(rw), hit ? __builtin_ctzll(hit) : 0));
+    if (lane == l && hit) mw = x;
   }
-  if (w == ~0u) mw = 0.0f;
   // rows shared with step t + 1
-  bool again = false;
-  if (u > 0) {
-    const uint32_t w1 = row(A.widx, W, step + 1), r1 = row(A.ridx, R, step + 1);
-    for (int l = 0; l < W; ++l) {
-      const uint32_t s = (uint32_t)__builtin_amdgcn_readlane((int)w1, l);
-      again |= s != ~0u && (w == s || r == s);
-    }
-    for (int l = 0; l < R; ++l) {
-      const uint32_t s = (uint32_t)__builtin_amdgcn_readlane((int)r1, l);
-      again |= s != ~0u && (w == s || r == s);
-    }
+  bool shared = false;
+  for (uint64_t m = aw; m && !shared; m &= m - 1) {
+    const uint32_t s = (uint32_t)__builtin_amdgcn_readlane((int)w, __builtin_ctzll(m));
+    shared = __ballot(w1 == s || r1 == s) != 0ull;
   }
-  const bool shared = __ballot(again) != 0ull;
+  for (uint64_t m = ar; m && !shared; m &= m - 1) {
+    const uint32_t s = (uint32_t)__builtin_amdgcn_readlane((int)r, __builtin_ctzll(m));
+    shared = __ballot(w1 == s || r1 == s) != 0ull;
+  }
   out.wofs[at] = w == ~0u ? kOffNone : w * row_bytes | (uint32_t)((fw >> lane) & 1ull);
   out.rofs[at] = r == ~0u ? kOffNone : r * row_bytes | (uint32_t)((fr >> lane) & 1ull);
   out.mw[at] = mw;
@@ -145,37 +175,38 @@ __global__ __launch_bounds__(256) void prepare_kernel(Bwd8Args A) {
   }
 
   // dr: lane l's read row, block by block, against the step's output gradient
-  if (lane < R) {
-    const int nb = A.d_v / 16;
-    const int64_t S = A.T * (W + R);
-    float dr = 0.0f;
-    if (r != ~0u) {
-      for (int b = 0; b < nb; ++b) {
-        const int64_t rec = (mem * nb + b) * S + t * (W + R) + W + lane;
-        const u32x4 q = *reinterpret_cast<const u32x4*>(A.tape + rec * 16);
-        const uint32_t c[4] = {q.x, q.y, q.z, q.w};
-        const float* d = A.dout + step * A.d_v + b * 16;
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x[4];
-          int8_unpack4(c[i], x);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s = fmaf(d[4 * i + e], x[e], s);
-        }
-        dr = fmaf(s, __uint_as_float((uint32_t)A.tape_scale[rec] << 23), dr);
-      }
+  const int nb = A.d_v / 16;
+  const int64_t S = A.T * (W + R), rec = mem * nb * S + t * (W + R) + W + lane;
+  const float* d = A.dout + step * A.d_v;
+  float dr = 0.0f;
+#pragma unroll 2
+  for (int b = 0; b < nb; ++b) {
+    u32x4 q = {0u, 0u, 0u, 0u};
+    uint32_t scale = 0;
+    if (r != ~0u) {  // lanes past R among them: nothing is read there
+      q = *reinterpret_cast<const u32x4*>(A.tape + (rec + b * S) * 16);
+      scale = A.tape_scale[rec + b * S];
     }
-    A.drw[step * R + lane] = dr;
+    const uint32_t c[4] = {q.x, q.y, q.z, q.w};
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[4];
+      int8_unpack4(c[i], x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s = fmaf(d[b * 16 + 4 * i + e], x[e], s);
+    }
+    dr = fmaf(s, __uint_as_float(scale << 23), dr);
   }
+  if (lane < R) A.drw[step * R + lane] = dr;
 }
 
 // ---------------------------------------------------------------- scan
 
-template <int COLS>
+template <int COLS, int NC>
 struct Lds8 {
   Record rec[kRing][kChunk];
-  float vd[kRing][2][kChunk][COLS];  // the tile's columns of v and dout
+  float vd[kRing][2][kChunk][NC * COLS];  // the workgroup's columns of v and dout
 };
 
 __device__ __forceinline__ void chunk_barrier() {
@@ -202,27 +233,28 @@ __device__ __forceinline__ float fold(float a, float b) {
   return keep + __uint_as_float(lane_xor(__float_as_uint(send), 1 << BIT));
 }
 
-template <int COLS>
+template <int COLS, int NC>
 struct Scan8 {
-  static constexpr int LPR = COLS / 4, RPI = kWave / LPR, NI = 64 / RPI, NG = NI / 4;
+  static constexpr int LPR = COLS / 4, RPI = kWave / LPR, NI = 64 / RPI;
+  static_assert(NI == LPR, "lane lc of a row ends with the sums of instruction lc's row");
 
   // A step in flight: its offsets, its rows of G and its pre-write records.
   struct Step {
     uint32_t wo[NI], ro[NI];
     u32x4 Gw[NI], Gr[NI];
-    u32x4 codes[NG];
-    uint32_t scale[NG];
+    u32x4 codes;     // 16 columns: see issue(); 8: a word per instruction
+    uint8_t scale[COLS == 16 ? 1 : NI];  // as loaded: widened at its use, so that nothing waits before
   };
 
   const Bwd8Args& A;
-  Lds8<COLS>& sh;
+  Lds8<COLS, NC>& sh;
   __amdgpu_buffer_rsrc_t gres, tres, sres;
   uint32_t lane_off, rec0, step_rows;
-  int lr, lc;
-  int64_t T;
+  uint32_t word;  // 8 columns: byte offset of the lane's four codes in a record
+  int lr, lc, col0, T;
 
-  __device__ __forceinline__ const Record& record(int64_t u) const {
-    return sh.rec[(u / kChunk) % kRing][u % kChunk];
+  __device__ __forceinline__ const Record& record(int u) const {
+    return sh.rec[(uint32_t)u / kChunk % kRing][u % kChunk];
   }
 
   __device__ __forceinline__ void gather(Step& s) const {
@@ -236,7 +268,7 @@ struct Scan8 {
           gres, (s.wo[k] & 1u) ? kOffNone : s.wo[k] + lane_off, 0, 0);
   }
 
-  __device__ __forceinline__ void issue(Step& s, int64_t u) const {
+  __device__ __forceinline__ void issue(Step& s, int u) const {
     const Record& r = record(u);
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
@@ -244,20 +276,27 @@ struct Scan8 {
       s.ro[k] = r.rofs[lr * NI + k];
     }
     gather(s);
-    // lane q of a quad: the record of slot (4 g + q) * RPI + lr in the quad's block
-    const int q = lane_id() & 3;
-    const uint32_t row0 = rec0 + (uint32_t)(T - 1 - u) * step_rows;
+    const uint32_t rec = rec0 + (uint32_t)(T - 1 - u) * step_rows;
+    if constexpr (COLS == 16) {
+      // the whole tape record (16 code bytes, a scale) of slot lc * RPI + lr:
+      // one load of each for 64 rows; the quads exchange the codes' words later
+      const bool none = r.wofs[lr * NI + lc] >= kOffNone;
+      const uint32_t at = rec + (uint32_t)(lc * RPI + lr);
+      s.codes = __builtin_amdgcn_raw_buffer_load_b128(tres, none ? kOffNone : at * 16u, 0, 0);
+      s.scale[0] = __builtin_amdgcn_raw_buffer_load_b8(sres, none ? kOffNone : at, 0, 0);
+    } else {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const bool none = r.wofs[lr * NI + 4 * g + q] >= kOffNone;
-      const uint32_t rec = row0 + (uint32_t)(4 * g * RPI);
-      s.codes[g] = __builtin_amdgcn_raw_buffer_load_b128(tres, none ? kOffNone : rec * 16u, 0, 0);
-      s.scale[g] = __builtin_amdgcn_raw_buffer_load_b8(sres, none ? kOffNone : rec, 0, 0);
+      for (int k = 0; k < NI; ++k) {
+        const bool none = s.wo[k] >= kOffNone;
+        const uint32_t at = rec + (uint32_t)(k * RPI + lr);
+        s.codes[k] = __builtin_amdgcn_raw_buffer_load_b32(tres, none ? kOffNone : at * 16u + word, 0, 0);
+        s.scale[k] = __builtin_amdgcn_raw_buffer_load_b8(sres, none ? kOffNone : at, 0, 0);
+      }
     }
   }
 
   // Step u, with step u + 1's loads going out first.
-  __device__ __forceinline__ void step(Step& s, Step& next, int64_t u, float* dv, float* sums) const {
+  __device__ __forceinline__ void step(Step& s, Step& next, int u, float* dv, float* sums) const {
     issue(next, u + 1);
     const Record& r = record(u);
     float rw[NI], mw[NI], wk[NI];
@@ -269,9 +308,9 @@ struct Scan8 {
     }
     const float a = r.alpha, b = r.beta;
     const uint32_t again = record(u + 1).again;
-    const int ring = (int)((u / kChunk) % kRing), at = (int)(u % kChunk);
-    const f32x4 vv = *reinterpret_cast<const f32x4*>(&sh.vd[ring][0][at][lc * 4]);
-    const f32x4 dd = *reinterpret_cast<const f32x4*>(&sh.vd[ring][1][at][lc * 4]);
+    const int ring = (uint32_t)u / kChunk % kRing, at = u % kChunk;
+    const f32x4 vv = *reinterpret_cast<const f32x4*>(&sh.vd[ring][0][at][col0 + lc * 4]);
+    const f32x4 dd = *reinterpret_cast<const f32x4*>(&sh.vd[ring][1][at][col0 + lc * 4]);
 
     // ---- read rows: G += r do
 #pragma unroll
@@ -286,39 +325,41 @@ struct Scan8 {
     // ---- write rows
     f32x4 dva = {0.f, 0.f, 0.f, 0.f};
     float da = 0.0f, dbk[NI];
-#pragma unroll
-    for (int g4 = 0; g4 < NG; ++g4) {
-      // word i, after the exchange within the quad, is this lane's four
-      // columns of slot (4 g4 + i) * RPI + lr; its scale is lane i's
-      uint32_t w[4] = {s.codes[g4].x, s.codes[g4].y, s.codes[g4].z, s.codes[g4].w};
+    // word k: this lane's four codes of slot k * RPI + lr, sc[k] their scale
+    uint32_t w[4] = {s.codes.x, s.codes.y, s.codes.z, s.codes.w};
+    float sc[NI];
+    if constexpr (COLS == 16) {
       quad_transpose(w);
-      const float sc[4] = {__uint_as_float(dpp_mov<0x00>(s.scale[g4]) << 23),
-                           __uint_as_float(dpp_mov<0x55>(s.scale[g4]) << 23),
-                           __uint_as_float(dpp_mov<0xAA>(s.scale[g4]) << 23),
-                           __uint_as_float(dpp_mov<0xFF>(s.scale[g4]) << 23)};
+      const uint32_t scale = (uint32_t)s.scale[0] << 23;
+      sc[0] = __uint_as_float(dpp_mov<0x00>(scale));
+      sc[1] = __uint_as_float(dpp_mov<0x55>(scale));
+      sc[2] = __uint_as_float(dpp_mov<0xAA>(scale));
+      sc[3] = __uint_as_float(dpp_mov<0xFF>(scale));
+    } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = 4 * g4 + i;
-        float p[4];
-        int8_unpack4(w[i], p);
-        f32x4 g = as_f4(s.Gw[k]);
-        g.x = fmaf(mw[k], dd.x, g.x);
-        g.y = fmaf(mw[k], dd.y, g.y);
-        g.z = fmaf(mw[k], dd.z, g.z);
-        g.w = fmaf(mw[k], dd.w, g.w);
-        const float bk = b * wk[k], keep = fmaf(-b, wk[k], 1.0f);
-        dva.x = fmaf(bk, g.x, dva.x);
-        dva.y = fmaf(bk, g.y, dva.y);
-        dva.z = fmaf(bk, g.z, dva.z);
-        dva.w = fmaf(bk, g.w, dva.w);
-        const float gp = g.x * p[0] + g.y * p[1] + g.z * p[2] + g.w * p[3];
-        da = fmaf(keep * sc[i], gp, da);
-        const float ap = a * sc[i];
-        dbk[k] = g.x * (vv.x - ap * p[0]) + g.y * (vv.y - ap * p[1]) +
-                 g.z * (vv.z - ap * p[2]) + g.w * (vv.w - ap * p[3]);
-        const float c = a * keep;
-        s.Gw[k] = as_u4(f32x4{c * g.x, c * g.y, c * g.z, c * g.w});
-      }
+      for (int k = 0; k < NI; ++k) sc[k] = __uint_as_float((uint32_t)s.scale[k] << 23);
+    }
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      float p[4];
+      int8_unpack4(w[k], p);
+      f32x4 g = as_f4(s.Gw[k]);
+      g.x = fmaf(mw[k], dd.x, g.x);
+      g.y = fmaf(mw[k], dd.y, g.y);
+      g.z = fmaf(mw[k], dd.z, g.z);
+      g.w = fmaf(mw[k], dd.w, g.w);
+      const float bk = b * wk[k], keep = fmaf(-b, wk[k], 1.0f);
+      dva.x = fmaf(bk, g.x, dva.x);
+      dva.y = fmaf(bk, g.y, dva.y);
+      dva.z = fmaf(bk, g.z, dva.z);
+      dva.w = fmaf(bk, g.w, dva.w);
+      const float gp = g.x * p[0] + g.y * p[1] + g.z * p[2] + g.w * p[3];
+      da = fmaf(keep * sc[k], gp, da);
+      const float ap = a * sc[k];
+      dbk[k] = g.x * (vv.x - ap * p[0]) + g.y * (vv.y - ap * p[1]) + g.z * (vv.z - ap * p[2]) +
+               g.w * (vv.w - ap * p[3]);
+      const float c = a * keep;
+      s.Gw[k] = as_u4(f32x4{c * g.x, c * g.y, c * g.z, c * g.w});
     }
     // ---- stores: read rows, then write rows (a row that is both ends with its
     // write-side value)
@@ -331,14 +372,10 @@ struct Scan8 {
 
     // ---- the step's sums.  d(beta k): over the row's LPR lanes, folded so that
     // lane lc ends with the row of k = lc.
-    float f[NI / 2];
-#pragma unroll
-    for (int i = 0; i < NI / 2; ++i) f[i] = fold<0>(dbk[2 * i], dbk[2 * i + 1]);
-#pragma unroll
-    for (int i = 0; i < NI / 4; ++i) f[i] = fold<1>(f[2 * i], f[2 * i + 1]);
-    if constexpr (NI == 8) f[0] = fold<2>(f[0], f[1]);
+    float f = fold<0>(dbk[0], dbk[1]);
+    if constexpr (NI == 4) f = fold<1>(f, fold<0>(dbk[2], dbk[3]));
     const int j = lc * RPI + lr;
-    if (j < A.W) sums[j] = f[0];
+    if (j < A.W) sums[j] = f;
     // dv: over the lanes of the same columns; half wavefronts and rows of 16
     // are added two values at a time, so component (0, 2, 1, 3)[lane / 16] of
     // the lane's four columns stays
@@ -350,7 +387,8 @@ struct Scan8 {
       auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(s0), __float_as_uint(s1), false, false);
       float x = __uint_as_float(q[0]) + __uint_as_float(q[1]);
       x += __uint_as_float(dpp_row_ror8(__float_as_uint(x)));
-      if constexpr (LPR == 4) x += __uint_as_float(dpp_row_ror4(__float_as_uint(x)));
+      x += __uint_as_float(dpp_row_ror4(__float_as_uint(x)));
+      if constexpr (LPR == 2) x += __uint_as_float(dpp_mov<0x122>(__float_as_uint(x)));  // ror 2
       const int lane = lane_id(), row = lane >> 4;
       if ((lane & 15) < LPR) dv[(lane & 15) * 4 + ((row & 1) << 1 | row >> 1)] = x;
     }
@@ -377,24 +415,24 @@ struct Scan8 {
   }
 };
 
-template <int COLS>
-__global__ __launch_bounds__(2 * kWave) void scan_bwd8_kernel(Bwd8Args A) {
-  __shared__ __align__(16) Lds8<COLS> sh;
-  using S = Scan8<COLS>;
+template <int COLS, int NC>
+__global__ __launch_bounds__((NC + 1) * kWave) void scan_bwd8_kernel(Bwd8Args A) {
+  __shared__ __align__(16) Lds8<COLS, NC> sh;
+  using S = Scan8<COLS, NC>;
   // XCD-aware numbering as in the forward: every tile of a memory on one XCD
   const int x = blockIdx.x & 7, rest = blockIdx.x >> 3;
-  const int tile = rest % A.ntiles, mem = (rest / A.ntiles) * 8 + x;
+  const int groups = A.ntiles / NC;
+  const int tile0 = (rest % groups) * NC, mem = (rest / groups) * 8 + x;
   if (mem >= A.n_mem) return;  // whole workgroup leaves together
-  const int64_t T = A.T, Tp = padded_steps(T);
-  const int64_t nchunks = Tp / kChunk;
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const int T = (int)A.T, Tp = (int)padded_steps(T);  // below 2^26 (checked on the host)
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 
-  if (wave == 1) {
+  if (wave == NC) {
     // loader: chunks 0 and 1 before the walk starts, then chunk c + 2 while
-    // the other wavefront walks chunk c
+    // the others walk chunk c
     const uint8_t* recs = reinterpret_cast<const uint8_t*>(A.rec + (int64_t)mem * Tp);
-    auto load = [&](int64_t c) __attribute__((always_inline)) {
-      if (c >= nchunks) return;
+    auto load = [&](int c) __attribute__((always_inline)) {
+      if (c * kChunk >= Tp) return;
       constexpr int kPieces = (int)(sizeof(Record) * kChunk / 16);
       const uint8_t* src = recs + c * (int64_t)(sizeof(Record) * kChunk);
       uint8_t* dst = reinterpret_cast<uint8_t*>(&sh.rec[c % kRing][0]);
@@ -403,18 +441,18 @@ __global__ __launch_bounds__(2 * kWave) void scan_bwd8_kernel(Bwd8Args A) {
         if (i * kWave + lane < kPieces)
           __builtin_amdgcn_global_load_lds((const void*)(src + (i * kWave + lane) * 16),
                                            (void*)(dst + i * kWave * 16), 16, 0, 0);
-      // v, then dout: kChunk steps of COLS columns; a step before the first: the first
-      constexpr int kVec = kChunk * COLS / 4;
+      // v, then dout: kChunk steps of the columns; a step before the first: the first
+      constexpr int kPer = NC * COLS / 4, kVec = kChunk * kPer;
       float* vd = &sh.vd[c % kRing][0][0][0];
 #pragma unroll
       for (int i = 0; i < (2 * kVec + kWave - 1) / kWave; ++i) {
-        const int e = i * kWave + lane, half = e / kVec, s = (e % kVec) / (COLS / 4);
-        int64_t t = T - 1 - (c * kChunk + s);
+        const int e = i * kWave + lane, half = e / kVec, s = (e % kVec) / kPer;
+        int t = T - 1 - (c * kChunk + s);
         t = t < 0 ? 0 : t;
         if (e < 2 * kVec)
           __builtin_amdgcn_global_load_lds(
-              (const void*)((half ? A.dout : A.v) + ((int64_t)mem * T + t) * A.d_v + tile * COLS +
-                            (e % (COLS / 4)) * 4),
+              (const void*)((half ? A.dout : A.v) + ((int64_t)mem * T + t) * A.d_v + tile0 * COLS +
+                            (e % kPer) * 4),
               (void*)(vd + i * kWave * 4), 16, 0, 0);
       }
     };
@@ -422,23 +460,27 @@ __global__ __launch_bounds__(2 * kWave) void scan_bwd8_kernel(Bwd8Args A) {
     load(1);
     __builtin_amdgcn_s_waitcnt(0);
     chunk_barrier();
-    for (int64_t c = 0; c * kChunk < T; ++c) {
-      load(c + 2);
-      __builtin_amdgcn_s_waitcnt(0);
+    for (int u = 0; u < T; u += 2) {
+      if (u % kChunk == 0) load(u / kChunk + 2);
+      if ((u + 2) % kChunk == 0) __builtin_amdgcn_s_waitcnt(0);
       chunk_barrier();
     }
+    // (a chunk still on its way at the end lands before the wavefront ends)
+    __builtin_amdgcn_s_waitcnt(0);
     return;
   }
 
+  const int tile = tile0 + wave;
   const int64_t recs = (int64_t)(A.d_v / 16) * T * (A.W + A.R);
   S s{A, sh};
   s.lr = lane / S::LPR;
   s.lc = lane % S::LPR;
+  s.col0 = wave * COLS;
+  s.word = (uint32_t)(tile * COLS % 16 + s.lc * 4);
   s.T = T;
   s.lane_off = (uint32_t)s.lc * 16u;
   s.step_rows = (uint32_t)(A.W + A.R);
-  s.rec0 = (uint32_t)(tile * (COLS / 16) + s.lc / 4) * (uint32_t)(T * (A.W + A.R)) +
-           (uint32_t)((lane & 3) * S::RPI + s.lr);
+  s.rec0 = (uint32_t)(tile * COLS / 16) * (uint32_t)((int64_t)T * (A.W + A.R));
   // descriptor ranges from ranges.h (checked on the host before the launch)
   s.gres = __builtin_amdgcn_make_buffer_rsrc(
       A.G + (int64_t)mem * A.N * A.d_v + tile * COLS, 0,
@@ -454,14 +496,26 @@ __global__ __launch_bounds__(2 * kWave) void scan_bwd8_kernel(Bwd8Args A) {
   chunk_barrier();
   typename S::Step even, odd;
   s.issue(even, 0);
-  for (int64_t u = 0; u < T; u += 2) {
-    s.step(even, odd, u, dv - u * A.d_v, sums - u * sums_step);
-    if (u + 1 < T) s.step(odd, even, u + 1, dv - (u + 1) * A.d_v, sums - (u + 1) * sums_step);
-    // end of a chunk: its LDS reads are done; the next but one is in
-    if ((u + 2) % kChunk == 0 || u + 2 >= T) {
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-      chunk_barrier();
-    }
+  // As many stores as a step makes after its loads, to offsets past the range
+  // (dropped; distinct, or they would be merged): the compiler's wait counts at
+  // the loop's head are the tighter of the two ways into it.
+#pragma unroll
+  for (int i = 0; i < 2 * S::NI; ++i)
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{0u, 0u, 0u, 0u}, s.gres,
+                                           kOffNone + (uint32_t)i * 16u, 0, 0);
+  const int64_t dv_step = -(int64_t)A.d_v;
+  int u = 0;
+  for (; u + 1 < T; u += 2, dv += 2 * dv_step, sums -= 2 * sums_step) {
+    s.step(even, odd, u, dv, sums);
+    s.step(odd, even, u + 1, dv + dv_step, sums - sums_step);
+    // Every two steps: keeps the two halves of a cache line of G close in time
+    // and, at a chunk's end (its LDS reads are done), the ring in step.
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    chunk_barrier();
+  }
+  if (u < T) {
+    s.step(even, odd, u, dv, sums);
+    chunk_barrier();
   }
 }
 
@@ -472,9 +526,11 @@ __global__ __launch_bounds__(256) void finish_kernel(Bwd8Args A) {
   if (u >= (int64_t)A.n_mem * A.T) return;  // whole wavefront leaves together
   const int lane = lane_id(), W = A.W;
   const float* p = A.sums + u * A.ntiles * (W + 1);
+  const int at = lane < W ? lane : W;  // lanes past W: dalpha's word again
   float sbk = 0.0f, sda = 0.0f;
+#pragma unroll 4
   for (int tl = 0; tl < A.ntiles; ++tl) {
-    if (lane < W) sbk += p[tl * (W + 1) + lane];
+    sbk += p[tl * (W + 1) + at];
     sda += p[tl * (W + 1) + W];
   }
   const float kj = lane < W ? A.wk[u * W + lane] : 0.0f;
@@ -488,9 +544,22 @@ __global__ __launch_bounds__(256) void finish_kernel(Bwd8Args A) {
 
 }  // namespace
 
+namespace {
+
+// Columns of a wavefront's tile.  Few memories: the scan goes at the pace of
+// one wavefront's instructions for a step, so with room for 8-column tiles on
+// a compute unit each (half the rows' instructions, twice the wavefronts) they
+// are taken.
+int scan_columns(int n_mem, int d_v) {
+  return (int64_t)n_mem * (d_v / 8) <= compute_units() ? 8 : 16;
+}
+
+}  // namespace
+
 size_t scan_backward8_workspace_bytes(int n_mem, int d_v, int64_t T, int W) {
   return (size_t)n_mem * ((size_t)padded_steps(T) * sizeof(Record) +
-                          (size_t)T * (size_t)(d_v / 16) * (size_t)(W + 1) * sizeof(float));
+                          (size_t)T * (size_t)(d_v / scan_columns(n_mem, d_v)) * (size_t)(W + 1) *
+                              sizeof(float));
 }
 
 hipError_t launch_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
@@ -503,7 +572,7 @@ hipError_t launch_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, in
   if (T == 0) return hipSuccess;
   if (!ranges::tape8_ok(d_v, T, W, R)) return hipErrorInvalidValue;  // checked by the C-ABI layer
   const int n_mem = B * H;
-  const int cols = first ? 16 : (d_v < 32 ? d_v : 32);
+  const int cols = scan_columns(n_mem, d_v);
   const int64_t Tp = padded_steps(T);
   Record* const rec = reinterpret_cast<Record*>(ws);
   Bwd8Args A{n_mem, N,    d_v, T,  W,   R,   widx,   wk,    ridx,  rw,  v,
@@ -513,11 +582,17 @@ hipError_t launch_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, in
                      stream, A);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t blocks = (int64_t)((n_mem + 7) / 8) * A.ntiles * 8;
-  if (cols == 32)
-    hipLaunchKernelGGL(scan_bwd8_kernel<32>, dim3((unsigned)blocks), dim3(2 * kWave), 0, stream, A);
+  // Many memories: the two 16-column halves of each cache line of G go to one
+  // workgroup, in step (64 memories: 1.71 against 2.12 ms in the sparse mode of
+  // 1024 steps; 16 memories, the chip not filled: 2.15 against 1.90).
+  const int nc = cols == 16 && A.ntiles > 1 && (int64_t)n_mem * (A.ntiles / 2) >= compute_units() ? 2 : 1;
+  const dim3 blocks((unsigned)((int64_t)((n_mem + 7) / 8) * (A.ntiles / nc) * 8));
+  if (nc == 2)
+    hipLaunchKernelGGL((scan_bwd8_kernel<16, 2>), blocks, dim3(3 * kWave), 0, stream, A);
+  else if (cols == 16)
+    hipLaunchKernelGGL((scan_bwd8_kernel<16, 1>), blocks, dim3(2 * kWave), 0, stream, A);
   else
-    hipLaunchKernelGGL(scan_bwd8_kernel<16>, dim3((unsigned)blocks), dim3(2 * kWave), 0, stream, A);
+    hipLaunchKernelGGL((scan_bwd8_kernel<8, 1>), blocks, dim3(2 * kWave), 0, stream, A);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(finish_kernel, dim3((unsigned)(((int64_t)n_mem * T + 3) / 4)), dim3(256), 0,

@@ -133,9 +133,11 @@ def test_tape8_read_entry_point():
 def test_backward8_entry_point():
     L = sdm.lib()
     size = L.sdm_scan_backward8_workspace_size
-    # 16 padded steps' records of 5 x 64 + 4 words, and 8 steps' sums of W + 1
+    # 16 padded steps' records of 5 x 64 + 4 words, and 8 steps' sums of W + 1 per tile
+    # (8 columns where there is a compute unit for each, else 16)
     ws = size(1, 1, 16, 8, 8, 8)
-    assert ws == 16 * 1296 + 8 * 9 * 4 and size(2, 3, 128, 7, 64, 1) == 6 * (8 * 1296 + 7 * 8 * 65 * 4)
+    assert ws == 16 * 1296 + 8 * 2 * 9 * 4
+    assert size(8, 8, 128, 7, 64, 1) == 64 * (8 * 1296 + 7 * 8 * 65 * 4)
     for bad in ((0, 1, 16, 8, 8, 8), (1, 1, 24, 8, 8, 8), (1, 1, 16, -1, 8, 8), (1, 1, 16, 8, 65, 8),
                 (1, 1, 16, 8, 8, 0), (1 << 11, 1 << 10, 16, 8, 8, 8), (1, 1, 16, 1 << 40, 8, 8)):
         assert size(*bad) == 0, bad
