@@ -25,6 +25,13 @@ __device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
+// The largest of four values' magnitude bits (the maximum that a NaN wins).
+__device__ __forceinline__ uint32_t max_mag4(const u32x4& x) {
+  const float a = __builtin_elementwise_maximum(fabsf(__uint_as_float(x.x)), fabsf(__uint_as_float(x.y)));
+  const float b = __builtin_elementwise_maximum(a, fabsf(__uint_as_float(x.z)));
+  return mag_bits(__builtin_elementwise_maximum(b, fabsf(__uint_as_float(x.w))));
+}
+
 // Maximum over the four lanes of a quad.
 __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
   m = umax(m, dpp_qp_xor1(m));
@@ -48,20 +55,22 @@ __device__ __forceinline__ uint32_t int8_scale(uint32_t m) {
   return m >= kF32Inf ? kMxNan : (e < (int)kMxMinScale ? kMxMinScale : (uint32_t)e);
 }
 
-// Four values over the scale 2^(b - 127), rounded to nearest even, as two's
-// complement bytes (0 in a block marked 255).  x * 2^(127 - b) is exact and
-// at most 127.5 in magnitude, so adding 1.5 * 2^23 leaves the rounded integer
-// in the low byte of the sum.
-__device__ __forceinline__ uint32_t int8_pack4(const float (&x)[4], uint32_t b) {
-  const float inv = scale_f32(254u - b);
+// Bits of the inverse scale 2^(127 - b).
+__device__ __forceinline__ uint32_t int8_inverse(uint32_t b) { return (254u - b) << 23; }
+
+// Four values (binary32 bits) times the inverse scale of their block, rounded
+// to nearest even, as two's complement bytes.  The product is exact and at
+// most 127.5 in magnitude, so adding 1.5 * 2^23 leaves the rounded integer in
+// the low byte of the sum.  (Of no meaning in a block marked 255.)
+__device__ __forceinline__ uint32_t int8_pack4(const u32x4& x, float inv) {
   constexpr float kMagic = 12582912.0f;
-  const uint32_t q0 = __float_as_uint(fmaf(x[0], inv, kMagic));
-  const uint32_t q1 = __float_as_uint(fmaf(x[1], inv, kMagic));
-  const uint32_t q2 = __float_as_uint(fmaf(x[2], inv, kMagic));
-  const uint32_t q3 = __float_as_uint(fmaf(x[3], inv, kMagic));
+  const uint32_t q0 = __float_as_uint(fmaf(__uint_as_float(x.x), inv, kMagic));
+  const uint32_t q1 = __float_as_uint(fmaf(__uint_as_float(x.y), inv, kMagic));
+  const uint32_t q2 = __float_as_uint(fmaf(__uint_as_float(x.z), inv, kMagic));
+  const uint32_t q3 = __float_as_uint(fmaf(__uint_as_float(x.w), inv, kMagic));
   const uint32_t lo = __builtin_amdgcn_perm(q1, q0, 0x0C0C0400u);
   const uint32_t hi = __builtin_amdgcn_perm(q3, q2, 0x04000C0Cu);
-  return b == kMxNan ? 0u : (lo | hi);
+  return lo | hi;
 }
 
 // The four integers of a code word as binary32 (exact).

@@ -431,7 +431,7 @@ struct Consumer {
 
   // The 8-bit tape (kSave8): 64 row slots' tile rows as blocks of 16 columns
   // (mx.h, 8-bit form).  The four lanes of a quad hold one block of a row;
-  // they agree on its scale, pack their four codes into a word each, and
+  // the scale comes from all four, each packs its four codes into a word, and
   // exchange words so that lane q of the quad ends with the whole records
   // (16 code bytes and the scale byte) of row slots (4 g + q) * RPI + lr: one
   // 16-byte and one 1-byte store per lane and 4 RPI rows, whose lanes write
@@ -441,23 +441,31 @@ struct Consumer {
                                         uint32_t row0) const {
     const int lane = lane_id(), q = lane & 3, lr = lane / LPR;
     const uint32_t block = block0 + (uint32_t)((lane % LPR) / 4) * block_rows;
+    const bool odd = q & 1, high = q & 2;
 #pragma unroll
     for (int g = 0; g < NI / 4; ++g) {
-      uint32_t w[4], sc = 0, at = kOffNone;
+      // maxima: folded over the quad so that lane q ends with slot q's, and its
+      // scale is found once
+      uint32_t m[4], at = kOffNone;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = 4 * g + i;
-        float x[4];
-        unpack<float>(rows[k], x);
-        uint32_t m = umax(umax(mag_bits(x[0]), mag_bits(x[1])), umax(mag_bits(x[2]), mag_bits(x[3])));
-        const uint32_t b = int8_scale(quad_max(m));
-        w[i] = int8_pack4(x, b);
-        sc = q == i ? b : sc;
+        m[i] = max_mag4(rows[k]);
         at = q == i ? ofs[k] : at;
       }
+      const uint32_t m01 = umax(odd ? m[1] : m[0], dpp_qp_xor1(odd ? m[0] : m[1]));
+      const uint32_t m23 = umax(odd ? m[3] : m[2], dpp_qp_xor1(odd ? m[2] : m[3]));
+      const uint32_t sc = int8_scale(umax(high ? m23 : m01, dpp_qp_xor2(high ? m01 : m23)));
+      const uint32_t inv = int8_inverse(sc);
+      uint32_t w[4] = {
+          int8_pack4(rows[4 * g], __uint_as_float(dpp_mov<0x00>(inv))),
+          int8_pack4(rows[4 * g + 1], __uint_as_float(dpp_mov<0x55>(inv))),
+          int8_pack4(rows[4 * g + 2], __uint_as_float(dpp_mov<0xAA>(inv))),
+          int8_pack4(rows[4 * g + 3], __uint_as_float(dpp_mov<0xFF>(inv)))};
       quad_transpose(w);
       const uint32_t rec = block + row0 + (uint32_t)((4 * g + q) * RPI + lr);
       const bool none = at >= kOffNone;
+      if (sc == kMxNan) w[0] = w[1] = w[2] = w[3] = 0u;
       __builtin_amdgcn_raw_buffer_store_b128(u32x4v{w[0], w[1], w[2], w[3]}, tres,
                                              none ? kOffNone : rec * 16u, 0, 0);
       __builtin_amdgcn_raw_buffer_store_b8((uint8_t)sc, sres, none ? kOffNone : rec, 0, 0);

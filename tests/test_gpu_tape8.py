@@ -60,12 +60,14 @@ def _step(d):
     return [d[k] for k in STEP]
 
 
-# (B, H, N, d_v, T, W, R): 16-column tiles with two row shards, 16-column tiles
-# unsharded, 32-column tiles, one tile, one step, one slot, the widest rows
+# (B, H, N, d_v, T, W, R): forward tiles of 16 columns with two row shards, 16
+# unsharded and 32, reverse tiles of 8 and 16; one tile, one step, one slot, the
+# widest rows
 CASES = [
     (1, 2, 70, 16, 77, 8, 5), (2, 2, 200, 64, 61, 32, 32), (3, 7, 100, 128, 45, 16, 9),
     (5, 8, 90, 128, 33, 13, 64), (1, 3, 128, 128, 60, 64, 64), (1, 1, 40, 16, 1, 1, 1),
     (2, 5, 64, 256, 19, 7, 33), (1, 1, 5, 32, 40, 3, 2), (9, 4, 50, 256, 9, 11, 1),
+    (8, 8, 70, 128, 18, 9, 12),  # 64 memories: cache lines of G shared by two wavefronts
 ]
 
 
