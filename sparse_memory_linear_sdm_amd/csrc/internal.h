@@ -45,7 +45,7 @@ hipError_t launch_project(const uint16_t* X, const uint16_t* Wt, int B, int T, i
 
 // 4-bit microscaled matrices (mx4.hip): tiles of this many rows and 512
 // columns, fewer rows where that would leave compute units without a tile.
-constexpr int kQuantRows = 32, kQuantFewRows = 4;
+constexpr int kQuantRows = 16, kQuantFewRows = 4;
 inline int quantize_rows(int64_t rows, int cols) {
   const int64_t tiles = (rows + kQuantRows - 1) / kQuantRows * ((cols + 511) / 512);
   return tiles >= 512 ? kQuantRows : kQuantFewRows;
