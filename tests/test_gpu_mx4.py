@@ -174,14 +174,19 @@ def _check(ops, got, B, T, d_model, H, n, d_v, tokens=None):
 
 
 PROJECT = [
-    # one block and ragged counts of tokens in the few-token kernel
+    # the few-token kernel: 1, 2 and 4 token fragments, 1 to 9 column fragments,
+    # one block of tokens and several, K shorter than its wavefronts' first turns
     (1, 1, 128, 1, 1, 1), (1, 1, 128, 1, 64, 16), (16, 1, 256, 2, 37, 32), (17, 1, 384, 1, 16, 16),
     (3, 11, 640, 3, 37, 32), (1, 47, 1152, 2, 128, 64), (64, 1, 4480, 1, 64, 128),
-    (32, 2, 8192, 1, 5, 16),
-    # 256 x 256 tiles: ragged rows and columns, half stages, T = 1 and 3
+    (32, 2, 8192, 1, 5, 16), (5, 1, 1024, 5, 1024, 64), (1, 64, 1408, 3, 2048, 16),
+    (30, 1, 1152, 6, 1024, 100), (10, 1, 256, 9, 1024, 128), (63, 1, 1280, 8, 1024, 128),
     (65, 1, 128, 1, 16, 16), (2, 150, 384, 3, 64, 16), (1, 257, 256, 1, 37, 32),
     (300, 1, 640, 1, 8, 16), (37, 3, 128, 2, 16, 16), (2, 700, 1024, 1, 128, 128),
     (1, 300, 512, 2, 256, 64),
+    # 256 x 256 tiles (enough tokens and columns to fill the chip with them): one
+    # stage of K and several, ragged rows and columns, T = 1, 3, 4 and long
+    (300, 4, 640, 3, 333, 40), (1, 1025, 128, 4, 256, 66), (3, 401, 1152, 2, 512, 17),
+    (1203, 1, 384, 1, 1024, 16), (401, 3, 256, 1, 1024, 16), (1, 2048, 512, 1, 1020, 14),
 ]
 
 
@@ -197,16 +202,32 @@ def test_project_mx4_parity(B, T, d_model, H, n, d_v):
     print(f"worst |err| / bound = {worst:.3e}")
 
 
-@pytest.mark.parametrize("B,T", [(1, 40), (2, 100)])
-def test_project_mx4_wide_scales(B, T):
+@pytest.mark.parametrize("B,T,H,n", [(1, 40, 2, 32), (2, 100, 2, 32), (2, 600, 1, 1024)])
+def test_project_mx4_wide_scales(B, T, H, n):
     """Block scales over 40 powers of two: sums of terms of very unequal size."""
-    ops = _operands(B, T, 1024, 2, 32, 32, seed=9, spread=20)
-    _check(ops, _project(ops, B, T, 1024, 2, 32, 32), B, T, 1024, 2, 32, 32)
+    ops = _operands(B, T, 1024, H, n, 32, seed=9, spread=20)
+    _check(ops, _project(ops, B, T, 1024, H, n, 32), B, T, 1024, H, n, 32)
 
 
-@pytest.mark.parametrize("B,T", [(5, 9), (3, 100)])
-def test_project_mx4_nan_blocks_stay_in_their_rows(B, T):
-    d_model, H, n, d_v = 512, 2, 16, 16
+@pytest.mark.parametrize("tokens", [3, 33, 1200])
+def test_project_mx4_writes_nothing_beside_its_outputs(tokens):
+    """Ragged last blocks: guard words around every output stay as they were."""
+    import torch
+
+    B, T, d_model, H, n, d_v = 1, tokens, 256, 1, 1025, 20
+    ops = _operands(B, T, d_model, H, n, d_v, seed=tokens)
+    shapes = [(B, H, T, n)] * 4 + [(B, H, T, d_v), (B, H, T), (B, H, T)]
+    bufs = [torch.full((64 + int(np.prod(s)) + 64,), 5.0, device="cuda") for s in shapes]
+    out = tuple(b[64:-64].view(s) for b, s in zip(bufs, shapes))
+    got = _project(ops, B, T, d_model, H, n, d_v, out=out)
+    assert all(a is b for a, b in zip(got, out))
+    _check(ops, got, B, T, d_model, H, n, d_v)
+    assert all(torch.all(b[:64] == 5) and torch.all(b[-64:] == 5) for b in bufs)
+
+
+@pytest.mark.parametrize("B,T,H,n", [(5, 9, 2, 16), (3, 100, 2, 16), (4, 300, 1, 1024)])
+def test_project_mx4_nan_blocks_stay_in_their_rows(B, T, H, n):
+    d_model, d_v = 512, 16
     ops = _operands(B, T, d_model, H, n, d_v, seed=4)
     (xq, xs), (wq, ws) = ops
     xs[2, 7, 1] = 255
@@ -249,7 +270,8 @@ def test_project_mx4_full_width_sampled():
     """The mid workload's widths (d_model 16384, H = 8, n = 1024, d_v = 128):
     prompts through the tiles, a decode step through the few-token kernel."""
     H, n, d_v, d_model = 8, 1024, 128, 16384
-    for B, T, toks in ((2, 300, [0, 255, 256, 300, 511, 599]), (48, 1, [0, 15, 16, 33, 47])):
+    for B, T, toks in ((2, 300, [0, 255, 256, 300, 511, 599]), (48, 1, [0, 15, 16, 33, 47]),
+                       (9, 1, [0, 4, 8])):
         ops = _operands(B, T, d_model, H, n, d_v, seed=T)
         got = _project(ops, B, T, d_model, H, n, d_v)
         _check(ops, got, B, T, d_model, H, n, d_v, tokens=toks)
