@@ -199,6 +199,30 @@ def _call(fn, t, stream, *args):
     _check(fn(*args, handle))
 
 
+def _empty_on(stream, device):
+    """torch.empty(shape, dtype) for the tensors a call makes.  The call's
+    stream is the first to write them, so they are that stream's memory (what
+    the allocator hands out for another stream may still be in use there), and
+    those the caller gets are marked as used by the current stream too."""
+    import torch
+
+    if stream is None or device.type != "cuda":
+        return lambda shape, dtype, mine=False: torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+
+    def make(shape, dtype, mine=False):
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        if not mine and stream != current:
+            t.record_stream(current)
+        return t
+
+    return make
+
+
 def _state_dtype(M):
     import torch
 
@@ -224,9 +248,9 @@ def _units(lead):
     return units
 
 
-def _project_out(B, T, H, P, n, weights, out, device):
-    """The projections' 7 output tensors, made unless the caller gives them,
-    and their checked arguments."""
+def _project_out(B, T, H, P, n, weights, out, empty):
+    """The projections' 7 output tensors, made by empty(shape, dtype) unless
+    the caller gives them, and their checked arguments."""
     import torch
 
     f32 = torch.float32
@@ -237,7 +261,7 @@ def _project_out(B, T, H, P, n, weights, out, device):
     shapes = [(B, H, T, n)] * 4 + [(B, H, T, d_v), (B, H, T), (B, H, T)]
     names = ("s1", "s2", "q1", "q2", "v", "alpha", "beta")
     if out is None:
-        out = tuple(torch.empty(sh, dtype=f32, device=device) for sh in shapes)
+        out = tuple(empty(sh, f32) for sh in shapes)
     if len(out) != 7:
         raise ValueError("out must hold 7 tensors (s1, s2, q1, q2, v, alpha, beta)")
     return tuple(out), [_arg(t, f32, sh, nm) for t, sh, nm in zip(out, shapes, names)]
@@ -256,7 +280,7 @@ def project(X, Wt, n: int, out=None, stream=None):
         raise ValueError("X must be [B, T, d_model] and Wt [H, P, d_model]")
     B, T, d_model = X.shape
     H, P = Wt.shape[0], Wt.shape[1]
-    out, outs = _project_out(B, T, H, P, n, "Wt", out, X.device)
+    out, outs = _project_out(B, T, H, P, n, "Wt", out, _empty_on(None, X.device))
     ptrs = _gpu(_arg(X, bf16, (B, T, d_model), "X"), _arg(Wt, bf16, (H, P, d_model), "Wt"), *outs)
     _check(lib().sdm_project(ptrs[0], ptrs[1], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[2:],
                              _stream(stream)))
@@ -296,8 +320,8 @@ def mx4_quantize(x, out=None, stream=None):
     *lead, cols = shape
     rows, dtype = _units(lead), _value_dtype(x.dtype)
     if out is None:
-        out = (torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device),
-               torch.empty((cols // 128, rows, 4), dtype=torch.uint8, device=x.device))
+        empty = _empty_on(stream, x.device)
+        out = (empty((*lead, cols // 2), torch.uint8), empty((cols // 128, rows, 4), torch.uint8))
     codes, scales = out
     px, pc, ps = _gpu(_arg(x, x.dtype, shape, "x"), *_mx4_args(codes, scales, shape))
     _call(lib().sdm_mx4_quantize, x, stream, px, dtype, rows, cols, pc, ps)
@@ -313,8 +337,7 @@ def mx4_dequantize(codes, scales, dtype=None, out=None, stream=None):
         raise ValueError("codes must have a last dimension cols/2")
     shape = (*codes.shape[:-1], 2 * codes.shape[-1])
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32 if dtype is None else dtype,
-                          device=codes.device)
+        out = _empty_on(stream, codes.device)(shape, torch.float32 if dtype is None else dtype)
     elif dtype is not None and dtype != out.dtype:
         raise ValueError(f"out must be {dtype}, got {out.dtype}")
     dt = _value_dtype(out.dtype)
@@ -333,7 +356,7 @@ def project_mx4(Xq, Xs, Wq, Ws, n: int, out=None, stream=None):
     B, T, half = Xq.shape
     H, P = Wq.shape[0], Wq.shape[1]
     d_model = 2 * half
-    out, outs = _project_out(B, T, H, P, n, "Wq", out, Xq.device)
+    out, outs = _project_out(B, T, H, P, n, "Wq", out, _empty_on(stream, Xq.device))
     ptrs = _gpu(*_mx4_args(Xq, Xs, (B, T, d_model), ("Xq", "Xs")),
                 *_mx4_args(Wq, Ws, (H, P, d_model), ("Wq", "Ws")), *outs)
     _call(lib().sdm_project_mx4, Xq, stream, *ptrs[:4], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[4:])
@@ -551,11 +574,12 @@ def scan_train8(M, widx, wk, ridx, rw, v, alpha, beta, out=None, tape=None, stre
     B, H, N, d_v, T, W, R = _scan_shapes(M, widx, ridx)
     am = _arg(M, f32, (B, H, N, d_v), "M")
     ins = _scan_args(B, H, T, W, R, d_v, widx, wk, ridx, rw, v, alpha, beta)
+    empty = _empty_on(stream, M.device)
     if out is None:
-        out = torch.empty((B, H, T, d_v), dtype=f32, device=M.device)
+        out = empty((B, H, T, d_v), f32)
     if tape is None:
-        tape = (torch.empty((B, H, d_v // 16, T, W + R, 16), dtype=torch.int8, device=M.device),
-                torch.empty((B, H, d_v // 16, T, W + R), dtype=torch.uint8, device=M.device))
+        tape = (empty((B, H, d_v // 16, T, W + R, 16), torch.int8),
+                empty((B, H, d_v // 16, T, W + R), torch.uint8))
     pm, *ptrs = _gpu(am, *ins, _arg(out, f32, (B, H, T, d_v), "out"),
                      *_tape8_args(tape, B, H, T, W + R, d_v))
     _call(lib().sdm_scan_train8, M, stream, pm, B, H, N, d_v, T, W, R, *ptrs)
@@ -573,8 +597,7 @@ def tape8_read(tape, dtype=None, out=None, stream=None):
     B, H, nb, T, S = codes.shape[:5]
     shape = (B, H, T, S, 16 * nb)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32 if dtype is None else dtype,
-                          device=codes.device)
+        out = _empty_on(stream, codes.device)(shape, torch.float32 if dtype is None else dtype)
     elif dtype is not None and dtype != out.dtype:
         raise ValueError(f"out must be {dtype}, got {out.dtype}")
     dt = _value_dtype(out.dtype)
@@ -597,13 +620,14 @@ def scan_backward8(widx, wk, ridx, rw, v, alpha, beta, tape, dout, G, workspace=
     ins += [_arg(dout, f32, (B, H, T, d_v), "dout"), _arg(G, f32, (B, H, N, d_v), "G")]
     shapes = {"dv": (B, H, T, d_v), "dwk": (B, H, T, W), "drw": (B, H, T, R),
               "dalpha": (B, H, T), "dbeta": (B, H, T)}
+    empty = _empty_on(stream, G.device)
     if out is None:
-        out = {k: torch.empty(shp, dtype=f32, device=G.device) for k, shp in shapes.items()}
+        out = {k: empty(shp, f32) for k, shp in shapes.items()}
     ins += [_arg(out[k], f32, shp, k) for k, shp in shapes.items()]
     af = None if first is None else _arg(first, torch.int64, (B, H, T, 2), "first")
     if workspace is None:
         need = int(lib().sdm_scan_backward8_workspace_size(B, H, d_v, T, W, R))
-        workspace = torch.empty((max(need, 16) + 3) // 4, dtype=f32, device=G.device)
+        workspace = empty((max(need, 16) + 3) // 4, f32, mine=True)
     ptrs = _gpu(*ins, af, _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()
     _call(lib().sdm_scan_backward8, G, stream, B, H, N, d_v, T, W, R, *ptrs, nbytes)

@@ -324,6 +324,92 @@ def test_backward8_without_allocation():
     assert b is out and torch.equal(Ga, Gb) and all(torch.equal(a[k], out[k]) for k in a)
 
 
+def test_a_side_stream_owns_what_the_call_makes():
+    """Called on a side stream with nothing passed in, and with the current stream
+    filling fresh memory of the workspace's size right after: the workspace the
+    call made must not be among it."""
+    import torch
+
+    sdm = _sdm()
+    B, H, N, d_v, T, W, R = 2, 2, 300, 64, 400, 32, 32
+    d = _inputs(B, H, N, d_v, T, W, R, seed=12, strays=False)
+    _, tape = sdm.scan_train8(d["M"].clone(), *_step(d))
+    G0 = torch.randn_like(d["M"])
+    Ga = G0.clone()
+    want = sdm.scan_backward8(*_step(d), tape, d["dout"], Ga)
+    size = sdm.lib().sdm_scan_backward8_workspace_size(B, H, d_v, T, W, R)
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        Gb = G0.clone()
+        torch.cuda.synchronize()
+        got = sdm.scan_backward8(*_step(d), tape, d["dout"], Gb, stream=handle)
+        for _ in range(3):
+            torch.full((size // 4,), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(Ga, Gb) and all(torch.equal(want[k], got[k]) for k in want)
+
+
+def test_two_streams_at_once():
+    """Two training steps side by side on two streams, each with its own workspace."""
+    import torch
+
+    sdm = _sdm()
+    size = (2, 4, 120, 128, 150, 16, 16)
+    B, H, N, d_v, T, W, R = size
+    ds = [_inputs(*size, seed=k, strays=False) for k in (20, 21)]
+
+    def run(d, stream):
+        M, G = d["M"].clone(), torch.zeros_like(d["M"])
+        out, tape = sdm.scan_train8(M, *_step(d), stream=stream)
+        g = sdm.scan_backward8(*_step(d), tape, d["dout"], G, stream=stream)
+        return [M, out, *tape, G, *g.values()]
+
+    want = [run(d, None) for d in ds]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for d, s in zip(ds, streams):
+            with torch.cuda.stream(s):
+                got.append(run(d, s))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_graphs_share_a_workspace():
+    """Reverse passes of two sizes captured into two graphs over one workspace,
+    replayed in turn on one stream."""
+    import torch
+
+    sdm = _sdm()
+    sizes = [(1, 2, 50, 64, 30, 8, 8), (4, 4, 90, 128, 21, 12, 16)]
+    ds = [_inputs(*z, seed=k, strays=False) for k, z in enumerate(sizes)]
+    need = max(sdm.lib().sdm_scan_backward8_workspace_size(z[0], z[1], *z[3:]) for z in sizes)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for d in ds:
+        _, tape = sdm.scan_train8(d["M"].clone(), *_step(d))
+        G0 = torch.randn_like(d["M"])
+        Gw = G0.clone()
+        want = sdm.scan_backward8(*_step(d), tape, d["dout"], Gw)
+        G, out = G0.clone(), {k: torch.empty_like(x) for k, x in want.items()}
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            G.copy_(G0)
+            sdm.scan_backward8(*_step(d), tape, d["dout"], G, workspace=ws, out=out)
+        graphs.append((graph, G, Gw, out, want, G0, tape))
+    for k in range(4):
+        graphs[k % 2][0].replay()
+        graphs[1 - k % 2][0].replay()
+        torch.cuda.synchronize()
+        for _, G, Gw, out, want, *_ in graphs:
+            assert torch.equal(G, Gw) and all(torch.equal(out[n], want[n]) for n in want), k
+            G.fill_(5.0)
+            for x in out.values():
+                x.fill_(5.0)
+
+
 def test_the_layer_in_4_and_8_bits():
     """A training step as it would be used: tokens and weights in 4 bits through
     the projections, both selections, the forward with its 8-bit tape, the
