@@ -550,16 +550,21 @@ namespace {
 // one wavefront's instructions for a step, so with room for 8-column tiles on
 // a compute unit each (half the rows' instructions, twice the wavefronts) they
 // are taken.
+constexpr int kMostUnits = 256;  // compute units of an undivided GPU
+bool few_memories(int n_mem, int d_v, int units) { return (int64_t)n_mem * (d_v / 8) <= units; }
 int scan_columns(int n_mem, int d_v) {
-  return (int64_t)n_mem * (d_v / 8) <= compute_units() ? 8 : 16;
+  const int cus = compute_units();
+  return few_memories(n_mem, d_v, cus < kMostUnits ? cus : kMostUnits) ? 8 : 16;
 }
 
 }  // namespace
 
+// (for the narrower tiles wherever some GPU would take them: the size is the
+// same whichever GPU is current)
 size_t scan_backward8_workspace_bytes(int n_mem, int d_v, int64_t T, int W) {
+  const int tiles = d_v / (few_memories(n_mem, d_v, kMostUnits) ? 8 : 16);
   return (size_t)n_mem * ((size_t)padded_steps(T) * sizeof(Record) +
-                          (size_t)T * (size_t)(d_v / scan_columns(n_mem, d_v)) * (size_t)(W + 1) *
-                              sizeof(float));
+                          (size_t)T * (size_t)tiles * (size_t)(W + 1) * sizeof(float));
 }
 
 hipError_t launch_scan_backward8(int B, int H, int64_t N, int d_v, int64_t T, int W, int R,
