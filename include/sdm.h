@@ -110,9 +110,9 @@ int sdm_project(const uint16_t* X, const uint16_t* Wt, int B, int T, int d_model
  *           (g, r) scales columns 128 g + 32 j .. + 31 of row r.
  *   x       [rows, cols] fp32 (dtype SDM_F32) or bf16 bits (SDM_BF16),
  *           16-byte aligned.
- * cols is a multiple of 128 in [128, 65536]; at most 2^24 - 1 tiles of 32
- * rows x 512 columns per call (4 rows when there are fewer than 512 such
- * tiles).  rows = 0 is a valid no-op (every array may then be NULL). */
+ * cols is a multiple of 128 in [128, 65536]; rows < 2^31, and at most
+ * 2^24 - 1 tiles of 16 rows x 512 columns per call.  rows = 0 is a valid no-op
+ * (every array may then be NULL). */
 int sdm_mx4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, uint8_t* codes,
                      uint8_t* scales, void* stream);
 
@@ -362,7 +362,7 @@ int sdm_tape8_read(const int8_t* tape, const uint8_t* tape_scale, int B, int H, 
 
 /* Bytes of workspace sdm_scan_backward8 needs for these sizes (0 if they are
  * not supported): about 1.3 KB per memory and step, and 4*(W + 1) for each 16
- * columns. */
+ * columns (8 columns for up to 2048/d_v memories). */
 size_t sdm_scan_backward8_workspace_size(int B, int H, int d_v, int64_t T, int W, int R);
 
 /* sdm_scan_backward from an 8-bit tape: the gradients of the step at the

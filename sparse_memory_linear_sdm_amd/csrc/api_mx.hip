@@ -19,9 +19,9 @@ int check_mx4(int64_t rows, int64_t cols, int dtype, const uint8_t* codes, const
                 (long long)cols);
   if (rows >= ((int64_t)1 << 31) ||
       sdm::quantize_blocks(rows, (int)cols) > sdm::kMaxStrideBlocks)
-    return fail(SDM_ERR_UNSUPPORTED, "more than 2^24 - 1 tiles of 32 rows x 512 columns "
-                "(rows=%lld, cols=%lld); split the rows over several calls", (long long)rows,
-                (long long)cols);
+    return fail(SDM_ERR_UNSUPPORTED, "rows must be below 2^31, and in at most 2^24 - 1 tiles of 16 "
+                "rows x 512 columns (rows=%lld, cols=%lld); split the rows over several calls",
+                (long long)rows, (long long)cols);
   if (rows > 0 && (!codes || !scales))
     return fail(SDM_ERR_INVALID, "codes and scales must not be NULL");
   if (!aligned(codes, 16) || !aligned(scales, 4))

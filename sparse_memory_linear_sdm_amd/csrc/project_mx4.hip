@@ -276,7 +276,7 @@ __global__ __launch_bounds__(kXThreads) void project_mx4_kernel(Mx4Args A) {
 // for 64 tokens at d_model 16384 x 33808 columns.  So four neighbouring lanes
 // load 64 bytes of a row, the turn's fragments pass through the wavefront's own
 // piece of LDS (16-byte segments swizzled as in the tiles), and the turn after
-// it is in flight in registers: 90 us, floor 63; one token 57-59 us.
+// it is in flight in registers: 79 us, floor 63; one token 56 us.
 template <int MT, int CT>
 constexpr int few_waves() {  // the accumulators of 4 x 7 blocks and up leave room for four
   return MT * CT >= 28 ? 4 : 8;

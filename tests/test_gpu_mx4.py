@@ -58,7 +58,7 @@ def _inputs(rows, cols, seed, dtype):
 
 
 SHAPES = [(1, 128), (3, 128), (4, 512), (5, 640), (33, 384), (130, 1152),
-          (2049, 4224)]  # the last: 65 x 9 tiles of 32 rows
+          (2049, 4224)]  # the last: 129 x 9 tiles of 16 rows
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
@@ -313,6 +313,31 @@ def test_calls_on_another_stream_and_captured():
             want = sdm.project_mx4(*sdm.mx4_quantize(inp), *w, 16)
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(want, held)), k
+
+
+@pytest.mark.parametrize("B,T,n", [(1, 1, 8), (2, 35, 8), (3, 400, 256)])
+def test_project_mx4_widest_rows(B, T, n):
+    """d_model 65536, the largest."""
+    ops = _operands(B, T, 65536, 1, n, 16, seed=T)
+    _check(ops, _project(ops, B, T, 65536, 1, n, 16), B, T, 65536, 1, n, 16,
+           tokens=None if B * T < 100 else [0, 255, 256, 700, B * T - 1])
+
+
+def test_two_streams_project_at_once():
+    """Prompt tiles on one stream beside decode steps on another."""
+    import torch
+
+    sdm = _sdm()
+    w = sdm.mx4_quantize(torch.randn(2, 4 * 256 + 64 + 2, 1024, device="cuda"))
+    xs = [sdm.mx4_quantize(torch.randn(B, T, 1024, device="cuda")) for B, T in ((4, 500), (7, 1))]
+    want = [sdm.project_mx4(*x, *w, 256) for x in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [sdm.project_mx4(*x, *w, 256, stream=s) for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
 def test_refusals_on_the_gpu():

@@ -32,7 +32,7 @@ def test_mx4_entry_points():
         (4, None, 1, "codes"), (4, FAKE + 8, 1, "16-byte"), (5, None, 1, "scales"),
         (5, FAKE + 2, 1, "4-byte")])
     assert L.sdm_mx4_quantize(None, 0, 0, 256, None, None, None) == 0
-    # one tile of 512 columns per 32 rows: 2^24 - 1 tiles is the largest grid
+    # one tile of 512 columns per 16 rows: 2^24 - 1 tiles is the largest grid
     assert L.sdm_mx4_quantize(FAKE, 0, 1 << 30, 512, FAKE, FAKE, None) == 2 and "tiles" in _err()
     ok = (FAKE, FAKE, 0, 10, 256, FAKE, None)  # codes, scales, dtype, rows, cols, x, stream
     _each(L.sdm_mx4_dequantize, ok, [
