@@ -111,8 +111,9 @@ int sdm_project(const uint16_t* X, const uint16_t* Wt, int B, int T, int d_model
  *   x       [rows, cols] fp32 (dtype SDM_F32) or bf16 bits (SDM_BF16),
  *           16-byte aligned.
  * cols is a multiple of 128 in [128, 65536]; rows < 2^31, and at most
- * 2^24 - 1 tiles of 16 rows x 512 columns per call.  rows = 0 is a valid no-op
- * (every array may then be NULL). */
+ * 2^24 - 1 tiles of 8 rows x 512 columns per call (256 columns where
+ * sdm_mx4_dequantize writes fp32).  rows = 0 is a valid no-op (every array may
+ * then be NULL). */
 int sdm_mx4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, uint8_t* codes,
                      uint8_t* scales, void* stream);
 

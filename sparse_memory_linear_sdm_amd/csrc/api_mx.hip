@@ -10,7 +10,8 @@ namespace {
 using namespace sdm::api;
 
 // A 4-bit microscaled matrix and the type of its unquantised side.
-int check_mx4(int64_t rows, int64_t cols, int dtype, const uint8_t* codes, const uint8_t* scales) {
+int check_mx4(int64_t rows, int64_t cols, int dtype, int tile_cols, const uint8_t* codes,
+              const uint8_t* scales) {
   if (dtype != SDM_F32 && dtype != SDM_BF16)
     return fail(SDM_ERR_INVALID, "dtype must be SDM_F32 or SDM_BF16 (got %d)", dtype);
   if (rows < 0) return fail(SDM_ERR_INVALID, "rows must be >= 0");
@@ -18,10 +19,10 @@ int check_mx4(int64_t rows, int64_t cols, int dtype, const uint8_t* codes, const
     return fail(SDM_ERR_UNSUPPORTED, "cols must be a multiple of 128 in [128, 65536] (got %lld)",
                 (long long)cols);
   if (rows >= ((int64_t)1 << 31) ||
-      sdm::quantize_blocks(rows, (int)cols) > sdm::kMaxStrideBlocks)
-    return fail(SDM_ERR_UNSUPPORTED, "rows must be below 2^31, and in at most 2^24 - 1 tiles of 16 "
-                "rows x 512 columns (rows=%lld, cols=%lld); split the rows over several calls",
-                (long long)rows, (long long)cols);
+      sdm::quantize_tiles(rows, (int)cols, tile_cols) > sdm::kMaxStrideBlocks)
+    return fail(SDM_ERR_UNSUPPORTED, "rows must be below 2^31, and in at most 2^24 - 1 tiles of 8 "
+                "rows x %d columns (rows=%lld, cols=%lld); split the rows over several calls",
+                tile_cols, (long long)rows, (long long)cols);
   if (rows > 0 && (!codes || !scales))
     return fail(SDM_ERR_INVALID, "codes and scales must not be NULL");
   if (!aligned(codes, 16) || !aligned(scales, 4))
@@ -36,7 +37,7 @@ extern "C" {
 int sdm_mx4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, uint8_t* codes,
                      uint8_t* scales, void* stream) {
   int rc;
-  if ((rc = check_mx4(rows, cols, dtype, codes, scales))) return rc;
+  if ((rc = check_mx4(rows, cols, dtype, 512, codes, scales))) return rc;
   hipStream_t s = (hipStream_t)stream;
   if (rows == 0) return finish("sdm_mx4_quantize", hipSuccess, s);  // the arrays may be NULL
   if (!x) return fail(SDM_ERR_INVALID, "x is NULL");
@@ -48,7 +49,8 @@ int sdm_mx4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, uint8
 int sdm_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype, int64_t rows,
                        int64_t cols, void* x, void* stream) {
   int rc;
-  if ((rc = check_mx4(rows, cols, dtype, codes, scales))) return rc;
+  const int tile_cols = sdm::dequantize_cols(dtype == SDM_BF16 ? 2 : 4);
+  if ((rc = check_mx4(rows, cols, dtype, tile_cols, codes, scales))) return rc;
   hipStream_t s = (hipStream_t)stream;
   if (rows == 0) return finish("sdm_mx4_dequantize", hipSuccess, s);  // the arrays may be NULL
   if (!x) return fail(SDM_ERR_INVALID, "x is NULL");

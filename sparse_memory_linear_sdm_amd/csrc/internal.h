@@ -43,16 +43,16 @@ hipError_t launch_project(const uint16_t* X, const uint16_t* Wt, int B, int T, i
                           int n, int d_v, float* s1, float* s2, float* q1, float* q2, float* v,
                           float* alpha, float* beta, hipStream_t stream);
 
-// 4-bit microscaled matrices (mx4.hip): tiles of this many rows and 512
-// columns, fewer rows where that would leave compute units without a tile.
-constexpr int kQuantRows = 16, kQuantFewRows = 4;
-inline int quantize_rows(int64_t rows, int cols) {
-  const int64_t tiles = (rows + kQuantRows - 1) / kQuantRows * ((cols + 511) / 512);
-  return tiles >= 512 ? kQuantRows : kQuantFewRows;
+// 4-bit microscaled matrices (mx4.hip): one workgroup per tile of kQuantRows
+// rows and 512 columns, reading back of as many columns as fill 1 KiB.
+constexpr int kQuantRows = 8;
+constexpr int dequantize_cols(int elem_bytes) { return 1024 / elem_bytes; }
+inline int64_t quantize_tiles(int64_t rows, int cols, int tile_cols) {
+  return (rows + kQuantRows - 1) / kQuantRows * ((cols + tile_cols - 1) / tile_cols);
 }
-inline int64_t quantize_blocks(int64_t rows, int cols) {
-  const int r = quantize_rows(rows, cols);
-  return (rows + r - 1) / r * ((cols + 511) / 512);
+inline int64_t quantize_blocks(int64_t rows, int cols) { return quantize_tiles(rows, cols, 512); }
+inline int64_t dequantize_blocks(int64_t rows, int cols, int elem_bytes) {
+  return quantize_tiles(rows, cols, dequantize_cols(elem_bytes));
 }
 hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t rows, int cols, uint8_t* codes,
                                uint8_t* scales, hipStream_t stream);

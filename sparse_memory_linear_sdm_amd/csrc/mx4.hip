@@ -8,13 +8,15 @@
 // 4-byte word per row and 128 columns).
 //
 // Both passes are streams bound by memory: each value is read once and
-// written once.  A workgroup takes 16 rows (4: quantize_rows) of 512 columns: a
-// wavefront reads 512 columns of a row at a time (8 values per lane: one
-// 16-byte load of bf16, two of fp32), the block maximum is two exchanges over
-// the four lanes that share a block, and the scale words are gathered in LDS
-// so that the rows' words of each group go out together.  32768 x 16384 bf16:
-// 319 us, 4.3 TB/s; 4226 x 16384 fp32: 51 us, 6.1 TB/s; back: 332 and 45 us.
-// (Loads past the caches: the fp32 case 63 us.)
+// written once.  A workgroup takes a tile of kQuantRows rows; tiles follow each
+// other along the columns, so that the chip walks whole rows of the matrix
+// (down the rows first: 326 against 216 us for 32768 x 16384 bf16; 4 and 16
+// rows a tile: 219 and 235).  Quantisation: a wavefront reads 512 columns of a
+// row at a time (8 values per lane: one 16-byte load of bf16, two of fp32), the
+// block maximum is two exchanges over the four lanes that share a block, and
+// the scale words are gathered in LDS so that the rows' words of each group go
+// out together.  32768 x 16384 bf16: 216 us, 6.4 TB/s, and 216 us back; 4226 x
+// 16384 fp32: 47 and 44 us.
 #include "internal.h"
 #include "mx.h"
 
@@ -46,16 +48,17 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
   }
 }
 
-template <typename T, int ROWS>
+template <typename T>
 __global__ __launch_bounds__(kQWaves* kWave) void quantize_kernel(const T* __restrict__ x,
                                                                   int64_t rows, int cols,
                                                                   uint32_t* __restrict__ codes,
                                                                   uint32_t* __restrict__ scales) {
-  __shared__ uint32_t sc[kQCols / 128][ROWS];
+  __shared__ uint32_t sc[kQCols / 128][kQuantRows];
   const int lane = lane_id(), wave = threadIdx.x / kWave;
-  const int64_t r0 = (int64_t)blockIdx.x * ROWS;
-  const int c0 = blockIdx.y * kQCols, c = c0 + lane * 8;
-  constexpr int kEach = ROWS / kQWaves;
+  const uint32_t tiles = (uint32_t)(cols + kQCols - 1) / kQCols, rowtile = blockIdx.x / tiles;
+  const int64_t r0 = (int64_t)rowtile * kQuantRows;
+  const int c0 = (int)(blockIdx.x - rowtile * tiles) * kQCols, c = c0 + lane * 8;
+  constexpr int kEach = kQuantRows / kQWaves;
   float v[kEach][8];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -85,38 +88,46 @@ __global__ __launch_bounds__(kQWaves* kWave) void quantize_kernel(const T* __res
       reinterpret_cast<uint8_t*>(&sc[lane / 16][wave * kEach + i])[(lane / 4) & 3] = (uint8_t)b;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kQCols / 128 * ROWS; i += kQWaves * kWave) {
-    const int g = c0 / 128 + i / ROWS;
-    const int64_t r = r0 + i % ROWS;
-    if (g < cols / 128 && r < rows) scales[(int64_t)g * rows + r] = sc[i / ROWS][i % ROWS];
+  for (int i = threadIdx.x; i < kQCols / 128 * kQuantRows; i += kQWaves * kWave) {
+    const int g = c0 / 128 + i / kQuantRows;
+    const int64_t r = r0 + i % kQuantRows;
+    if (g < cols / 128 && r < rows) scales[(int64_t)g * rows + r] = sc[i / kQuantRows][i % kQuantRows];
   }
 }
 
-// Reading back: a thread writes 16 bytes (8 bf16 values from a word of codes,
-// 4 fp32 values from half a word), so that a wavefront's stores are contiguous.
-// I: 32-bit index arithmetic where the pieces' count allows it.
-template <typename T, typename I>
-__global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restrict__ codes,
-                                                         const uint8_t* __restrict__ scales,
-                                                         int64_t rows, int cols, int64_t pieces,
-                                                         u32x4* __restrict__ x) {
-  constexpr int kEach = 16 / sizeof(T);
-  const I n = (I)pieces, per = (I)(cols / kEach), step = (I)gridDim.x * 256;
-  for (I i = (I)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-    const I r = i / per;
-    const int c = (int)(i - r * per) * kEach;
-    const uint32_t b = scales[((int64_t)(c / 128) * rows + r) * 4 + (c / 32) % 4];
-    // code 0 is 2^-127, a subnormal; 255 reads as NaN
-    const float s = b == kMxNan ? __uint_as_float(0x7FC00000u)
-                                : (b == 0 ? __uint_as_float(0x00400000u) : scale_f32(b));
-    uint32_t q;
+// Reading back: a thread takes 16 bytes of output (8 bf16 values from a word of
+// codes, 4 fp32 values from half a word) in each of its wavefront's rows, so
+// that the stores are contiguous.
+template <typename T>
+__global__ __launch_bounds__(kQWaves* kWave) void dequantize_kernel(
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int cols,
+    u32x4* __restrict__ x) {
+  constexpr int kEach = 16 / sizeof(T), kCols = kWave * kEach, kRows = kQuantRows / kQWaves;
+  static_assert(kCols == dequantize_cols(sizeof(T)), "the host's count of tiles");
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  const uint32_t tiles = (uint32_t)(cols + kCols - 1) / kCols, rowtile = blockIdx.x / tiles;
+  const int c = (int)(blockIdx.x - rowtile * tiles) * kCols + lane * kEach;
+  if (c >= cols) return;
+  const int64_t r0 = (int64_t)rowtile * kQuantRows + wave * kRows;
+  uint32_t q[kRows], b[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t r = r0 + i < rows ? r0 + i : rows - 1;
     if constexpr (kEach == 8)
-      q = reinterpret_cast<const uint32_t*>(codes)[i];
+      q[i] = reinterpret_cast<const uint32_t*>(codes)[(r * cols + c) / kEach];
     else
-      q = reinterpret_cast<const uint16_t*>(codes)[i];
+      q[i] = reinterpret_cast<const uint16_t*>(codes)[(r * cols + c) / kEach];
+    b[i] = scales[((int64_t)(c / 128) * rows + r) * 4 + (c / 32) % 4];
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (r0 + i >= rows) return;
+    // code 0 is 2^-127, a subnormal; 255 reads as NaN
+    const float s = b[i] == kMxNan ? __uint_as_float(0x7FC00000u)
+                                   : (b[i] == 0 ? __uint_as_float(0x00400000u) : scale_f32(b[i]));
     float f[kEach];
-    const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0);
-    const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1);
+    const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 0);
+    const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 1);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       f[j] = p0[j] * s;
@@ -124,8 +135,8 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restri
     }
     u32x4 o;
     if constexpr (kEach == 8) {
-      const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 2);
-      const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 3);
+      const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 2);
+      const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 3);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         f[4 + j] = p2[j] * s;
@@ -140,40 +151,26 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* __restri
       o = u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                 __float_as_uint(f[3])};
     }
-    __builtin_nontemporal_store(o, x + i);  // a stream: 45 against 84 us for 4226 x 16384 fp32
+    // a stream, past the caches: 44 against 58 us for 4226 x 16384 fp32
+    __builtin_nontemporal_store(o, x + ((r0 + i) * cols + c) / kEach);
   }
 }
 
 template <typename T>
-void launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
-                       void* x, hipStream_t stream) {
-  const int64_t pieces = rows * (cols / (16 / (int)sizeof(T)));
-  int64_t blocks = (pieces + 255) / 256;
-  if (blocks > kMaxStrideBlocks) blocks = kMaxStrideBlocks;  // the loop strides over the rest
-  u32x4* const o = reinterpret_cast<u32x4*>(x);
-  if (pieces <= ((int64_t)1 << 31))  // an index past the end stays below 2^32
-    hipLaunchKernelGGL((dequantize_kernel<T, uint32_t>), dim3((unsigned)blocks), dim3(256), 0,
-                       stream, codes, scales, rows, cols, pieces, o);
-  else
-    hipLaunchKernelGGL((dequantize_kernel<T, uint64_t>), dim3((unsigned)blocks), dim3(256), 0,
-                       stream, codes, scales, rows, cols, pieces, o);
+hipError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
+                             void* x, hipStream_t stream) {
+  const int64_t blocks = dequantize_blocks(rows, cols, sizeof(T));
+  hipLaunchKernelGGL((dequantize_kernel<T>), dim3((unsigned)blocks), dim3(kQWaves * kWave), 0,
+                     stream, codes, scales, rows, cols, reinterpret_cast<u32x4*>(x));
+  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_quantize(const void* x, int64_t rows, int cols, uint8_t* codes, uint8_t* scales,
                            hipStream_t stream) {
-  const unsigned tiles = (unsigned)((cols + kQCols - 1) / kQCols);
-  uint32_t* const c = reinterpret_cast<uint32_t*>(codes);
-  uint32_t* const s = reinterpret_cast<uint32_t*>(scales);
-  const T* const in = reinterpret_cast<const T*>(x);
-  if (quantize_rows(rows, cols) == kQuantRows)
-    hipLaunchKernelGGL((quantize_kernel<T, kQuantRows>),
-                       dim3((unsigned)((rows + kQuantRows - 1) / kQuantRows), tiles),
-                       dim3(kQWaves * kWave), 0, stream, in, rows, cols, c, s);
-  else
-    hipLaunchKernelGGL((quantize_kernel<T, kQuantFewRows>),
-                       dim3((unsigned)((rows + kQuantFewRows - 1) / kQuantFewRows), tiles),
-                       dim3(kQWaves * kWave), 0, stream, in, rows, cols, c, s);
+  hipLaunchKernelGGL((quantize_kernel<T>), dim3((unsigned)quantize_blocks(rows, cols)),
+                     dim3(kQWaves * kWave), 0, stream, reinterpret_cast<const T*>(x), rows, cols,
+                     reinterpret_cast<uint32_t*>(codes), reinterpret_cast<uint32_t*>(scales));
   return hipGetLastError();
 }
 
@@ -187,11 +184,8 @@ hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t rows, int cols,
 
 hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype,
                                  int64_t rows, int cols, void* x, hipStream_t stream) {
-  if (dtype == 1)
-    launch_dequantize<uint16_t>(codes, scales, rows, cols, x, stream);
-  else
-    launch_dequantize<float>(codes, scales, rows, cols, x, stream);
-  return hipGetLastError();
+  return dtype == 1 ? launch_dequantize<uint16_t>(codes, scales, rows, cols, x, stream)
+                    : launch_dequantize<float>(codes, scales, rows, cols, x, stream);
 }
 
 }  // namespace sdm

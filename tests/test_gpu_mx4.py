@@ -58,7 +58,7 @@ def _inputs(rows, cols, seed, dtype):
 
 
 SHAPES = [(1, 128), (3, 128), (4, 512), (5, 640), (33, 384), (130, 1152),
-          (2049, 4224)]  # the last: 129 x 9 tiles of 16 rows
+          (2049, 4224)]  # the last: 257 x 9 tiles of 8 rows
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)

@@ -32,7 +32,7 @@ def test_mx4_entry_points():
         (4, None, 1, "codes"), (4, FAKE + 8, 1, "16-byte"), (5, None, 1, "scales"),
         (5, FAKE + 2, 1, "4-byte")])
     assert L.sdm_mx4_quantize(None, 0, 0, 256, None, None, None) == 0
-    # one tile of 512 columns per 16 rows: 2^24 - 1 tiles is the largest grid
+    # one tile of 512 columns per 8 rows: 2^24 - 1 tiles is the largest grid
     assert L.sdm_mx4_quantize(FAKE, 0, 1 << 30, 512, FAKE, FAKE, None) == 2 and "tiles" in _err()
     ok = (FAKE, FAKE, 0, 10, 256, FAKE, None)  # codes, scales, dtype, rows, cols, x, stream
     _each(L.sdm_mx4_dequantize, ok, [
@@ -40,6 +40,8 @@ def test_mx4_entry_points():
         (3, -1, 1, "rows"), (4, 64, 2, "multiple of 128"), (5, None, 1, "x is NULL"),
         (5, FAKE + 2, 1, "16-byte")])
     assert L.sdm_mx4_dequantize(None, None, 1, 0, 128, None, None) == 0
+    # fp32 is written in tiles of half as many columns
+    assert L.sdm_mx4_dequantize(FAKE, FAKE, 0, 1 << 27, 384, FAKE, None) == 2 and "256" in _err()
 
 
 def test_project_mx4_entry_point():
