@@ -56,6 +56,8 @@
 // range (loads return zero, stores are dropped), which keeps the compiler's
 // count of outstanding loads exact, so the prefetch survives.
 // The two waves meet at one workgroup barrier per chunk.
+#include <type_traits>
+
 #include "device_common.h"
 #include "internal.h"
 #include "mx.h"
@@ -342,7 +344,99 @@ struct Producer {
 // ---------------------------------------------------------------- consumer
 
 // What the training forward keeps of the rows a step uses.
-enum { kSaveNone = 0, kSaveRows = 1, kSave8 = 2 };
+// kKeep8: as kSave8, by a wavefront of its own.
+enum { kSaveNone = 0, kSaveRows = 1, kSave8 = 2, kKeep8 = 3 };
+
+// The 8-bit tape (kSave8): 64 row slots' tile rows as blocks of 16 columns
+// (mx.h, 8-bit form).
+template <int COLS>
+struct Keep8 {
+  static constexpr int NI = Tile<float, COLS>::NI, LPR = Tile<float, COLS>::LPR,
+                       RPI = Tile<float, COLS>::RPI;
+
+  __amdgpu_buffer_rsrc_t tres;  // this memory's codes
+  __amdgpu_buffer_rsrc_t sres;  // its scale bytes
+  uint32_t block0;              // row records before the tile's first 16-column block
+  uint32_t block_rows;          // row records of one block, T * (W + R)
+  uint32_t step_rows;           // W + R
+  uint32_t writes;              // W
+
+  // descriptor ranges from ranges.h (checked on the host before the launch)
+  __device__ __forceinline__ void init(const ScanArgs& A, int mem, int tile) {
+    const int64_t recs = (int64_t)(A.d_v / 16) * A.T * (A.W + A.R);  // row records of one memory
+    step_rows = (uint32_t)(A.W + A.R);
+    writes = (uint32_t)A.W;
+    block_rows = (uint32_t)(A.T * (A.W + A.R));
+    block0 = (uint32_t)(tile * (COLS / 16)) * block_rows;
+    tres = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<uint8_t*>(A.tape) + (int64_t)mem * recs * 16, 0,
+        (int)ranges::table_range(recs, 16, 0, 16), kBufWord3);
+    sres = __builtin_amdgcn_make_buffer_rsrc(A.tape_scale + (int64_t)mem * recs, 0, (int)recs,
+                                             kBufWord3);
+  }
+
+  // The four lanes of a quad hold one block of a row; the scale comes from all
+  // four, each packs its four codes into a word, and they exchange words so
+  // that lane q of the quad ends with the whole records (16 code bytes and the
+  // scale byte) of row slots (4 g + q) * RPI + lr: one 16-byte and one 1-byte
+  // store per lane and 4 RPI rows, whose lanes write neighbouring records.
+  // ofs: the slots' state offsets (out of range: not kept); row0: the step's
+  // first record of these rows in a block.
+  __device__ __forceinline__ void rows(const u32x4v (&x)[NI], const uint32_t (&ofs)[NI],
+                                       uint32_t row0) const {
+    const int lane = lane_id(), q = lane & 3, lr = lane / LPR;
+    const uint32_t block = block0 + (uint32_t)((lane % LPR) / 4) * block_rows;
+    const bool odd = q & 1, high = q & 2;
+#pragma unroll
+    for (int g = 0; g < NI / 4; ++g) {
+      // maxima: folded over the quad so that lane q ends with slot q's, and its
+      // scale is found once
+      uint32_t m[4], at = kOffNone;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = 4 * g + i;
+        m[i] = max_mag4(x[k]);
+        at = q == i ? ofs[k] : at;
+      }
+      const uint32_t m01 = umax(odd ? m[1] : m[0], dpp_qp_xor1(odd ? m[0] : m[1]));
+      const uint32_t m23 = umax(odd ? m[3] : m[2], dpp_qp_xor1(odd ? m[2] : m[3]));
+      const uint32_t sc = int8_scale(umax(high ? m23 : m01, dpp_qp_xor2(high ? m01 : m23)));
+      const uint32_t inv = int8_inverse(sc);
+      uint32_t w[4] = {
+          int8_pack4(x[4 * g], __uint_as_float(dpp_mov<0x00>(inv))),
+          int8_pack4(x[4 * g + 1], __uint_as_float(dpp_mov<0x55>(inv))),
+          int8_pack4(x[4 * g + 2], __uint_as_float(dpp_mov<0xAA>(inv))),
+          int8_pack4(x[4 * g + 3], __uint_as_float(dpp_mov<0xFF>(inv)))};
+      quad_transpose(w);
+      const uint32_t rec = block + row0 + (uint32_t)((4 * g + q) * RPI + lr);
+      const bool none = at >= kOffNone;
+      if (sc == kMxNan) w[0] = w[1] = w[2] = w[3] = 0u;
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4v{w[0], w[1], w[2], w[3]}, tres,
+                                             none ? kOffNone : rec * 16u, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)sc, sres, none ? kOffNone : rec, 0, 0);
+    }
+  }
+};
+
+// The rows of a few steps on their way from the consumer to the keeper.
+constexpr int kKeepRing = 4;
+template <int COLS>
+struct KeepRing {
+  uint4 rows[kKeepRing][2][Tile<float, COLS>::NI][kWave];  // write rows, read rows, as the lanes hold them
+  uint32_t head, tail;  // steps written here, steps taken from here
+};
+
+// A word that the other wavefront writes.  A wavefront's LDS accesses are done
+// in their order, so rows stored before the word are there when it is.
+__device__ __forceinline__ uint32_t keep_peek(const uint32_t& w) {
+  const uint32_t x = __hip_atomic_load(&w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  asm volatile("" ::: "memory");
+  return x;
+}
+__device__ __forceinline__ void keep_post(uint32_t& w, uint32_t x) {
+  asm volatile("" ::: "memory");
+  __hip_atomic_store(&w, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
 
 template <typename DT, int COLS, int D, int SAVE>
 struct Consumer {
@@ -355,14 +449,12 @@ struct Consumer {
   u32x4v wv[D + 1][NI];
   u32x4v rv[D + 1][NI];
   __amdgpu_buffer_rsrc_t mres;  // this memory's tile column, range = the memory slice
-  __amdgpu_buffer_rsrc_t tres;  // SAVE: this memory's tape slice, shifted to the tile column
-  __amdgpu_buffer_rsrc_t sres;  // kSave8: this memory's scale bytes
-  uint32_t block0;               // kSave8: row records before the tile's first 16-column block
-  uint32_t block_rows;           // kSave8: row records of one block, T * (W + R)
-  uint32_t step_rows;            // kSave8: W + R
-  uint32_t tape_step;            // SAVE: bytes of one step's W + R tape rows
-  uint32_t read_base;            // SAVE: bytes (kSave8: records) before a step's first read row
-  uint32_t row_bytes;            // SAVE: bytes of one full row
+  __amdgpu_buffer_rsrc_t tres;  // kSaveRows: this memory's tape slice, shifted to the tile column
+  Keep8<COLS> k8;               // kSave8
+  KeepRing<COLS>* ring;         // kKeep8
+  uint32_t tape_step;            // kSaveRows: bytes of one step's W + R tape rows
+  uint32_t read_base;            // kSaveRows: bytes before a step's first read row (W rows)
+  uint32_t row_bytes;            // kSaveRows: bytes of one full row
   uint32_t lane_off;             // lc * 16
   bool accumulate;               // rows split over two workgroups: add into out
 
@@ -429,47 +521,10 @@ struct Consumer {
     }
   }
 
-  // The 8-bit tape (kSave8): 64 row slots' tile rows as blocks of 16 columns
-  // (mx.h, 8-bit form).  The four lanes of a quad hold one block of a row;
-  // the scale comes from all four, each packs its four codes into a word, and
-  // exchange words so that lane q of the quad ends with the whole records
-  // (16 code bytes and the scale byte) of row slots (4 g + q) * RPI + lr: one
-  // 16-byte and one 1-byte store per lane and 4 RPI rows, whose lanes write
-  // neighbouring records.  ofs: the slots' state offsets (out of range: not
-  // kept); row0: the step's first record of these rows in a block.
-  __device__ __forceinline__ void keep8(const u32x4v (&rows)[NI], const uint32_t (&ofs)[NI],
-                                        uint32_t row0) const {
-    const int lane = lane_id(), q = lane & 3, lr = lane / LPR;
-    const uint32_t block = block0 + (uint32_t)((lane % LPR) / 4) * block_rows;
-    const bool odd = q & 1, high = q & 2;
+  __device__ __forceinline__ void hand_over(const u32x4v (&rows)[NI], int part, int64_t u) const {
+    uint4(&to)[NI][kWave] = ring->rows[u % kKeepRing][part];
 #pragma unroll
-    for (int g = 0; g < NI / 4; ++g) {
-      // maxima: folded over the quad so that lane q ends with slot q's, and its
-      // scale is found once
-      uint32_t m[4], at = kOffNone;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = 4 * g + i;
-        m[i] = max_mag4(rows[k]);
-        at = q == i ? ofs[k] : at;
-      }
-      const uint32_t m01 = umax(odd ? m[1] : m[0], dpp_qp_xor1(odd ? m[0] : m[1]));
-      const uint32_t m23 = umax(odd ? m[3] : m[2], dpp_qp_xor1(odd ? m[2] : m[3]));
-      const uint32_t sc = int8_scale(umax(high ? m23 : m01, dpp_qp_xor2(high ? m01 : m23)));
-      const uint32_t inv = int8_inverse(sc);
-      uint32_t w[4] = {
-          int8_pack4(rows[4 * g], __uint_as_float(dpp_mov<0x00>(inv))),
-          int8_pack4(rows[4 * g + 1], __uint_as_float(dpp_mov<0x55>(inv))),
-          int8_pack4(rows[4 * g + 2], __uint_as_float(dpp_mov<0xAA>(inv))),
-          int8_pack4(rows[4 * g + 3], __uint_as_float(dpp_mov<0xFF>(inv)))};
-      quad_transpose(w);
-      const uint32_t rec = block + row0 + (uint32_t)((4 * g + q) * RPI + lr);
-      const bool none = at >= kOffNone;
-      if (sc == kMxNan) w[0] = w[1] = w[2] = w[3] = 0u;
-      __builtin_amdgcn_raw_buffer_store_b128(u32x4v{w[0], w[1], w[2], w[3]}, tres,
-                                             none ? kOffNone : rec * 16u, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)sc, sres, none ? kOffNone : rec, 0, 0);
-    }
+    for (int k = 0; k < NI; ++k) to[k][lane_id()] = make_uint4(rows[k].x, rows[k].y, rows[k].z, rows[k].w);
   }
 
   template <int SLOT>
@@ -490,6 +545,8 @@ struct Consumer {
     const float a = __uint_as_float(p.sc[kScAlpha]), b = __uint_as_float(p.sc[kScBeta]);
     const uint32_t fwd = p.sc[kScFwd];
     const uint64_t save = p.wsave;
+    uint32_t tail = 0;
+    if constexpr (SAVE == kKeep8) tail = keep_peek(ring->tail);
     if (fwd) {  // rare: take forwarded rows from the ring
 #pragma unroll
       for (int k = 0; k < NI; ++k) {
@@ -497,7 +554,14 @@ struct Consumer {
         if (src) wv[SLOT][k] = lds_u4(sh.upd[(src - 1) >> 6][((src - 1) & 63) * LPR + lc]);
       }
     }
-    if constexpr (SAVE == kSave8) keep8(wv[SLOT], wo, (uint32_t)u * step_rows);
+    if constexpr (SAVE == kSave8) k8.rows(wv[SLOT], wo, (uint32_t)u * k8.step_rows);
+    if constexpr (SAVE == kKeep8) {
+      while (tail + kKeepRing <= (uint32_t)u) {  // the keeper still holds the slot
+        __builtin_amdgcn_s_sleep(1);
+        tail = keep_peek(ring->tail);
+      }
+      hand_over(wv[SLOT], 0, u);
+    }
     if constexpr (SAVE == kSaveRows) {  // the pre-write rows, as stored, for the reverse pass
 #pragma unroll
       for (int k = 0; k < NI; ++k) {
@@ -548,7 +612,11 @@ struct Consumer {
       uint32_t ro[NI];
 #pragma unroll
       for (int k = 0; k < NI; ++k) ro[k] = p.rofs[lr * NI + k];
-      keep8(rv[SLOT], ro, (uint32_t)u * step_rows + read_base);
+      k8.rows(rv[SLOT], ro, (uint32_t)u * k8.step_rows + k8.writes);
+    }
+    if constexpr (SAVE == kKeep8) {
+      hand_over(rv[SLOT], 1, u);
+      keep_post(ring->head, (uint32_t)u + 1);
     }
     if constexpr (SAVE == kSaveRows) {  // the rows the read uses, for the reverse pass
 #pragma unroll
@@ -627,9 +695,11 @@ struct Consumer {
 };
 
 template <typename DT, int COLS, int D, int SAVE>
-__global__ __launch_bounds__(2 * kWave) void scan_kernel(DT* __restrict__ M, ScanArgs A) {
+__global__ __launch_bounds__((SAVE == kKeep8 ? 3 : 2) * kWave) void scan_kernel(DT* __restrict__ M,
+                                                                               ScanArgs A) {
   using TL = Tile<DT, COLS>;
   __shared__ ScanShared<DT, COLS, D> sh;
+  __shared__ std::conditional_t<SAVE == kKeep8, KeepRing<COLS>, char> ring;
 
   // XCD-aware numbering: bid = (((g * shards) + shard) * ntiles + tile) * 8 + x,
   // memory = g*8 + x, so every tile and shard of a memory shares one XCD's L2.
@@ -672,6 +742,40 @@ __global__ __launch_bounds__(2 * kWave) void scan_kernel(DT* __restrict__ M, Sca
     return;
   }
 
+  if constexpr (SAVE == kKeep8) {
+    // keeper: the tape of step u from the rows the consumer hands over.  It
+    // meets each chunk's barrier before the chunk's last step, so that nobody
+    // waits for that step's tape; its plan entries, which the producer may
+    // replace after the barrier, are read before.
+    if (wave == 2) {
+      const int lr = lane / TL::LPR;
+      Keep8<COLS> k8;
+      k8.init(A, mem, tile);
+      if (lane == 0) ring.head = ring.tail = 0;
+      __syncthreads();
+      for (uint32_t u = 0; u < (uint32_t)T; ++u) {
+        const StepPlan<COLS>& p = sh.plan[u / kChunk % kNBuf][u % kChunk];
+        uint32_t wo[TL::NI], ro[TL::NI];
+#pragma unroll
+        for (int k = 0; k < TL::NI; ++k) {
+          wo[k] = p.wofs[lr * TL::NI + k];
+          ro[k] = p.rofs[lr * TL::NI + k];
+        }
+        if (u % kChunk == kChunk - 1 || u == (uint32_t)T - 1) __syncthreads();
+        while (keep_peek(ring.head) <= u) __builtin_amdgcn_s_sleep(1);
+        u32x4v w[TL::NI], r[TL::NI];
+#pragma unroll
+        for (int k = 0; k < TL::NI; ++k) w[k] = lds_u4(ring.rows[u % kKeepRing][0][k][lane]);
+#pragma unroll
+        for (int k = 0; k < TL::NI; ++k) r[k] = lds_u4(ring.rows[u % kKeepRing][1][k][lane]);
+        keep_post(ring.tail, u + 1);
+        k8.rows(w, wo, u * k8.step_rows);
+        k8.rows(r, ro, u * k8.step_rows + k8.writes);
+      }
+      return;
+    }
+  }
+
   // consumer
   const int lr = lane / TL::LPR;
   const int lc = lane % TL::LPR;
@@ -683,18 +787,8 @@ __global__ __launch_bounds__(2 * kWave) void scan_kernel(DT* __restrict__ M, Sca
   cs.accumulate = A.shards > 1;
   // descriptor ranges from ranges.h (checked on the host before the launch)
   const int64_t row_bytes = (int64_t)d_v * (int64_t)sizeof(DT);
-  if constexpr (SAVE == kSave8) {
-    const int64_t recs = (int64_t)(d_v / 16) * T * (A.W + A.R);  // row records of one memory
-    cs.step_rows = (uint32_t)(A.W + A.R);
-    cs.read_base = (uint32_t)A.W;
-    cs.block_rows = (uint32_t)(T * (A.W + A.R));
-    cs.block0 = (uint32_t)(tile * (COLS / 16)) * cs.block_rows;
-    cs.tres = __builtin_amdgcn_make_buffer_rsrc(
-        reinterpret_cast<uint8_t*>(A.tape) + (int64_t)mem * recs * 16, 0,
-        (int)ranges::table_range(recs, 16, 0, 16), kBufWord3);
-    cs.sres = __builtin_amdgcn_make_buffer_rsrc(A.tape_scale + (int64_t)mem * recs, 0, (int)recs,
-                                                kBufWord3);
-  }
+  if constexpr (SAVE == kSave8) cs.k8.init(A, mem, tile);
+  if constexpr (SAVE == kKeep8) cs.ring = &ring;
   if constexpr (SAVE == kSaveRows) {
     const int64_t tape_rows = T * (A.W + A.R);  // rows of one memory's tape
     cs.tape_step = (uint32_t)((A.W + A.R) * row_bytes);
@@ -727,7 +821,7 @@ hipError_t launch(void* M, ScanArgs A, hipStream_t stream) {
   A.ntiles = A.d_v / COLS;
   if (!ranges::scan_tiles_ok(A.N, A.d_v, (int)sizeof(DT), A.T, A.W, A.R, COLS,
                              SAVE == kSaveRows) ||
-      (SAVE == kSave8 && !ranges::tape8_ok(A.d_v, A.T, A.W, A.R)))
+      (SAVE >= kSave8 && !ranges::tape8_ok(A.d_v, A.T, A.W, A.R)))
     return hipErrorInvalidValue;  // never taken: the C-ABI layer checked every tile width
   const int groups = (A.n_mem + 7) / 8;
   const int64_t blocks = (int64_t)groups * A.shards * A.ntiles * 8;
@@ -737,8 +831,8 @@ hipError_t launch(void* M, ScanArgs A, hipStream_t stream) {
     hipLaunchKernelGGL(zero_kernel, dim3((unsigned)zb), dim3(256), 0, stream,
                        reinterpret_cast<float4*>(A.out), n4);
   }
-  hipLaunchKernelGGL((scan_kernel<DT, COLS, D, SAVE>), dim3((unsigned)blocks), dim3(2 * kWave), 0,
-                     stream, reinterpret_cast<DT*>(M), A);
+  hipLaunchKernelGGL((scan_kernel<DT, COLS, D, SAVE>), dim3((unsigned)blocks),
+                     dim3((SAVE == kKeep8 ? 3 : 2) * kWave), 0, stream, reinterpret_cast<DT*>(M), A);
   return hipGetLastError();
 }
 
@@ -814,9 +908,9 @@ hipError_t launch_scan_train8(float* M, int B, int H, int64_t N, int d_v, int64_
   if (!narrow) return launch<float, 32, 1, kSave8>(M, A, stream);
   if (2 * (int64_t)A.n_mem * (d_v / 16) <= cus) {
     A.shards = 2;
-    return launch<float, 16, 3, kSave8>(M, A, stream);
+    return launch<float, 16, 3, kKeep8>(M, A, stream);
   }
-  return launch<float, 16, 2, kSave8>(M, A, stream);
+  return launch<float, 16, 2, kKeep8>(M, A, stream);
 }
 
 }  // namespace sdm
