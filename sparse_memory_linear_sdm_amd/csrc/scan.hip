@@ -56,6 +56,14 @@
 // range (loads return zero, stores are dropped), which keeps the compiler's
 // count of outstanding loads exact, so the prefetch survives.
 // The two waves meet at one workgroup barrier per chunk.
+//
+// The 8-bit tape (sdm_scan_train8) has a third wavefront, the keeper: the
+// consumer hands it each step's rows through an LDS ring of a few steps, and it
+// finds the scales, packs the codes and stores them.  With the packing among
+// the consumer's own instructions 4 memories x 301 steps took 299 us, so 233
+// (185 without a tape); 16 memories x 512 steps 511, so 386 (305); 45 memories
+// x 256 steps 435, so 354 (268); 64 memories x 1024 steps, bound by the
+// memory's traffic, 1.64 and 1.63 ms (1.37), 4.7 TB/s.
 #include <type_traits>
 
 #include "device_common.h"
@@ -344,8 +352,7 @@ struct Producer {
 // ---------------------------------------------------------------- consumer
 
 // What the training forward keeps of the rows a step uses.
-// kKeep8: as kSave8, by a wavefront of its own.
-enum { kSaveNone = 0, kSaveRows = 1, kSave8 = 2, kKeep8 = 3 };
+enum { kSaveNone = 0, kSaveRows = 1, kSave8 = 2 };
 
 // The 8-bit tape (kSave8): 64 row slots' tile rows as blocks of 16 columns
 // (mx.h, 8-bit form).
@@ -419,10 +426,10 @@ struct Keep8 {
 };
 
 // The rows of a few steps on their way from the consumer to the keeper.
-constexpr int kKeepRing = 4;
 template <int COLS>
 struct KeepRing {
-  uint4 rows[kKeepRing][2][Tile<float, COLS>::NI][kWave];  // write rows, read rows, as the lanes hold them
+  static constexpr int kSteps = COLS == 16 ? 4 : 3;  // what LDS has room for
+  uint4 rows[kSteps][2][Tile<float, COLS>::NI][kWave];  // write rows, read rows, as the lanes hold them
   uint32_t head, tail;  // steps written here, steps taken from here
 };
 
@@ -442,16 +449,14 @@ template <typename DT, int COLS, int D, int SAVE>
 struct Consumer {
   using TL = Tile<DT, COLS>;
   static constexpr int NI = TL::NI, EPL = TL::EPL, LPR = TL::LPR, RPI = TL::RPI;
-  // stores of a step: the write rows, and with a tape the W and R rows kept
-  // (8 bits: a code and a scale store per 4 instructions' rows of each)
-  static constexpr int kStores = SAVE == kSaveRows ? 3 * NI : SAVE == kSave8 ? 2 * NI : NI;
+  // stores of a step: the write rows, and with an fp32 tape the W and R rows kept
+  static constexpr int kStores = SAVE == kSaveRows ? 3 * NI : NI;
 
   u32x4v wv[D + 1][NI];
   u32x4v rv[D + 1][NI];
   __amdgpu_buffer_rsrc_t mres;  // this memory's tile column, range = the memory slice
   __amdgpu_buffer_rsrc_t tres;  // kSaveRows: this memory's tape slice, shifted to the tile column
-  Keep8<COLS> k8;               // kSave8
-  KeepRing<COLS>* ring;         // kKeep8
+  KeepRing<COLS>* ring;          // kSave8
   uint32_t tape_step;            // kSaveRows: bytes of one step's W + R tape rows
   uint32_t read_base;            // kSaveRows: bytes before a step's first read row (W rows)
   uint32_t row_bytes;            // kSaveRows: bytes of one full row
@@ -522,7 +527,7 @@ struct Consumer {
   }
 
   __device__ __forceinline__ void hand_over(const u32x4v (&rows)[NI], int part, int64_t u) const {
-    uint4(&to)[NI][kWave] = ring->rows[u % kKeepRing][part];
+    uint4(&to)[NI][kWave] = ring->rows[(uint32_t)u % KeepRing<COLS>::kSteps][part];
 #pragma unroll
     for (int k = 0; k < NI; ++k) to[k][lane_id()] = make_uint4(rows[k].x, rows[k].y, rows[k].z, rows[k].w);
   }
@@ -546,7 +551,7 @@ struct Consumer {
     const uint32_t fwd = p.sc[kScFwd];
     const uint64_t save = p.wsave;
     uint32_t tail = 0;
-    if constexpr (SAVE == kKeep8) tail = keep_peek(ring->tail);
+    if constexpr (SAVE == kSave8) tail = keep_peek(ring->tail);
     if (fwd) {  // rare: take forwarded rows from the ring
 #pragma unroll
       for (int k = 0; k < NI; ++k) {
@@ -554,9 +559,8 @@ struct Consumer {
         if (src) wv[SLOT][k] = lds_u4(sh.upd[(src - 1) >> 6][((src - 1) & 63) * LPR + lc]);
       }
     }
-    if constexpr (SAVE == kSave8) k8.rows(wv[SLOT], wo, (uint32_t)u * k8.step_rows);
-    if constexpr (SAVE == kKeep8) {
-      while (tail + kKeepRing <= (uint32_t)u) {  // the keeper still holds the slot
+    if constexpr (SAVE == kSave8) {
+      while (tail + KeepRing<COLS>::kSteps <= (uint32_t)u) {  // the keeper still holds the slot
         __builtin_amdgcn_s_sleep(1);
         tail = keep_peek(ring->tail);
       }
@@ -609,12 +613,6 @@ struct Consumer {
       }
     }
     if constexpr (SAVE == kSave8) {
-      uint32_t ro[NI];
-#pragma unroll
-      for (int k = 0; k < NI; ++k) ro[k] = p.rofs[lr * NI + k];
-      k8.rows(rv[SLOT], ro, (uint32_t)u * k8.step_rows + k8.writes);
-    }
-    if constexpr (SAVE == kKeep8) {
       hand_over(rv[SLOT], 1, u);
       keep_post(ring->head, (uint32_t)u + 1);
     }
@@ -695,11 +693,11 @@ struct Consumer {
 };
 
 template <typename DT, int COLS, int D, int SAVE>
-__global__ __launch_bounds__((SAVE == kKeep8 ? 3 : 2) * kWave) void scan_kernel(DT* __restrict__ M,
+__global__ __launch_bounds__((SAVE == kSave8 ? 3 : 2) * kWave) void scan_kernel(DT* __restrict__ M,
                                                                                ScanArgs A) {
   using TL = Tile<DT, COLS>;
   __shared__ ScanShared<DT, COLS, D> sh;
-  __shared__ std::conditional_t<SAVE == kKeep8, KeepRing<COLS>, char> ring;
+  __shared__ std::conditional_t<SAVE == kSave8, KeepRing<COLS>, char> ring;
 
   // XCD-aware numbering: bid = (((g * shards) + shard) * ntiles + tile) * 8 + x,
   // memory = g*8 + x, so every tile and shard of a memory shares one XCD's L2.
@@ -742,7 +740,7 @@ __global__ __launch_bounds__((SAVE == kKeep8 ? 3 : 2) * kWave) void scan_kernel(
     return;
   }
 
-  if constexpr (SAVE == kKeep8) {
+  if constexpr (SAVE == kSave8) {
     // keeper: the tape of step u from the rows the consumer hands over.  It
     // meets each chunk's barrier before the chunk's last step, so that nobody
     // waits for that step's tape; its plan entries, which the producer may
@@ -765,9 +763,9 @@ __global__ __launch_bounds__((SAVE == kKeep8 ? 3 : 2) * kWave) void scan_kernel(
         while (keep_peek(ring.head) <= u) __builtin_amdgcn_s_sleep(1);
         u32x4v w[TL::NI], r[TL::NI];
 #pragma unroll
-        for (int k = 0; k < TL::NI; ++k) w[k] = lds_u4(ring.rows[u % kKeepRing][0][k][lane]);
+        for (int k = 0; k < TL::NI; ++k) w[k] = lds_u4(ring.rows[u % KeepRing<COLS>::kSteps][0][k][lane]);
 #pragma unroll
-        for (int k = 0; k < TL::NI; ++k) r[k] = lds_u4(ring.rows[u % kKeepRing][1][k][lane]);
+        for (int k = 0; k < TL::NI; ++k) r[k] = lds_u4(ring.rows[u % KeepRing<COLS>::kSteps][1][k][lane]);
         keep_post(ring.tail, u + 1);
         k8.rows(w, wo, u * k8.step_rows);
         k8.rows(r, ro, u * k8.step_rows + k8.writes);
@@ -787,8 +785,7 @@ __global__ __launch_bounds__((SAVE == kKeep8 ? 3 : 2) * kWave) void scan_kernel(
   cs.accumulate = A.shards > 1;
   // descriptor ranges from ranges.h (checked on the host before the launch)
   const int64_t row_bytes = (int64_t)d_v * (int64_t)sizeof(DT);
-  if constexpr (SAVE == kSave8) cs.k8.init(A, mem, tile);
-  if constexpr (SAVE == kKeep8) cs.ring = &ring;
+  if constexpr (SAVE == kSave8) cs.ring = &ring;
   if constexpr (SAVE == kSaveRows) {
     const int64_t tape_rows = T * (A.W + A.R);  // rows of one memory's tape
     cs.tape_step = (uint32_t)((A.W + A.R) * row_bytes);
@@ -821,7 +818,7 @@ hipError_t launch(void* M, ScanArgs A, hipStream_t stream) {
   A.ntiles = A.d_v / COLS;
   if (!ranges::scan_tiles_ok(A.N, A.d_v, (int)sizeof(DT), A.T, A.W, A.R, COLS,
                              SAVE == kSaveRows) ||
-      (SAVE >= kSave8 && !ranges::tape8_ok(A.d_v, A.T, A.W, A.R)))
+      (SAVE == kSave8 && !ranges::tape8_ok(A.d_v, A.T, A.W, A.R)))
     return hipErrorInvalidValue;  // never taken: the C-ABI layer checked every tile width
   const int groups = (A.n_mem + 7) / 8;
   const int64_t blocks = (int64_t)groups * A.shards * A.ntiles * 8;
@@ -832,7 +829,7 @@ hipError_t launch(void* M, ScanArgs A, hipStream_t stream) {
                        reinterpret_cast<float4*>(A.out), n4);
   }
   hipLaunchKernelGGL((scan_kernel<DT, COLS, D, SAVE>), dim3((unsigned)blocks),
-                     dim3((SAVE == kKeep8 ? 3 : 2) * kWave), 0, stream, reinterpret_cast<DT*>(M), A);
+                     dim3((SAVE == kSave8 ? 3 : 2) * kWave), 0, stream, reinterpret_cast<DT*>(M), A);
   return hipGetLastError();
 }
 
@@ -908,9 +905,9 @@ hipError_t launch_scan_train8(float* M, int B, int H, int64_t N, int d_v, int64_
   if (!narrow) return launch<float, 32, 1, kSave8>(M, A, stream);
   if (2 * (int64_t)A.n_mem * (d_v / 16) <= cus) {
     A.shards = 2;
-    return launch<float, 16, 3, kKeep8>(M, A, stream);
+    return launch<float, 16, 3, kSave8>(M, A, stream);
   }
-  return launch<float, 16, 2, kKeep8>(M, A, stream);
+  return launch<float, 16, 2, kSave8>(M, A, stream);
 }
 
 }  // namespace sdm
