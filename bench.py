@@ -294,8 +294,8 @@ def run_prefill(cfg, args, torch, S, sdm):
     tokens_per_step = B * T
     slot_bytes = B * H * T * (2 * W + R) * d_v * es  # algorithmic, one scan launch
     scan_gbps = slot_bytes / (scan_ms * 1e-3) / 1e9
-    kname = {4: "scan_kernel<float,32,1,false>", 2: "scan_kernel<uint16_t(bf16),32,1,false>",
-             1: "scan_kernel<fp8e4m3,32,1,false>"}[es]
+    kname = {4: "scan_kernel<float,32,1,0>", 2: "scan_kernel<uint16_t(bf16),32,1,0>",
+             1: "scan_kernel<fp8e4m3,32,1,0>"}[es]
     traffic_file = {4: TRAFFIC_FILE, 2: BF16_TRAFFIC_FILE, 1: FP8_TRAFFIC_FILE}[es]
     traffic = measured_traffic(slot_bytes, traffic_file) if cfg.name == "mid" else None
     workload = (f"{cfg.name}: B{B} H{H} n{n} (N={N}) d_v{d_v} T{T} W={W} R={R} "
@@ -796,7 +796,7 @@ def run_long(cfg, args, torch, S, sdm):
                   "the shards' combine kernel of the same call)")
         traffic = measured_traffic(slot_bytes // nch, LONG_PLANNED_TRAFFIC_FILE, PLANNED_SOURCES)
     else:
-        kernel = ("scan_kernel<float,16,3,false>, two row shards (duration includes the output "
+        kernel = ("scan_kernel<float,16,3,0>, two row shards (duration includes the output "
                   "zero fill of the same call)")
         traffic = measured_traffic(slot_bytes // nch, LONG_TRAFFIC_FILE)
     roofline = {"bound": "hbm", "achieved": gbps, "peak": HBM_PEAK_GBPS, "unit": "GB/s",
