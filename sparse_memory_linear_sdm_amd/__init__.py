@@ -248,9 +248,9 @@ def _units(lead):
     return units
 
 
-def _project_out(B, T, H, P, n, weights, out, empty):
-    """The projections' 7 output tensors, made by empty(shape, dtype) unless
-    the caller gives them, and their checked arguments."""
+def _project_out(B, T, H, P, n, weights, out, stream, device):
+    """The projections' 7 output tensors, made unless the caller gives them,
+    and their checked arguments."""
     import torch
 
     f32 = torch.float32
@@ -258,10 +258,14 @@ def _project_out(B, T, H, P, n, weights, out, empty):
     if n < 1 or d_v < 1:
         raise ValueError(f"{weights} has P={P} rows per head: too few for n={n} "
                          "(P = 4n + d_v + 2)")
-    shapes = [(B, H, T, n)] * 4 + [(B, H, T, d_v), (B, H, T), (B, H, T)]
     names = ("s1", "s2", "q1", "q2", "v", "alpha", "beta")
     if out is None:
-        out = tuple(empty(sh, f32) for sh in shapes)
+        empty = _empty_on(stream, device)
+        s1, v, alpha = empty((B, H, T, n), f32), empty((B, H, T, d_v), f32), empty((B, H, T), f32)
+        like = torch.empty_like if stream is None else lambda t: empty(t.shape, f32)
+        out = (s1, like(s1), like(s1), like(s1), v, alpha, like(alpha))
+        return out, list(zip(names, out))
+    shapes = [(B, H, T, n)] * 4 + [(B, H, T, d_v), (B, H, T), (B, H, T)]
     if len(out) != 7:
         raise ValueError("out must hold 7 tensors (s1, s2, q1, q2, v, alpha, beta)")
     return tuple(out), [_arg(t, f32, sh, nm) for t, sh, nm in zip(out, shapes, names)]
@@ -280,7 +284,7 @@ def project(X, Wt, n: int, out=None, stream=None):
         raise ValueError("X must be [B, T, d_model] and Wt [H, P, d_model]")
     B, T, d_model = X.shape
     H, P = Wt.shape[0], Wt.shape[1]
-    out, outs = _project_out(B, T, H, P, n, "Wt", out, _empty_on(None, X.device))
+    out, outs = _project_out(B, T, H, P, n, "Wt", out, None, X.device)
     ptrs = _gpu(_arg(X, bf16, (B, T, d_model), "X"), _arg(Wt, bf16, (H, P, d_model), "Wt"), *outs)
     _check(lib().sdm_project(ptrs[0], ptrs[1], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[2:],
                              _stream(stream)))
@@ -321,9 +325,13 @@ def mx4_quantize(x, out=None, stream=None):
     rows, dtype = _units(lead), _value_dtype(x.dtype)
     if out is None:
         empty = _empty_on(stream, x.device)
-        out = (empty((*lead, cols // 2), torch.uint8), empty((cols // 128, rows, 4), torch.uint8))
-    codes, scales = out
-    px, pc, ps = _gpu(_arg(x, x.dtype, shape, "x"), *_mx4_args(codes, scales, shape))
+        codes = empty((*lead, cols // 2), torch.uint8)
+        scales = empty((cols // 128, rows, 4), torch.uint8)
+        outs = (("codes", codes), ("scales", scales))
+    else:
+        codes, scales = out
+        outs = _mx4_args(codes, scales, shape)
+    px, pc, ps = _gpu(_arg(x, x.dtype, shape, "x"), *outs)
     _call(lib().sdm_mx4_quantize, x, stream, px, dtype, rows, cols, pc, ps)
     return codes, scales
 
@@ -356,7 +364,7 @@ def project_mx4(Xq, Xs, Wq, Ws, n: int, out=None, stream=None):
     B, T, half = Xq.shape
     H, P = Wq.shape[0], Wq.shape[1]
     d_model = 2 * half
-    out, outs = _project_out(B, T, H, P, n, "Wq", out, _empty_on(stream, Xq.device))
+    out, outs = _project_out(B, T, H, P, n, "Wq", out, stream, Xq.device)
     ptrs = _gpu(*_mx4_args(Xq, Xs, (B, T, d_model), ("Xq", "Xs")),
                 *_mx4_args(Wq, Ws, (H, P, d_model), ("Wq", "Ws")), *outs)
     _call(lib().sdm_project_mx4, Xq, stream, *ptrs[:4], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[4:])
