@@ -163,7 +163,7 @@ def _gpu(*args):
     """Device pointers of checked arguments ((name, tensor) pairs from _arg,
     or None for an absent optional one): every tensor must be on the GPU, all
     on the same device."""
-    dev = None
+    dev = -1
     ptrs = []
     for a in args:
         if a is None:
@@ -172,10 +172,11 @@ def _gpu(*args):
         name, t = a
         if not t.is_cuda:
             raise ValueError(f"{name} must be on the GPU")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
+        at = t.get_device()
+        if at != dev:
+            if dev >= 0:
+                raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+            dev = at
         ptrs.append(t.data_ptr())
     return ptrs
 
