@@ -110,4 +110,51 @@ __device__ __forceinline__ void project_store_blocks(const ProjOut& A, const Pro
   }
 }
 
+// 64 tokens' values of a wavefront's 64 columns, one column a lane: token
+// row0 + r's at y[r * kWave ..] (the wavefront's own LDS; changed).
+__device__ __forceinline__ void project_store_rows(const ProjOut& A, const ProjColumn& c,
+                                                   int64_t row0, float* y) {
+  constexpr int kEach = 8;  // rows read together
+  const int rows = A.M - row0 < kWave ? (int)(A.M - row0) : kWave;
+  if (rows <= 0) return;
+  const int lane = lane_id();
+  // gate columns, one after the other with a token a lane: their few values a
+  // row would cost every row the logistic function's instructions
+  for (uint64_t m = __ballot(c.gate); m; m &= m - 1) {
+    float& g = y[lane * kWave + __builtin_ctzll(m)];
+    g = sigmoidf_(g);
+  }
+  wave_sync();
+  if (!c.dst) return;
+  // Which token comes next is the same for every lane, so an address is the
+  // last one plus the column's stride, and a step over the other heads at the
+  // end of a sequence.
+  const uint32_t T = (uint32_t)A.T;
+  uint32_t t = (uint32_t)row0 % T;
+  const bool whole = rows == kWave && t + kWave <= T;  // all of one sequence
+  const int64_t over = (int64_t)(A.H - 1) * A.T * c.stride;
+  float* p = c.dst + (project_token(A, (uint32_t)row0) + (int64_t)c.h * A.T) * c.stride + c.off;
+#pragma unroll 1
+  for (int r = 0; r < rows; r += kEach) {
+    float v[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) v[u] = y[(r + u) * kWave + lane];
+    if (whole) {
+#pragma unroll
+      for (int u = 0; u < kEach; ++u, p += c.stride) *p = v[u];
+      continue;
+    }
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      if (r + u >= rows) break;
+      *p = v[u];
+      p += c.stride;
+      if (++t == T) {
+        t = 0;
+        p += over;
+      }
+    }
+  }
+}
+
 }  // namespace sdm

@@ -183,10 +183,18 @@ PROJECT = [
     (65, 1, 128, 1, 16, 16), (2, 150, 384, 3, 64, 16), (1, 257, 256, 1, 37, 32),
     (300, 1, 640, 1, 8, 16), (37, 3, 128, 2, 16, 16), (2, 700, 1024, 1, 128, 128),
     (1, 300, 512, 2, 256, 64),
-    # 256 x 256 tiles (enough tokens and columns to fill the chip with them): one
-    # stage of K and several, ragged rows and columns, T = 1, 3, 4 and long
+    # tiles, of both sizes: one stage of K and several, ragged rows and columns,
+    # T = 1, 3, 4 and long, gates and array borders inside a wavefront's columns
     (300, 4, 640, 3, 333, 40), (1, 1025, 128, 4, 256, 66), (3, 401, 1152, 2, 512, 17),
     (1203, 1, 384, 1, 1024, 16), (401, 3, 256, 1, 1024, 16), (1, 2048, 512, 1, 1020, 14),
+    (130, 1, 8192, 1, 1024, 128), (9, 60, 8192, 1, 512, 64), (1, 640, 4096, 2, 256, 30),
+    (2, 1100, 1024, 7, 5, 3), (3000, 1, 128, 30, 1, 1), (60, 200, 128, 2, 64, 16),
+    (1, 2050, 4096, 2, 512, 64), (7, 117, 16384, 1, 512, 16), (7, 4681, 128, 1, 64, 16),
+    (3, 5461, 384, 1, 128, 20), (1, 16384, 128, 4, 30, 8), (777, 21, 256, 2, 64, 64),
+    # the few-token kernel's wide column blocks
+    (2, 7, 128, 8, 1024, 128), (3, 7, 384, 8, 1024, 128), (17, 1, 256, 4, 1024, 128),
+    (9, 2, 128, 1, 1024, 128), (21, 1, 128, 2, 1024, 128), (33, 1, 2048, 8, 1024, 128),
+    (5, 410, 1024, 1, 60, 30), (63, 1, 2176, 8, 1024, 128),
 ]
 
 
