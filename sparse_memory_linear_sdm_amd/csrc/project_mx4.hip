@@ -138,8 +138,8 @@ __global__ __launch_bounds__(X::kThreads) void project_mx4_kernel(Mx4Args A) {
 
   // Direct loads.  Codes: load q of wavefront w fills the 64 consecutive
   // 16-byte slots (q * kWaves + w) * 64 + lane; slot s is position s % 4 of row
-  // s / 4, whose swizzle is the same for every q.  Scales: thread i < 256
-  // (>= 256) loads token (column) i % 256's word.  Rows past the matrix read
+  // s / 4, whose swizzle is the same for every q.  Scales: thread i < BM
+  // (>= BM) loads token (column) i % BM's word.  Rows past the matrix read
   // its last row (their products land only in outputs that are never stored).
   // Offsets are from the tile's first row: 32 bits (256 rows of at most 32 KiB).
   const int nk = A.K / kXBK;

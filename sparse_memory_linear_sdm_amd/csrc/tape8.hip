@@ -5,7 +5,10 @@
 // the d_v/16 threads of a row are neighbours.  In bf16 a record is two 16-byte
 // pieces of the output: lanes 2m and 2m + 1 take records m and m + 32 of the
 // wavefront's 64 and swap halves, so that each of its two stores is 1 KiB in a
-// row and can pass the caches.
+// row and can pass the caches.  In fp32 it is four, and the lanes of a quad take
+// records 16 apart and exchange pieces, to the same end.  64 memories x 512
+// steps of 128 rows of 128 values: 475 us in fp32 (5.7 TB/s; 663 with a lane's
+// pieces stored as they lie), 300 us in bf16.
 #include "internal.h"
 #include "mx.h"
 
@@ -21,7 +24,7 @@ __global__ __launch_bounds__(256) void tape8_read_kernel(const u32x4* __restrict
   const int lane = lane_id();
   // whole wavefronts: the lanes past the end only take part in the exchange
   for (I i0 = (I)blockIdx.x * 256 + (threadIdx.x & ~63u); i0 < n; i0 += step) {
-    const I i = i0 + (sizeof(T) == 2 ? (lane >> 1) + 32 * (lane & 1) : lane);
+    const I i = i0 + (sizeof(T) == 2 ? (lane >> 1) + 32 * (lane & 1) : (lane >> 2) + 16 * (lane & 3));
     u32x4 c = {0u, 0u, 0u, 0u};
     uint32_t b = kMxMinScale;
     if (i < n) {
@@ -57,10 +60,20 @@ __global__ __launch_bounds__(256) void tape8_read_kernel(const u32x4* __restrict
       if (p < 2 * n) __builtin_nontemporal_store(u32x4{lo[0], lo[1], lo[2], lo[3]}, rows + p);
       if (p + 64 < 2 * n)
         __builtin_nontemporal_store(u32x4{hi[0], hi[1], hi[2], hi[3]}, rows + p + 64);
-    } else if (i < n) {
+    } else {
+      uint32_t g[4][4];  // word e of piece j of the lane's record; then of record j's piece lane % 4
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        rows[4 * i + k] = u32x4{f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]};
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[e][j] = f[4 * j + e];
+        quad_transpose(g[e]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // records i0 + 16 j .. + 15
+        const I p = 4 * i0 + 64 * j + lane;
+        if (p < 4 * n)
+          __builtin_nontemporal_store(u32x4{g[0][j], g[1][j], g[2][j], g[3][j]}, rows + p);
+      }
     }
   }
 }

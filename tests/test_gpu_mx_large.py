@@ -50,7 +50,8 @@ def test_mx4_matrix_above_2_34_elements():
         assert torch.equal(got, c[:got.shape[0]]), k
 
 
-def test_tape8_of_more_than_2_29_records():
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_tape8_of_more_than_2_29_records(dtype):
     """Five memories of 2^27 - 64 records each: rows as from one memory's call."""
     import torch
 
@@ -60,10 +61,11 @@ def test_tape8_of_more_than_2_29_records():
     codes = torch.randint(-127, 128, (B, 1, 1, T, S, 16), dtype=torch.int8, device="cuda")
     scales = torch.randint(2, 250, (B, 1, 1, T, S), dtype=torch.uint8, device="cuda")
     assert B * T * S > 1 << 29
-    rows = sdm.tape8_read((codes, scales), torch.bfloat16)
+    dtype, bits = getattr(torch, dtype), torch.int16 if dtype == "bfloat16" else torch.int32
+    rows = sdm.tape8_read((codes, scales), dtype)
     for b in range(B):
-        one = sdm.tape8_read((codes[b:b + 1], scales[b:b + 1]), torch.bfloat16)
-        assert torch.equal(one[0].view(torch.int16), rows[b].view(torch.int16)), b
+        one = sdm.tape8_read((codes[b:b + 1], scales[b:b + 1]), dtype)
+        assert torch.equal(one[0].view(bits), rows[b].view(bits)), b
 
 
 def test_project_mx4_outputs_above_2_31_values():
