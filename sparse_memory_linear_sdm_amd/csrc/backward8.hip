@@ -549,7 +549,9 @@ namespace {
 // Columns of a wavefront's tile.  Few memories: the scan goes at the pace of
 // one wavefront's instructions for a step, so with room for 8-column tiles on
 // a compute unit each (half the rows' instructions, twice the wavefronts) they
-// are taken.
+// are taken.  With 8 and 16 columns, us: 4 memories x 301 steps (d_v 64) 178 and
+// 268; 512 steps at d_v 128, dense and sparse, 16 memories 535 428 and 528 481,
+// 24 memories 776 629 and 592 549, 32 memories 878 732 and 653 630.
 constexpr int kMostUnits = 256;  // compute units of an undivided GPU
 bool few_memories(int n_mem, int d_v, int units) { return (int64_t)n_mem * (d_v / 8) <= units; }
 int scan_columns(int n_mem, int d_v) {
