@@ -899,7 +899,10 @@ hipError_t launch_scan_train8(float* M, int B, int H, int64_t N, int d_v, int64_
   if (T == 0) return hipSuccess;
   ScanArgs A{B * H, N,    d_v,   T,   W,    R,          widx, wk, ridx,
              rw,    v,    alpha, beta, out, tape, tape_scale, 0,    1};
-  // the tile widths and depths of the other scans
+  // The tile widths and depths of the other scans.  512 steps at d_v 128, us,
+  // with 32 columns, 16, and 16 in two row shards: 16 memories 623, 415, 393; 24
+  // memories 628, 453, 760; 32 memories 636, 494, 765; 40 memories 649, 799, -;
+  // 64 memories 823, 987, -.
   const int cus = compute_units();
   const bool narrow = d_v == 16 || (int64_t)A.n_mem * (d_v / 16) <= cus;
   if (!narrow) return launch<float, 32, 1, kSave8>(M, A, stream);
