@@ -23,8 +23,10 @@
 //            gathers again after them (never wrong, and rare while the table
 //            is much larger than a step's rows);
 //   finish   adds the tiles' partial sums in a fixed order.
-// Scales are powers of two, so the whole numbers of a tape row enter a sum as
-// they are and the block's scale multiplies the sum.
+// A whole number times its block's scale is exact in binary32, so the products
+// are with the rows' values, as from an fp32 tape.  (The scales multiplying
+// sums of products with the whole numbers, up to 127 times the values of a
+// block, made sums infinite that are not.)
 #include "internal.h"
 #include "mx.h"
 #include "ranges.h"
@@ -188,15 +190,16 @@ __global__ __launch_bounds__(256) void prepare_kernel(Bwd8Args A) {
       scale = A.tape_scale[rec + b * S];
     }
     const uint32_t c[4] = {q.x, q.y, q.z, q.w};
+    const float sc = __uint_as_float(scale << 23);
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float x[4];
       int8_unpack4(c[i], x);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s = fmaf(d[b * 16 + 4 * i + e], x[e], s);
+      for (int e = 0; e < 4; ++e) s = fmaf(d[b * 16 + 4 * i + e], x[e] * sc, s);
     }
-    dr = fmaf(s, __uint_as_float(scale << 23), dr);
+    dr += s;
   }
   if (lane < R) A.drw[step * R + lane] = dr;
 }
@@ -343,6 +346,8 @@ struct Scan8 {
     for (int k = 0; k < NI; ++k) {
       float p[4];
       int8_unpack4(w[k], p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] *= sc[k];
       f32x4 g = as_f4(s.Gw[k]);
       g.x = fmaf(mw[k], dd.x, g.x);
       g.y = fmaf(mw[k], dd.y, g.y);
@@ -354,10 +359,9 @@ struct Scan8 {
       dva.z = fmaf(bk, g.z, dva.z);
       dva.w = fmaf(bk, g.w, dva.w);
       const float gp = g.x * p[0] + g.y * p[1] + g.z * p[2] + g.w * p[3];
-      da = fmaf(keep * sc[k], gp, da);
-      const float ap = a * sc[k];
-      dbk[k] = g.x * (vv.x - ap * p[0]) + g.y * (vv.y - ap * p[1]) + g.z * (vv.z - ap * p[2]) +
-               g.w * (vv.w - ap * p[3]);
+      da = fmaf(keep, gp, da);
+      dbk[k] = g.x * (vv.x - a * p[0]) + g.y * (vv.y - a * p[1]) + g.z * (vv.z - a * p[2]) +
+               g.w * (vv.w - a * p[3]);
       const float c = a * keep;
       s.Gw[k] = as_u4(f32x4{c * g.x, c * g.y, c * g.z, c * g.w});
     }
