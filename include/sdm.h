@@ -356,7 +356,9 @@ int sdm_scan_train8(void* M, int B, int H, int64_t N, int d_v, int64_t T, int W,
 
 /* The rows of an 8-bit tape of S = W + R slots per step (1..128):
  *   rows  [B, H, T, S, d_v] fp32 (dtype SDM_F32) or bf16 bits (SDM_BF16),
- *         exact in both, 16-byte aligned.
+ *         exact in both, for any codes and scale bytes (values past the type's
+ *         range become infinite; a block of byte 255 reads as NaN whatever its
+ *         codes), 16-byte aligned.
  * T = 0 is a valid no-op (the arrays may then be NULL). */
 int sdm_tape8_read(const int8_t* tape, const uint8_t* tape_scale, int B, int H, int d_v,
                    int64_t T, int S, int dtype, void* rows, void* stream);

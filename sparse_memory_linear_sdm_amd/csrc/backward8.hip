@@ -190,7 +190,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(Bwd8Args A) {
       scale = A.tape_scale[rec + b * S];
     }
     const uint32_t c[4] = {q.x, q.y, q.z, q.w};
-    const float sc = __uint_as_float(scale << 23);
+    const float sc = scale_value(scale);
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -333,14 +333,14 @@ struct Scan8 {
     float sc[NI];
     if constexpr (COLS == 16) {
       quad_transpose(w);
-      const uint32_t scale = (uint32_t)s.scale[0] << 23;
+      const uint32_t scale = __float_as_uint(scale_value(s.scale[0]));
       sc[0] = __uint_as_float(dpp_mov<0x00>(scale));
       sc[1] = __uint_as_float(dpp_mov<0x55>(scale));
       sc[2] = __uint_as_float(dpp_mov<0xAA>(scale));
       sc[3] = __uint_as_float(dpp_mov<0xFF>(scale));
     } else {
 #pragma unroll
-      for (int k = 0; k < NI; ++k) sc[k] = __uint_as_float((uint32_t)s.scale[k] << 23);
+      for (int k = 0; k < NI; ++k) sc[k] = scale_value(s.scale[k]);
     }
 #pragma unroll
     for (int k = 0; k < NI; ++k) {

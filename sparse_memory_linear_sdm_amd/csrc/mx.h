@@ -41,6 +41,13 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
 // 2^(b - 127) for b in [1, 254].
 __device__ __forceinline__ float scale_f32(uint32_t b) { return __uint_as_float(b << 23); }
 
+// What any scale code stands for: 2^(b - 127), for 0 a subnormal; NaN for 255,
+// whose bits are infinity's and the product with zero NaN.
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  const float s = __uint_as_float(umax(b << 23, 0x00400000u));
+  return fmaf(s, 0.0f, s);
+}
+
 // Scale code of a 4-bit block from its maximum's magnitude bits.
 __device__ __forceinline__ uint32_t mx4_scale(uint32_t m) {
   const int e = (int)(m >> 23) - 2;

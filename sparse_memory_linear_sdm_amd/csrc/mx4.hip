@@ -122,9 +122,7 @@ __global__ __launch_bounds__(kQWaves* kWave) void dequantize_kernel(
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     if (r0 + i >= rows) return;
-    // code 0 is 2^-127, a subnormal; 255 reads as NaN
-    const float s = b[i] == kMxNan ? __uint_as_float(0x7FC00000u)
-                                   : (b[i] == 0 ? __uint_as_float(0x00400000u) : scale_f32(b[i]));
+    const float s = scale_value(b[i]);
     float f[kEach];
     const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 0);
     const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i], 1.0f, 1);

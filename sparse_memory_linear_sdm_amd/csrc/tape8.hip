@@ -34,8 +34,7 @@ __global__ __launch_bounds__(256) void tape8_read_kernel(const u32x4* __restrict
       c = codes[rec];
       b = scales[rec];
     }
-    const float s = b == kMxNan ? __uint_as_float(0x7FC00000u)
-                                : (b == 0 ? __uint_as_float(0x00400000u) : scale_f32(b));
+    const float s = scale_value(b);
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     uint32_t f[16];
 #pragma unroll

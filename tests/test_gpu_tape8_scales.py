@@ -1,6 +1,6 @@
-"""The reverse pass from an 8-bit tape over the range of fp32: it agrees with
-the rows that sdm_tape8_read gives, also where the sums come near fp32's
-largest value.
+"""The reverse pass from an 8-bit tape over the whole range of its scales and
+of fp32: it agrees with the rows that sdm_tape8_read gives, also where the
+sums come near fp32's largest value and for every scale byte.
 
 Every output here is a sum of terms of one sign, so it is within n roundings
 of 2^-24 of the float64 form, relative to itself; n is at most the number of
@@ -82,3 +82,40 @@ def test_sums_near_the_largest_value(H, d_v):
     want = _want(s, codes, scales, dout, G)
     assert all(np.all(np.abs(x) < 2.0 ** 128) for x in want.values())
     _check(_run(s, codes, scales, dout, G), want, d_v)
+
+
+@pytest.mark.parametrize("H,d_v", SIZES)
+def test_the_smallest_scale_bytes(H, d_v):
+    """Bytes 0 (2^-127) to 3 in turn; v = 0, so that d(beta k) is the rows' part alone."""
+    rng = np.random.default_rng(H * d_v)
+    s = _step(rng, H, d_v, 0.0, 0.5)
+    shape = (1, H, d_v // 16, T, W + R)
+    codes = rng.integers(1, 128, (*shape, 16)).astype(np.int8)
+    big = np.float32(2.0 ** 100)
+    dout = rng.uniform(.5, 1, (1, H, T, d_v)).astype(np.float32) * big
+    G = rng.uniform(.5, 1, (1, H, N, d_v)).astype(np.float32) * big
+    for byte in range(4):
+        scales = np.full(shape, byte, np.uint8)
+        _check(_run(s, codes, scales, dout, G), _want(s, codes, scales, dout, G), d_v)
+
+
+@pytest.mark.parametrize("H,d_v", SIZES)
+def test_a_marked_block_is_nan_whatever_its_codes(H, d_v):
+    """Byte 255 on one block of one write slot and of one read slot: the sums
+    that take these rows are NaN, the others as without the mark."""
+    rng = np.random.default_rng(H * d_v + 1)
+    s = _step(rng, H, d_v, 2.0, 0.5)
+    shape = (1, H, d_v // 16, T, W + R)
+    codes = rng.integers(1, 128, (*shape, 16)).astype(np.int8)
+    scales = np.full(shape, 120, np.uint8)
+    scales[:, :, -1, 1, 0] = 255  # step 1: write slot 0 and read slot 1
+    scales[:, :, 0, 1, W + 1] = 255
+    dout = rng.uniform(.5, 1, (1, H, T, d_v)).astype(np.float32)
+    G = rng.uniform(.5, 1, (1, H, N, d_v)).astype(np.float32)
+    got, want = _run(s, codes, scales, dout, G), _want(s, codes, scales, dout, G)
+    for k in (*GRADS, "G"):
+        nan = np.isnan(want[k])
+        assert np.array_equal(np.isnan(got[k]), nan), k
+        got[k], want[k] = np.where(nan, 0, got[k]), np.where(nan, 0, want[k])
+    assert np.isnan(_want(s, codes, scales, dout, G)["drw"]).sum() == H
+    _check(got, want, d_v)
