@@ -29,6 +29,11 @@ Planned scan (fp32 state; few memories, long sequences):
   touch_prepare(widx, ridx, N) -> (seen, first)
   select_backward(idx, weight, dweight, n) -> (dx1, dx2)
   state_init_backward(G) -> dM0
+
+stream= is a torch stream or a raw handle (None: the current stream).  Tensors
+that a call makes are allocated for that stream and marked as used by the
+current one; tensors passed in have to stay allocated until the stream has run
+the call.
 """
 from __future__ import annotations
 
@@ -285,7 +290,7 @@ def project(X, Wt, n: int, out=None, stream=None):
         raise ValueError("X must be [B, T, d_model] and Wt [H, P, d_model]")
     B, T, d_model = X.shape
     H, P = Wt.shape[0], Wt.shape[1]
-    out, outs = _project_out(B, T, H, P, n, "Wt", out, None, X.device)
+    out, outs = _project_out(B, T, H, P, n, "Wt", out, stream, X.device)
     ptrs = _gpu(_arg(X, bf16, (B, T, d_model), "X"), _arg(Wt, bf16, (H, P, d_model), "Wt"), *outs)
     _check(lib().sdm_project(ptrs[0], ptrs[1], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[2:],
                              _stream(stream)))
@@ -385,9 +390,8 @@ def select(x1, x2, K: int, out=None, stream=None):
         raise ValueError("x1 and x2 must have a last dimension n")
     n, lead = shape[-1], shape[:-1]
     if out is None:
-        idx = torch.empty(lead + (K,), dtype=torch.int32, device=x1.device)
-        score = torch.empty(lead + (K,), dtype=f32, device=x1.device)
-        weight = torch.empty(lead + (K,), dtype=f32, device=x1.device)
+        empty = _empty_on(stream, x1.device)
+        idx, score, weight = (empty(lead + (K,), dt) for dt in (torch.int32, f32, f32))
     else:
         idx, score, weight = out
     p1, p2, pi, ps, pw = _gpu(
@@ -410,7 +414,7 @@ def state_init(M0, B: int, dtype=None, out=None, stream=None):
     a0 = _arg(M0, torch.float32, (H, N, d_v), "M0")
     if out is None:
         dtype = torch.float32 if dtype is None else dtype
-        M = torch.empty((B, H, N, d_v), dtype=dtype, device=M0.device)
+        M = _empty_on(stream, M0.device)((B, H, N, d_v), dtype)
     else:
         M = out
     p0, pm = _gpu(a0, _arg(M, _state_types(), (B, H, N, d_v), "M"))
@@ -449,7 +453,7 @@ def scan(M, widx, wk, ridx, rw, v, alpha, beta, out=None, stream=None):
     am = _arg(M, _state_types(), (B, H, N, d_v), "M")
     ins = _scan_args(B, H, T, W, R, d_v, widx, wk, ridx, rw, v, alpha, beta)
     if out is None:
-        out = torch.empty((B, H, T, d_v), dtype=torch.float32, device=M.device)
+        out = _empty_on(stream, M.device)((B, H, T, d_v), torch.float32)
     pm, *ptrs = _gpu(am, *ins, _arg(out, torch.float32, (B, H, T, d_v), "out"))
     _check(lib().sdm_scan(pm, _state_dtype(M), B, H, N, d_v, T, W, R, *ptrs, _stream(stream)))
     return out
@@ -473,13 +477,13 @@ def step_decode(M, s1, s2, q1, q2, v, alpha, beta, W: int, R: int, out=None, wan
             (("s1", s1), ("s2", s2), ("q1", q1), ("q2", q2))]
     ins += [_arg(v, f32, (B, H, d_v), "v"), _arg(alpha, f32, (B, H), "alpha"),
             _arg(beta, f32, (B, H), "beta")]
+    empty = _empty_on(stream, M.device) if out is None or want_idx else None
     if out is None:
-        out = torch.empty((B, H, d_v), dtype=f32, device=M.device)
+        out = empty((B, H, d_v), f32)
     ins.append(_arg(out, f32, (B, H, d_v), "out"))
     widx = ridx = None
     if want_idx:
-        widx = torch.empty((B, H, W), dtype=torch.int32, device=M.device)
-        ridx = torch.empty((B, H, R), dtype=torch.int32, device=M.device)
+        widx, ridx = empty((B, H, W), torch.int32), empty((B, H, R), torch.int32)
     pm, *ptrs = _gpu(*ins)
     _check(lib().sdm_step_decode(pm, _state_dtype(M), B, H, n, d_v, W, R, *ptrs,
                                  widx.data_ptr() if widx is not None else None,
@@ -498,10 +502,11 @@ def scan_train(M, widx, wk, ridx, rw, v, alpha, beta, out=None, tape=None, strea
     B, H, N, d_v, T, W, R = _scan_shapes(M, widx, ridx)
     am = _arg(M, f32, (B, H, N, d_v), "M")
     ins = _scan_args(B, H, T, W, R, d_v, widx, wk, ridx, rw, v, alpha, beta)
+    empty = _empty_on(stream, M.device)
     if out is None:
-        out = torch.empty((B, H, T, d_v), dtype=f32, device=M.device)
+        out = empty((B, H, T, d_v), f32)
     if tape is None:
-        tape = torch.empty((B, H, T, W + R, d_v), dtype=f32, device=M.device)
+        tape = empty((B, H, T, W + R, d_v), f32)
     pm, *ptrs = _gpu(am, *ins, _arg(out, f32, (B, H, T, d_v), "out"),
                      _arg(tape, f32, (B, H, T, W + R, d_v), "tape"))
     _check(lib().sdm_scan_train(pm, B, H, N, d_v, T, W, R, *ptrs, _stream(stream)))
@@ -524,19 +529,14 @@ def scan_backward(widx, wk, ridx, rw, v, alpha, beta, tape, dout, G, workspace=N
     ins += [_arg(tape, f32, (B, H, T, W + R, d_v), "tape"),
             _arg(dout, f32, (B, H, T, d_v), "dout"), _arg(G, f32, (B, H, N, d_v), "G")]
     af = None if first is None else _arg(first, torch.int64, (B, H, T, 2), "first")
-    aw = None if workspace is None else _arg(workspace, None, None, "workspace")
-    dev = G.device
-    o = {"dv": torch.empty((B, H, T, d_v), dtype=f32, device=dev),
-         "dwk": torch.empty((B, H, T, W), dtype=f32, device=dev),
-         "drw": torch.empty((B, H, T, R), dtype=f32, device=dev),
-         "dalpha": torch.empty((B, H, T), dtype=f32, device=dev),
-         "dbeta": torch.empty((B, H, T), dtype=f32, device=dev)}
-    ptrs = _gpu(*ins, *(_arg(o[k], f32, None, k) for k in ("dv", "dwk", "drw", "dalpha", "dbeta")),
-                af, aw)
-    need = int(lib().sdm_scan_backward_workspace_size(B, H, d_v, T, W, R))
+    empty = _empty_on(stream, G.device)
+    shapes = {"dv": (B, H, T, d_v), "dwk": (B, H, T, W), "drw": (B, H, T, R),
+              "dalpha": (B, H, T), "dbeta": (B, H, T)}
+    o = {k: empty(shp, f32) for k, shp in shapes.items()}
     if workspace is None:
-        workspace = torch.empty((max(need, 16) + 3) // 4, dtype=f32, device=dev)
-        ptrs[-1] = workspace.data_ptr()
+        need = int(lib().sdm_scan_backward_workspace_size(B, H, d_v, T, W, R))
+        workspace = empty(((max(need, 16) + 3) // 4,), f32, mine=True)
+    ptrs = _gpu(*ins, *o.items(), af, _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()
     _check(lib().sdm_scan_backward(B, H, N, d_v, T, W, R, *ptrs, nbytes, _stream(stream)))
     return o
@@ -636,7 +636,7 @@ def scan_backward8(widx, wk, ridx, rw, v, alpha, beta, tape, dout, G, workspace=
     af = None if first is None else _arg(first, torch.int64, (B, H, T, 2), "first")
     if workspace is None:
         need = int(lib().sdm_scan_backward8_workspace_size(B, H, d_v, T, W, R))
-        workspace = empty((max(need, 16) + 3) // 4, f32, mine=True)
+        workspace = empty(((max(need, 16) + 3) // 4,), f32, mine=True)
     ptrs = _gpu(*ins, af, _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()
     _call(lib().sdm_scan_backward8, G, stream, B, H, N, d_v, T, W, R, *ptrs, nbytes)
@@ -656,10 +656,11 @@ def touch_prepare(widx, ridx, N: int, seen=None, first=None, stream=None):
     R = ridx.shape[3]
     ins = [_arg(widx, torch.int32, (B, H, T, W), "widx"),
            _arg(ridx, torch.int32, (B, H, T, R), "ridx")]
+    empty = _empty_on(stream, widx.device)
     if seen is None:
-        seen = torch.empty((B, H, (N + 31) // 32), dtype=torch.int32, device=widx.device)
+        seen = empty((B, H, (N + 31) // 32), torch.int32)
     if first is None:
-        first = torch.empty((B, H, T, 2), dtype=torch.int64, device=widx.device)
+        first = empty((B, H, T, 2), torch.int64)
     ptrs = _gpu(*ins, _arg(seen, torch.int32, (B, H, (N + 31) // 32), "seen"),
                 _arg(first, torch.int64, (B, H, T, 2), "first"))
     _check(lib().sdm_touch_prepare(B, H, N, T, W, R, *ptrs, _stream(stream)))
@@ -687,9 +688,9 @@ def select_backward(idx, weight, dweight, n: int, stream=None):
     K, lead = shape[-1], shape[:-1]
     ins = [_arg(idx, torch.int32, shape, "idx"), _arg(weight, f32, shape, "weight"),
            _arg(dweight, f32, shape, "dweight")]
-    dx1 = torch.empty(lead + (n,), dtype=f32, device=idx.device)
-    dx2 = torch.empty(lead + (n,), dtype=f32, device=idx.device)
-    ptrs = _gpu(*ins, _arg(dx1, f32, None, "dx1"), _arg(dx2, f32, None, "dx2"))
+    empty = _empty_on(stream, idx.device)
+    dx1, dx2 = empty(lead + (n,), f32), empty(lead + (n,), f32)
+    ptrs = _gpu(*ins, ("dx1", dx1), ("dx2", dx2))
     _check(lib().sdm_select_backward(ptrs[0], ptrs[1], ptrs[2], _units(lead), n, K, ptrs[3],
                                      ptrs[4], _stream(stream)))
     return dx1, dx2
@@ -706,7 +707,7 @@ def state_init_backward(G, out=None, seen=None, stream=None):
     B, H, N, d_v = G.shape
     ag = _arg(G, f32, (B, H, N, d_v), "G")
     as_ = None if seen is None else _arg(seen, torch.int32, (B, H, (N + 31) // 32), "seen")
-    dM0 = torch.empty((H, N, d_v), dtype=f32, device=G.device) if out is None else out
+    dM0 = _empty_on(stream, G.device)((H, N, d_v), f32) if out is None else out
     pg, ps, po = _gpu(ag, as_, _arg(dM0, f32, (H, N, d_v), "dM0"))
     _check(lib().sdm_state_init_backward(pg, B, H, N, d_v, ps, po, _stream(stream)))
     return dM0
@@ -732,7 +733,7 @@ def scan_plan(widx, wk, ridx, rw, N: int, d_v: int, workspace=None, stream=None)
            _arg(ridx, torch.int32, (B, H, T, R), "ridx"), _arg(rw, f32, (B, H, T, R), "rw")]
     need = scan_plan_workspace_size(B, H, d_v, T)
     if workspace is None:
-        workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=widx.device)
+        workspace = _empty_on(stream, widx.device)((max(need, 256),), torch.uint8)
     ptrs = _gpu(*ins, _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()
     _check(lib().sdm_scan_plan(B, H, N, d_v, T, W, R, *ptrs, nbytes, _stream(stream)))
@@ -751,7 +752,7 @@ def scan_planned(M, v, alpha, beta, workspace, out=None, stream=None):
     T = v.shape[2]
     f32 = torch.float32
     if out is None:
-        out = torch.empty((B, H, T, d_v), dtype=f32, device=M.device)
+        out = _empty_on(stream, M.device)((B, H, T, d_v), f32)
     ptrs = _gpu(_arg(M, f32, (B, H, N, d_v), "M"), _arg(v, f32, (B, H, T, d_v), "v"),
                 _arg(alpha, f32, (B, H, T), "alpha"), _arg(beta, f32, (B, H, T), "beta"),
                 _arg(out, f32, (B, H, T, d_v), "out"), _arg(workspace, None, None, "workspace"))

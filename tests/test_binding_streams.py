@@ -1,0 +1,116 @@
+"""Calls of the binding on a stream given by the caller.  What a call makes is
+that stream's memory: the current stream may still be using what the allocator
+would hand out for it, and may be handed the call's own workspace as soon as
+the call returns."""
+import pytest
+import torch
+
+import sparse_memory_linear_sdm_amd as sdm
+
+f32, i32, i64, u8 = torch.float32, torch.int32, torch.int64, torch.uint8
+B, H, N, n, d_v, T, W, R, d_model = 2, 3, 64, 8, 32, 5, 4, 3, 128
+P = 4 * n + d_v + 2
+
+
+def _calls(device):
+    """name -> (call with only a stream left out, how many tensors it makes)."""
+    def z(*shape, dtype=f32):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+    sel = dict(widx=torch.arange(W, dtype=i32, device=device).expand(B, H, T, W).contiguous(),
+               wk=z(B, H, T, W) + 1 / W,
+               ridx=torch.arange(R, dtype=i32, device=device).expand(B, H, T, R).contiguous(),
+               rw=z(B, H, T, R) + 1 / R)
+    gates = dict(v=z(B, H, T, d_v) + 1, alpha=z(B, H, T) + 1, beta=z(B, H, T) + .5)
+    step = {**sel, **gates}
+    M, x, dout = z(B, H, N, d_v), torch.rand(B, H, T, n, device=device), z(B, H, T, d_v) + 1
+    half, vec, one = torch.rand(B, H, n, device=device), z(B, H, d_v), z(B, H)
+    M0, rows = z(H, N, d_v), z(6, d_model)
+    X, Wt = z(B, T, d_model, dtype=torch.bfloat16), z(H, P, d_model, dtype=torch.bfloat16)
+    tape = z(B, H, T, W + R, d_v)
+    tape8 = (z(B, H, 2, T, W + R, 16, dtype=torch.int8), z(B, H, 2, T, W + R, dtype=u8) + 127)
+    xq, xs = z(B, T, d_model // 2, dtype=u8), z(1, B * T, 4, dtype=u8) + 127
+    wq, ws = z(H, P, d_model // 2, dtype=u8), z(1, H * P, 4, dtype=u8) + 127
+    plan = sdm.scan_plan(**sel, N=N, d_v=d_v) if device == "cuda" else z(256, dtype=u8)
+    return {
+        "project": (lambda s: sdm.project(X, Wt, n, stream=s), 7),
+        "mx4_quantize": (lambda s: sdm.mx4_quantize(rows, stream=s), 2),
+        "mx4_dequantize": (lambda s: sdm.mx4_dequantize(xq, xs, stream=s), 1),
+        "project_mx4": (lambda s: sdm.project_mx4(xq, xs, wq, ws, n, stream=s), 7),
+        "select": (lambda s: sdm.select(x, x, W, stream=s), 3),
+        "state_init": (lambda s: sdm.state_init(M0, B, stream=s), 1),
+        "scan": (lambda s: sdm.scan(M, **step, stream=s), 1),
+        "step_decode": (lambda s: sdm.step_decode(M, half, half, half, half, vec, one, one,
+                                                  W, R, stream=s), 3),
+        "scan_train": (lambda s: sdm.scan_train(M, **step, stream=s), 2),
+        "scan_backward": (lambda s: sdm.scan_backward(**step, tape=tape, dout=dout, G=M, stream=s), 6),
+        "scan_train8": (lambda s: sdm.scan_train8(M, **step, stream=s), 3),
+        "tape8_read": (lambda s: sdm.tape8_read(tape8, stream=s), 1),
+        "scan_backward8": (lambda s: sdm.scan_backward8(**step, tape=tape8, dout=dout, G=M, stream=s), 6),
+        "touch_prepare": (lambda s: sdm.touch_prepare(sel["widx"], sel["ridx"], N, stream=s), 2),
+        "select_backward": (lambda s: sdm.select_backward(sel["widx"], sel["wk"], sel["wk"], n,
+                                                          stream=s), 2),
+        "state_init_backward": (lambda s: sdm.state_init_backward(M, stream=s), 1),
+        "scan_plan": (lambda s: sdm.scan_plan(**sel, N=N, d_v=d_v, stream=s), 1),
+        "scan_planned": (lambda s: sdm.scan_planned(M, **gates, workspace=plan, stream=s), 1),
+    }
+
+
+NAMES = sorted(_calls("cpu"))
+DROPPED = {"scan_backward": 1, "scan_backward8": 1}  # workspaces that end with the call
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_what_a_call_makes_is_its_streams(name, monkeypatch):
+    """Every tensor a call makes is asked for on its stream, workspaces as the
+    call's own (CPU tensors: the call stops at the device check)."""
+    call, count = _calls("cpu")[name]
+    made = []
+
+    def empty_on(stream, device):
+        def make(shape, dtype, mine=False):
+            made.append((stream, mine))
+            return torch.zeros(shape, dtype=dtype)
+        return make
+
+    def refuse(*a, **k):
+        raise AssertionError("made on the current stream")
+
+    stream = object()
+    monkeypatch.setattr(sdm, "_empty_on", empty_on)
+    monkeypatch.setattr(torch, "empty", refuse)
+    monkeypatch.setattr(torch, "empty_like", refuse)
+    with pytest.raises(ValueError, match="on the GPU"):
+        call(stream)
+    assert [s for s, _ in made] == [stream] * count
+    assert sum(mine for _, mine in made) == DROPPED.get(name, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", NAMES)
+def test_the_memory_belongs_to_the_stream(name, monkeypatch):
+    """The same on the GPU, by the allocator's record of each tensor's segment."""
+    call, count = _calls("cuda")[name]
+    made = []
+    inner = sdm._empty_on
+
+    def empty_on(stream, device):
+        make = inner(stream, device)
+
+        def keep(*a, **k):
+            made.append(make(*a, **k))
+            return made[-1]
+        return keep
+
+    monkeypatch.setattr(sdm, "_empty_on", empty_on)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        call(handle)
+    side.synchronize()
+    assert len(made) == 2 * count
+    segments = torch.cuda.memory_snapshot()
+    for t in made:
+        at = t.data_ptr()
+        of = [g["stream"] for g in segments if g["address"] <= at < g["address"] + g["total_size"]]
+        assert of == [side.cuda_stream]
