@@ -33,7 +33,8 @@ Planned scan (fp32 state; few memories, long sequences):
 stream= is a torch stream or a raw handle (None: the current stream).  Tensors
 that a call makes are allocated for that stream and marked as used by the
 current one; tensors passed in have to stay allocated until the stream has run
-the call.
+the call.  A call runs on its tensors' GPU, whichever is current; a stream of
+another GPU is refused.
 """
 from __future__ import annotations
 
@@ -126,16 +127,6 @@ def _check(rc: int):
         raise SDMError(rc, lib().sdm_last_error().decode())
 
 
-def _stream(stream):
-    import torch
-
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    if isinstance(stream, torch.cuda.Stream):
-        return stream.cuda_stream
-    return int(stream)
-
-
 def _arg(t, dtype, shape, name):
     """Check one tensor argument: type, exact shape (the one the call derives
     from its other arguments), dtype (one dtype or a tuple of allowed ones;
@@ -198,10 +189,12 @@ def _call(fn, t, stream, *args):
             return _call(fn, t, stream, *args)
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        if isinstance(stream, torch.cuda.Stream) and stream.device != t.device:
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device != t.device:
             raise ValueError(f"the stream is on {stream.device}, the call's tensors on {t.device}")
-        handle = _stream(stream)
+        handle = stream.cuda_stream
+    else:
+        handle = int(stream)
     _check(fn(*args, handle))
 
 
@@ -292,8 +285,7 @@ def project(X, Wt, n: int, out=None, stream=None):
     H, P = Wt.shape[0], Wt.shape[1]
     out, outs = _project_out(B, T, H, P, n, "Wt", out, stream, X.device)
     ptrs = _gpu(_arg(X, bf16, (B, T, d_model), "X"), _arg(Wt, bf16, (H, P, d_model), "Wt"), *outs)
-    _check(lib().sdm_project(ptrs[0], ptrs[1], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[2:],
-                             _stream(stream)))
+    _call(lib().sdm_project, X, stream, *ptrs[:2], B, T, d_model, H, n, P - 4 * n - 2, *ptrs[2:])
     return out
 
 
@@ -399,7 +391,7 @@ def select(x1, x2, K: int, out=None, stream=None):
         _arg(idx, torch.int32, lead + (K,), "idx"),
         None if score is None else _arg(score, f32, lead + (K,), "score"),
         _arg(weight, f32, lead + (K,), "weight"))
-    _check(lib().sdm_select(p1, p2, _units(lead), n, K, pi, ps, pw, _stream(stream)))
+    _call(lib().sdm_select, x1, stream, p1, p2, _units(lead), n, K, pi, ps, pw)
     return idx, score, weight
 
 
@@ -418,7 +410,7 @@ def state_init(M0, B: int, dtype=None, out=None, stream=None):
     else:
         M = out
     p0, pm = _gpu(a0, _arg(M, _state_types(), (B, H, N, d_v), "M"))
-    _check(lib().sdm_state_init(pm, _state_dtype(M), p0, B, H, N, d_v, _stream(stream)))
+    _call(lib().sdm_state_init, M, stream, pm, _state_dtype(M), p0, B, H, N, d_v)
     return M
 
 
@@ -455,7 +447,7 @@ def scan(M, widx, wk, ridx, rw, v, alpha, beta, out=None, stream=None):
     if out is None:
         out = _empty_on(stream, M.device)((B, H, T, d_v), torch.float32)
     pm, *ptrs = _gpu(am, *ins, _arg(out, torch.float32, (B, H, T, d_v), "out"))
-    _check(lib().sdm_scan(pm, _state_dtype(M), B, H, N, d_v, T, W, R, *ptrs, _stream(stream)))
+    _call(lib().sdm_scan, M, stream, pm, _state_dtype(M), B, H, N, d_v, T, W, R, *ptrs)
     return out
 
 
@@ -485,10 +477,9 @@ def step_decode(M, s1, s2, q1, q2, v, alpha, beta, W: int, R: int, out=None, wan
     if want_idx:
         widx, ridx = empty((B, H, W), torch.int32), empty((B, H, R), torch.int32)
     pm, *ptrs = _gpu(*ins)
-    _check(lib().sdm_step_decode(pm, _state_dtype(M), B, H, n, d_v, W, R, *ptrs,
-                                 widx.data_ptr() if widx is not None else None,
-                                 ridx.data_ptr() if ridx is not None else None,
-                                 _stream(stream)))
+    _call(lib().sdm_step_decode, M, stream, pm, _state_dtype(M), B, H, n, d_v, W, R, *ptrs,
+          widx.data_ptr() if widx is not None else None,
+          ridx.data_ptr() if ridx is not None else None)
     return out, widx, ridx
 
 
@@ -509,7 +500,7 @@ def scan_train(M, widx, wk, ridx, rw, v, alpha, beta, out=None, tape=None, strea
         tape = empty((B, H, T, W + R, d_v), f32)
     pm, *ptrs = _gpu(am, *ins, _arg(out, f32, (B, H, T, d_v), "out"),
                      _arg(tape, f32, (B, H, T, W + R, d_v), "tape"))
-    _check(lib().sdm_scan_train(pm, B, H, N, d_v, T, W, R, *ptrs, _stream(stream)))
+    _call(lib().sdm_scan_train, M, stream, pm, B, H, N, d_v, T, W, R, *ptrs)
     return out, tape
 
 
@@ -538,7 +529,7 @@ def scan_backward(widx, wk, ridx, rw, v, alpha, beta, tape, dout, G, workspace=N
         workspace = empty(((max(need, 16) + 3) // 4,), f32, mine=True)
     ptrs = _gpu(*ins, *o.items(), af, _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().sdm_scan_backward(B, H, N, d_v, T, W, R, *ptrs, nbytes, _stream(stream)))
+    _call(lib().sdm_scan_backward, G, stream, B, H, N, d_v, T, W, R, *ptrs, nbytes)
     return o
 
 
@@ -561,7 +552,7 @@ def scan_backward_noalloc(widx, wk, ridx, rw, v, alpha, beta, tape, dout, G, out
     ins += [_arg(out[k], f32, shp, k) for k, shp in shapes.items()]
     af = None if first is None else _arg(first, torch.int64, (B, H, T, 2), "first")
     ptrs = _gpu(*ins, af)
-    _check(lib().sdm_scan_backward_noalloc(B, H, N, d_v, T, W, R, *ptrs, _stream(stream)))
+    _call(lib().sdm_scan_backward_noalloc, G, stream, B, H, N, d_v, T, W, R, *ptrs)
     return out
 
 
@@ -663,7 +654,7 @@ def touch_prepare(widx, ridx, N: int, seen=None, first=None, stream=None):
         first = empty((B, H, T, 2), torch.int64)
     ptrs = _gpu(*ins, _arg(seen, torch.int32, (B, H, (N + 31) // 32), "seen"),
                 _arg(first, torch.int64, (B, H, T, 2), "first"))
-    _check(lib().sdm_touch_prepare(B, H, N, T, W, R, *ptrs, _stream(stream)))
+    _call(lib().sdm_touch_prepare, widx, stream, B, H, N, T, W, R, *ptrs)
     return seen, first
 
 
@@ -691,8 +682,7 @@ def select_backward(idx, weight, dweight, n: int, stream=None):
     empty = _empty_on(stream, idx.device)
     dx1, dx2 = empty(lead + (n,), f32), empty(lead + (n,), f32)
     ptrs = _gpu(*ins, ("dx1", dx1), ("dx2", dx2))
-    _check(lib().sdm_select_backward(ptrs[0], ptrs[1], ptrs[2], _units(lead), n, K, ptrs[3],
-                                     ptrs[4], _stream(stream)))
+    _call(lib().sdm_select_backward, idx, stream, *ptrs[:3], _units(lead), n, K, *ptrs[3:])
     return dx1, dx2
 
 
@@ -709,7 +699,7 @@ def state_init_backward(G, out=None, seen=None, stream=None):
     as_ = None if seen is None else _arg(seen, torch.int32, (B, H, (N + 31) // 32), "seen")
     dM0 = _empty_on(stream, G.device)((H, N, d_v), f32) if out is None else out
     pg, ps, po = _gpu(ag, as_, _arg(dM0, f32, (H, N, d_v), "dM0"))
-    _check(lib().sdm_state_init_backward(pg, B, H, N, d_v, ps, po, _stream(stream)))
+    _call(lib().sdm_state_init_backward, G, stream, pg, B, H, N, d_v, ps, po)
     return dM0
 
 
@@ -736,7 +726,7 @@ def scan_plan(widx, wk, ridx, rw, N: int, d_v: int, workspace=None, stream=None)
         workspace = _empty_on(stream, widx.device)((max(need, 256),), torch.uint8)
     ptrs = _gpu(*ins, _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().sdm_scan_plan(B, H, N, d_v, T, W, R, *ptrs, nbytes, _stream(stream)))
+    _call(lib().sdm_scan_plan, widx, stream, B, H, N, d_v, T, W, R, *ptrs, nbytes)
     return workspace
 
 
@@ -757,5 +747,5 @@ def scan_planned(M, v, alpha, beta, workspace, out=None, stream=None):
                 _arg(alpha, f32, (B, H, T), "alpha"), _arg(beta, f32, (B, H, T), "beta"),
                 _arg(out, f32, (B, H, T, d_v), "out"), _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().sdm_scan_planned(ptrs[0], B, H, N, d_v, T, *ptrs[1:], nbytes, _stream(stream)))
+    _call(lib().sdm_scan_planned, M, stream, ptrs[0], B, H, N, d_v, T, *ptrs[1:], nbytes)
     return out

@@ -114,3 +114,87 @@ def test_the_memory_belongs_to_the_stream(name, monkeypatch):
         at = t.data_ptr()
         of = [g["stream"] for g in segments if g["address"] <= at < g["address"] + g["total_size"]]
         assert of == [side.cuda_stream]
+
+
+# ------------------------------------------------------- the GPU a call runs on
+
+class _On:
+    """Stands for a tensor or a stream of GPU `index`."""
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+        self.cuda_stream = 1000 + index
+
+    def get_device(self):
+        return self.device.index
+
+
+@pytest.fixture
+def two_gpus(monkeypatch):
+    """GPU 0 current, of two; the current stream of GPU i has handle 10 + i."""
+    now = [0]
+
+    class device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 10 + i, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "Stream", _On)
+    return now
+
+
+def test_a_call_runs_on_its_tensors_gpu(two_gpus):
+    seen = []
+
+    def fn(*args):
+        seen.append((two_gpus[0], *args))
+        return 0
+
+    sdm._call(fn, _On(0), None, 5)
+    sdm._call(fn, _On(1), None, 6)
+    sdm._call(fn, _On(1), _On(1), 7)
+    sdm._call(fn, _On(1), 99, 8)
+    assert seen == [(0, 5, 10), (1, 6, 11), (1, 7, 1001), (1, 8, 99)] and two_gpus[0] == 0
+    with pytest.raises(ValueError, match="the stream is on cuda:0, the call's tensors on cuda:1"):
+        sdm._call(fn, _On(1), _On(0), 9)
+    assert len(seen) == 4 and two_gpus[0] == 0
+
+
+@pytest.mark.parametrize("name", NAMES + ["scan_backward_noalloc"])
+def test_every_call_runs_on_its_tensors_gpu(name, monkeypatch):
+    """Each launch goes through the one place that makes the tensors' GPU current."""
+    calls = _calls("cpu")
+    if name in calls:
+        call = calls[name][0]
+    else:
+        z = torch.zeros
+        out = dict(dv=z(B, H, T, d_v), dwk=z(B, H, T, W), drw=z(B, H, T, R), dalpha=z(B, H, T),
+                   dbeta=z(B, H, T))
+        i = [z(B, H, T, K, dtype=i32) for K in (W, R)]
+        call = lambda s: sdm.scan_backward_noalloc(  # noqa: E731
+            i[0], out["dwk"], i[1], out["drw"], out["dv"], out["dalpha"], out["dbeta"],
+            z(B, H, T, W + R, d_v), out["dv"], z(B, H, N, d_v), out, stream=s)
+    seen = []
+
+    def launched(rc):
+        raise AssertionError("launched on whatever GPU is current")
+
+    def at(fn, t, stream, *args):
+        assert isinstance(t, torch.Tensor)
+        seen.append((fn.__name__, stream))
+
+    monkeypatch.setattr(sdm, "_gpu", lambda *args: [None] * len(args))
+    monkeypatch.setattr(sdm, "_check", launched)
+    monkeypatch.setattr(sdm, "_call", at)
+    stream = object()
+    call(stream)
+    call(None)
+    assert seen == [("sdm_" + name, stream), ("sdm_" + name, None)]
