@@ -68,13 +68,20 @@ class SDMError(RuntimeError):
 
 
 def lib():
-    """Load libsdm.so (raises if it is not built)."""
+    """Load libsdm.so (raises if it is not built, or built from other sources
+    than this binding's)."""
     global _lib
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(
                 f"{LIB_PATH} is not built; run `python -m sparse_memory_linear_sdm_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
+        missing = [e for e in EXPORTS if not hasattr(L, e)]
+        if "sdm_abi_version" not in missing and L.sdm_abi_version() != ABI_VERSION:
+            raise RuntimeError(f"{LIB_PATH} has ABI {L.sdm_abi_version()}, this binding "
+                               f"expects {ABI_VERSION}: rebuild it")
+        if missing:
+            raise RuntimeError(f"{LIB_PATH} lacks {', '.join(missing)}: rebuild it")
         p, i32, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
         L.sdm_project.argtypes = [p, p, i32, i32, i32, i32, i32, i32] + [p] * 8
         L.sdm_mx4_quantize.argtypes = [p, i32, i64, i64, p, p, p]
@@ -115,9 +122,6 @@ def lib():
         L.sdm_status_string.restype = ctypes.c_char_p
         L.sdm_last_error.argtypes = []
         L.sdm_last_error.restype = ctypes.c_char_p
-        if L.sdm_abi_version() != ABI_VERSION:
-            raise RuntimeError(f"{LIB_PATH} has ABI {L.sdm_abi_version()}, this binding "
-                               f"expects {ABI_VERSION}: rebuild it")
         _lib = L
     return _lib
 
