@@ -128,6 +128,10 @@ int sdm_tape8_read(const int8_t* tape, const uint8_t* tape_scale, int B, int H, 
 size_t sdm_scan_backward8_workspace_size(int B, int H, int d_v, int64_t T, int W, int R) {
   if (B < 1 || H < 1 || T < 0 || W < 1 || W > 64 || R < 1 || R > 64 || !dv_supported(d_v)) return 0;
   if ((int64_t)B * H > sdm::kMaxMemories || T > sdm::kMaxWaveUnits) return 0;
+  // the call's own limits on the steps and on one memory's tape
+  if ((int64_t)B * H * (T + sdm::kBackward8Pad) > sdm::kMaxWaveUnits ||
+      T * (W + R) * d_v >= ((int64_t)1 << 31) || !sdm::ranges::tape8_ok(d_v, T, W, R))
+    return 0;
   return sdm::scan_backward8_workspace_bytes(B * H, d_v, T, W);
 }
 

@@ -198,3 +198,25 @@ def test_projection_launches_stay_below_2_to_the_32_work_items():
     for call, ptrs in ((L.sdm_project, 2), (L.sdm_project_mx4, 4)):
         a = [FAKE] * ptrs + [1 << 15, 1 << 16, 256, 1, 64, 16] + [FAKE] * 7 + [None]
         assert call(*a) == 2 and "2^23 - 1" in _err()  # 2^23 row tiles x 2
+
+
+def test_backward8_workspace_size_is_0_where_the_call_refuses():
+    """Its limits on steps and on a memory's tape: the last size inside, the first outside."""
+    L = sdm.lib()
+    size = L.sdm_scan_backward8_workspace_size
+    ok = [1, 1, 4096, 16, 8, 8, 8] + [FAKE] * 18 + [1 << 60, None]
+    for inside, outside, word in [
+            # B*H*(T + 8) <= 2^26 - 4
+            ((8, 8, 16, (1 << 20) - 9, 1, 1), (8, 8, 16, (1 << 20) - 8, 1, 1), "T + 8"),
+            ((1 << 10, 1 << 10, 16, 55, 1, 1), (1 << 10, 1 << 10, 16, 56, 1, 1), "T + 8"),
+            # T*(W + R)*d_v < 2^31
+            ((1, 1, 128, (1 << 17) - 1, 64, 64), (1, 1, 128, 1 << 17, 64, 64), "2 GiB"),
+            ((8, 8, 256, 1 << 18, 16, 15), (8, 8, 256, 1 << 18, 16, 16), "2 GiB")]:
+        assert size(*inside) > 0, inside
+        assert size(*outside) == 0, outside
+        B, H, d_v, T, W, R = outside
+        a = list(ok)
+        a[0], a[1], a[3], a[4], a[5], a[6] = B, H, d_v, T, W, R
+        assert L.sdm_scan_backward8(*a) == 2 and word in _err()
+    # 164 GiB of workspace for a call that refuses
+    assert size(8, 8, 16, 1 << 21, 1, 1) == 0
