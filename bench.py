@@ -47,14 +47,25 @@ FP8_TRAFFIC_FILE = os.path.join(ROOT, "profiles", "scan_mid_fp8_traffic.json")
 LONG_PLANNED_TRAFFIC_FILE = os.path.join(ROOT, "profiles", "scan_long_planned_traffic.json")
 DECODE_TRAFFIC_FILE = os.path.join(ROOT, "profiles", "decode_traffic.json")
 _CSRC = os.path.join(ROOT, "sparse_memory_linear_sdm_amd", "csrc")
-SCAN_SOURCES = [os.path.join(_CSRC, f)
-                for f in ("scan.hip", "scan_rows.h", "ranges.h", "device_common.h")]
-BWD_SOURCES = [os.path.join(_CSRC, f) for f in ("backward.hip", "ranges.h", "device_common.h")]
-PROJ_SOURCES = [os.path.join(_CSRC, f) for f in ("project.hip", "device_common.h", "internal.h")]
-PLANNED_SOURCES = [os.path.join(_CSRC, f) for f in
-                   ("scan_planned.hip", "planned.h", "scan_rows.h", "ranges.h", "device_common.h")]
-DECODE_SOURCES = [os.path.join(_CSRC, f) for f in
-                  ("decode.hip", "select_wave.h", "device_common.h", "internal.h")]
+
+
+def _sources(kernel: str) -> list:
+    """A kernel's file and the library's files that it includes, itself or
+    through another of them."""
+    files = [os.path.join(_CSRC, kernel)]
+    for path in files:
+        with open(path, encoding="utf-8") as fh:
+            for name in re.findall(r'^#include "([^"/]+)"', fh.read(), flags=re.M):
+                if os.path.join(_CSRC, name) not in files:
+                    files.append(os.path.join(_CSRC, name))
+    return files
+
+
+SCAN_SOURCES = _sources("scan.hip")
+BWD_SOURCES = _sources("backward.hip")
+PROJ_SOURCES = _sources("project.hip")
+PLANNED_SOURCES = _sources("scan_planned.hip")
+DECODE_SOURCES = _sources("decode.hip")
 
 
 def _code_only(text: str) -> str:
