@@ -131,7 +131,9 @@ int sdm_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int dtype, i
  *           of each head).
  * Products of two elements are exact; each y is a binary32 sum of the d_model
  * of them, in an unspecified but fixed order, within sdm_project's bound.  A
- * token or weight row with a block of scale 255 gives NaN.  d_model is a
+ * token or weight row with a block of scale 255 gives NaN.  (The quantisation
+ * itself is no part of that bound: for normally distributed tokens and weights
+ * it moves y by about 17% of its norm, and the selections with it.)  d_model is a
  * multiple of 128 in [128, 65536]; every other size, and B*T = 0, as for
  * sdm_project.  Few tokens (a decode step) take a kernel of their own that
  * reads each weight once. */

@@ -90,7 +90,7 @@ struct Bwd8Args {
 
 // A set of rows as bits: three bits of one of kSetWords words per row (word
 // and bits from two multiplicative hashes).  Of 128 rows in the set, an absent
-// row is found about once in 10^4.
+// row is found about once in 3000.
 constexpr int kSetWords = 512;
 __device__ __forceinline__ uint32_t set_word(uint32_t row) { return (row * 2654435761u) >> 23; }
 __device__ __forceinline__ uint32_t set_bits(uint32_t row) {

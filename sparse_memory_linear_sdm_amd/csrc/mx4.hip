@@ -15,8 +15,8 @@
 // row at a time (8 values per lane: one 16-byte load of bf16, two of fp32), the
 // block maximum is two exchanges over the four lanes that share a block, and
 // the scale words are gathered in LDS so that the rows' words of each group go
-// out together.  32768 x 16384 bf16: 216 us, 6.4 TB/s, and 216 us back; 4226 x
-// 16384 fp32: 47 and 44 us.
+// out together.  32768 x 16384 bf16: 216-228 us (6.0-6.3 TB/s) and
+// 216-233 us back; 4226 x 16384 fp32: 47-50 and 44 us.
 #include "internal.h"
 #include "mx.h"
 

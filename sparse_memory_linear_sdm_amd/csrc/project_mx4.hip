@@ -18,7 +18,7 @@
 // wavefronts and the 34 KB that arrive), so the order inside a stage decides: a
 // matrix instruction, then two fragment reads or a load, and so on, against all
 // reads first, is 8.1 against 9.3 ms without the outputs.  32768 tokens x 33808
-// columns at d_model 16384: 9.1-9.4 ms, 3.9-4.0 PFLOP/s (bf16 tiles: 33 ms).
+// columns at d_model 16384: 9.1-9.8 ms, 3.7-4.0 PFLOP/s (bf16 tiles: 32 ms).
 // What bounds it: with no loads in flight the same loop reaches 5.9, bare
 // matrix instructions on random codes 6.3 (8.8 on zeros: the card's power limit
 // sets the clock), and the outputs' 4.4 GB take 1.0 ms that nothing overlaps.
@@ -304,7 +304,8 @@ __global__ __launch_bounds__(X::kThreads) void project_mx4_kernel(Mx4Args A) {
 // for 64 tokens at d_model 16384 x 33808 columns.  So four neighbouring lanes
 // load 64 bytes of a row, the turn's fragments pass through the wavefront's own
 // piece of LDS (16-byte segments swizzled as in the tiles), and the turn after
-// it is in flight in registers: 79 us, floor 63; one token 56 us.
+// it is in flight in registers: 79 us, 3.9 TB/s; one token, the weights' stream
+// and little else, 52 us, 5.7 TB/s.
 template <int MT, int CT>
 constexpr int few_waves() {  // the accumulators of 4 x 7 blocks and up leave room for four
   return MT * CT >= 28 ? 4 : 8;
