@@ -38,6 +38,7 @@ another GPU is refused.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -708,7 +709,7 @@ def state_init_backward(G, out=None, seen=None, stream=None):
 
 
 def scan_plan_workspace_size(B: int, H: int, d_v: int, T: int) -> int:
-    """Bytes of workspace scan_plan / scan_planned need (0: unsupported)."""
+    """Bytes of workspace scan_plan / scan_planned need on the current GPU (0: unsupported)."""
     return int(lib().sdm_scan_plan_workspace_size(B, H, d_v, T))
 
 
@@ -725,8 +726,9 @@ def scan_plan(widx, wk, ridx, rw, N: int, d_v: int, workspace=None, stream=None)
     f32 = torch.float32
     ins = [_arg(widx, torch.int32, (B, H, T, W), "widx"), _arg(wk, f32, (B, H, T, W), "wk"),
            _arg(ridx, torch.int32, (B, H, T, R), "ridx"), _arg(rw, f32, (B, H, T, R), "rw")]
-    need = scan_plan_workspace_size(B, H, d_v, T)
     if workspace is None:
+        with torch.cuda.device(widx.get_device()) if widx.is_cuda else contextlib.nullcontext():
+            need = scan_plan_workspace_size(B, H, d_v, T)
         workspace = _empty_on(stream, widx.device)((max(need, 256),), torch.uint8)
     ptrs = _gpu(*ins, _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()

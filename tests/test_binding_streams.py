@@ -198,3 +198,29 @@ def test_every_call_runs_on_its_tensors_gpu(name, monkeypatch):
     call(stream)
     call(None)
     assert seen == [("sdm_" + name, stream), ("sdm_" + name, None)]
+
+
+def test_a_plan_is_sized_for_its_tensors_gpu(two_gpus, monkeypatch):
+    """Shards, and so the workspace, are chosen from the GPU's compute units."""
+    asked = []
+
+    def size(*args):
+        asked.append((two_gpus[0], *args))
+        return 0
+
+    class On1(torch.Tensor):
+        """A CPU tensor that says it is on GPU 1."""
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    def on1(x):
+        return x.as_subclass(On1)
+
+    monkeypatch.setattr(sdm, "scan_plan_workspace_size", size)
+    monkeypatch.setattr(sdm, "_call", lambda *a: None)
+    monkeypatch.setattr(sdm, "_gpu", lambda *a: [None] * len(a))
+    i, w = torch.zeros(B, H, T, W, dtype=i32), torch.zeros(B, H, T, W)
+    sdm.scan_plan(on1(i), on1(w), on1(i), on1(w), N, d_v)
+    assert asked == [(1, B, H, d_v, T)] and two_gpus[0] == 0
