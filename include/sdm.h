@@ -420,6 +420,108 @@ int sdm_state_init_backward(const float* G, int B, int H, int64_t N, int d_v,
 int sdm_touch_prepare(int B, int H, int64_t N, int64_t T, int W, int R, const int32_t* widx,
                       const int32_t* ridx, uint32_t* seen, uint64_t* first, void* stream);
 
+/* ---- The dense recurrence with a decay for each head (linear attention): the
+ * dense state that the sparse table stands in place of ("Meccanismo Core",
+ * item 1; section "Problema").  Per memory (b,h), with S of d_k x d_v values:
+ *   S_t = exp(g_t) * S_{t-1} + k_t v_t^T;   out_t = S_t^T q_t  (after the write).
+ *   S     [B, H, d_k, d_v] fp32 state, updated in place.
+ *   q, k  [B, Hk, T, d_k], v, out [B, H, T, d_v] fp32 (dtype SDM_F32) or bf16
+ *         bits (SDM_BF16).  H is a multiple of Hk: head h takes the queries and
+ *         keys of head h / (H / Hk).  Queries are taken as they are (a factor
+ *         such as 1 / sqrt(d_k) is the caller's).
+ *   g     [B, H, T] fp32 logarithms of the decays, normally <= 0.  At or below
+ *         -128 (-infinity too) the step forgets the state: sequences can follow
+ *         one another in one row of T steps.
+ * Sums are fp32, states and decays hold fp32's precision for both types.  bf16:
+ * out is rounded once to bf16, from the state and the products q_t . k_s rounded
+ * to bf16 as operands of the matrix cores.  Every q, k, v and S has to be finite
+ * and products to stay in fp32's range: a NaN or an infinity spreads over all
+ * outputs of its chunk of steps (below), earlier ones too, and the later ones.
+ * d_k, d_v in {32, 64, 128}; B*H <= 2^20, T < 2^31.  S, q, k, v, out, tape and
+ * their gradients 16-byte aligned.  A sequence may be split over consecutive
+ * calls (equal up to the order of the fp32 sums). */
+
+/* Bytes of workspace for sdm_linear_scan (0 where none is needed, for many
+ * memories or few steps, and for sizes that are not supported): the states of
+ * the segments into which few memories' steps are cut. */
+size_t sdm_linear_scan_workspace_size(int dtype, int B, int H, int d_k, int d_v, int64_t T);
+
+/* T steps of every memory.
+ *   tape  NULL, or [B, H, ceil(T/C), d_k, d_v] fp32 out, for
+ *         sdm_linear_backward: the state before each chunk of C steps (C = 64
+ *         for SDM_BF16, 32 for SDM_F32).
+ *   workspace  device buffer of at least sdm_linear_scan_workspace_size bytes,
+ *         256-byte aligned (NULL if that is 0); its contents on entry do not
+ *         matter.
+ * T = 0 is a valid no-op (every array but S may then be NULL). */
+int sdm_linear_scan(float* S, int dtype, int B, int H, int Hk, int d_k, int d_v, int64_t T,
+                    const void* q, const void* k, const void* v, const float* g, void* out,
+                    float* tape, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of every memory (T = 1 without a time axis: q, k [B, Hk, d_k],
+ * v, out [B, H, d_v], g [B, H]), in fp32 throughout. */
+int sdm_linear_step(float* S, int dtype, int B, int H, int Hk, int d_k, int d_v, const void* q,
+                    const void* k, const void* v, const float* g, void* out, void* stream);
+
+/* Bytes of workspace for sdm_linear_backward (0 where none is needed, and for
+ * sizes that are not supported): segments' states as above and, with shared
+ * keys, fp32 gradients of q and k for every head. */
+size_t sdm_linear_backward_workspace_size(int dtype, int B, int H, int Hk, int d_k, int d_v,
+                                          int64_t T);
+
+/* Reverse pass of sdm_linear_scan from its tape (the state is not needed).
+ *   q, k, v, g  the forward's inputs;  dout [B, H, T, d_v] dL/d out, of dtype.
+ *   G      [B, H, d_k, d_v] fp32 in/out: in, dL/d(state after the last step);
+ *          out, dL/d(state before the first).
+ *   dq, dk [B, Hk, T, d_k] (summed over the heads that share them, in fp32),
+ *          dv [B, H, T, d_v] out, of dtype;  dg [B, H, T] fp32 out, dL/dg (0 for
+ *          steps that forget the state).
+ * dg and G hold fp32's precision for both types.  Results are deterministic.
+ * B*H*T <= 2^26 - 4.  T = 0 is a valid no-op (G unchanged; every other array may
+ * then be NULL).  workspace as for sdm_linear_scan. */
+int sdm_linear_backward(int dtype, int B, int H, int Hk, int d_k, int d_v, int64_t T,
+                        const void* q, const void* k, const void* v, const float* g,
+                        const float* tape, const void* dout, float* G, void* dq, void* dk,
+                        void* dv, float* dg, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* ---- Norms before and after a block, with its gate and residual scale.  Per
+ * row y of d values:
+ *   out = x + scale * silu(z) * w * y / sqrt(mean(y^2) + eps)
+ * with silu(z) = z / (1 + exp(-z)); z NULL: no gate; x NULL: no residual.
+ *   y     [B, H, T, d] fp32 (y_dtype SDM_F32) or bf16 bits (SDM_BF16): the
+ *         layout of the scans' outputs, normalised per head; H = 1 for plain
+ *         rows (B*T of them).
+ *   w     [d] fp32, the same for every head.
+ *   z, x, out  [B, T, H*d] of out_dtype: the layout that sdm_project takes.
+ *         out may be x.
+ *   next_w, next  NULL, or (H = 1) [d] fp32 and [B, T, d] of out_dtype: the norm
+ *         before the next block of the same row, next_w * out /
+ *         sqrt(mean(out^2) + eps), from out before its rounding.
+ * Arithmetic in fp32, each output rounded once.  d a multiple of 8 in
+ * [8, 16384]; B*H*T < 2^31; all arrays 16-byte aligned; eps >= 0.  No rows
+ * (B*T = 0) is a valid no-op (the arrays may then be NULL). */
+int sdm_norm(const void* y, int y_dtype, const float* w, const void* z, const void* x, float scale,
+             float eps, int B, int H, int64_t T, int d, void* out, int out_dtype,
+             const float* next_w, void* next, void* stream);
+
+/* Bytes of workspace for sdm_norm_backward (0 for sizes that are not supported). */
+size_t sdm_norm_backward_workspace_size(int B, int H, int64_t T, int d);
+
+/* Gradients of sdm_norm (dL/dx is dout itself; next's come from a call of its
+ * own with y = out, w = next_w and skip = dL/dout).
+ *   dout  [B, T, H*d] of out_dtype;  y, w, z, scale, eps as in the forward.
+ *   skip  NULL, or like y: a gradient that reaches y past the norm, added to dy.
+ *   dy    like y;  dw [d] fp32, the sum over all rows;  dz like z (NULL without z).
+ *   workspace  device buffer of at least sdm_norm_backward_workspace_size bytes,
+ *         256-byte aligned.
+ * dy may be skip.  Results are deterministic.  Without rows dw is 0 and every
+ * other array may be NULL. */
+int sdm_norm_backward(const void* dout, int out_dtype, const void* y, int y_dtype, const float* w,
+                      const void* z, const void* skip, float scale, float eps, int B, int H,
+                      int64_t T, int d, void* dy, float* dw, void* dz, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* sdm_status_string(int status);
 

@@ -29,6 +29,14 @@ Planned scan (fp32 state; few memories, long sequences):
   touch_prepare(widx, ridx, N) -> (seen, first)
   select_backward(idx, weight, dweight, n) -> (dx1, dx2)
   state_init_backward(G) -> dM0
+Dense recurrence with a decay for each head (fp32 or bf16; fp32 state):
+  linear_scan(S, q, k, v, g) -> out                       (S updated in place)
+  linear_step(S, q, k, v, g) -> out                       (one token)
+  linear_scan_train(S, q, k, v, g) -> (out, tape)
+  linear_backward(q, k, v, g, tape, dout, G) -> dict      (G updated in place)
+Norms before and after a block (fp32 or bf16):
+  norm(y, w, z, x, scale, eps) -> out, or (out, next) with next_w
+  norm_backward(dout, y, w, z, scale, eps, skip) -> dict
 
 stream= is a torch stream or a raw handle (None: the current stream).  Tensors
 that a call makes are allocated for that stream and marked as used by the
@@ -56,7 +64,9 @@ EXPORTS = ("sdm_project", "sdm_mx4_quantize", "sdm_mx4_dequantize", "sdm_project
            "sdm_scan_backward_workspace_size", "sdm_scan_backward", "sdm_scan_backward_noalloc",
            "sdm_select_backward", "sdm_scan_plan_workspace_size", "sdm_scan_plan",
            "sdm_scan_planned", "sdm_state_init_backward", "sdm_touch_prepare", "sdm_scan_train8", "sdm_tape8_read",
-           "sdm_scan_backward8", "sdm_scan_backward8_workspace_size", "sdm_status_string", "sdm_last_error",
+           "sdm_scan_backward8", "sdm_scan_backward8_workspace_size", "sdm_linear_scan_workspace_size", "sdm_linear_scan",
+           "sdm_linear_step", "sdm_linear_backward_workspace_size", "sdm_linear_backward", "sdm_norm",
+           "sdm_norm_backward_workspace_size", "sdm_norm_backward", "sdm_status_string", "sdm_last_error",
            "sdm_abi_version")
 
 _lib = None
@@ -111,13 +121,27 @@ def lib():
         L.sdm_scan_planned.argtypes = [p, i32, i32, i64, i32, i64] + [p] * 5 + [ctypes.c_size_t, p]
         L.sdm_select_backward.argtypes = [p, p, p, i64, i32, i32, p, p, p]
         L.sdm_state_init_backward.argtypes = [p, i32, i32, i64, i32, p, p, p]
+        f32, size = ctypes.c_float, ctypes.c_size_t
+        L.sdm_linear_scan_workspace_size.argtypes = [i32] * 5 + [i64]
+        L.sdm_linear_scan_workspace_size.restype = size
+        L.sdm_linear_scan.argtypes = [p] + [i32] * 6 + [i64] + [p] * 7 + [size, p]
+        L.sdm_linear_step.argtypes = [p] + [i32] * 6 + [p] * 6
+        L.sdm_linear_backward_workspace_size.argtypes = [i32] * 6 + [i64]
+        L.sdm_linear_backward_workspace_size.restype = size
+        L.sdm_linear_backward.argtypes = [i32] * 6 + [i64] + [p] * 12 + [size, p]
+        L.sdm_norm.argtypes = ([p, i32, p, p, p, f32, f32, i32, i32, i64, i32, p, i32] + [p] * 3)
+        L.sdm_norm_backward_workspace_size.argtypes = [i32, i32, i64, i32]
+        L.sdm_norm_backward_workspace_size.restype = size
+        L.sdm_norm_backward.argtypes = ([p, i32, p, i32, p, p, p, f32, f32, i32, i32, i64, i32] +
+                                        [p] * 4 + [size, p])
         for f in ("sdm_project", "sdm_mx4_quantize", "sdm_mx4_dequantize", "sdm_project_mx4",
                   "sdm_select", "sdm_state_init", "sdm_scan", "sdm_step_decode",
                   "sdm_abi_version", "sdm_scan_train", "sdm_scan_backward",
                   "sdm_scan_backward_noalloc",
                   "sdm_select_backward", "sdm_state_init_backward", "sdm_touch_prepare",
                   "sdm_scan_plan", "sdm_scan_planned", "sdm_scan_train8", "sdm_tape8_read",
-                  "sdm_scan_backward8"):
+                  "sdm_scan_backward8", "sdm_linear_scan", "sdm_linear_step",
+                  "sdm_linear_backward", "sdm_norm", "sdm_norm_backward"):
             getattr(L, f).restype = ctypes.c_int
         L.sdm_status_string.argtypes = [i32]
         L.sdm_status_string.restype = ctypes.c_char_p
@@ -754,4 +778,197 @@ def scan_planned(M, v, alpha, beta, workspace, out=None, stream=None):
                 _arg(out, f32, (B, H, T, d_v), "out"), _arg(workspace, None, None, "workspace"))
     nbytes = workspace.numel() * workspace.element_size()
     _call(lib().sdm_scan_planned, M, stream, ptrs[0], B, H, N, d_v, T, *ptrs[1:], nbytes)
+    return out
+
+
+def _linear_args(S, name, q, k, v, g, time):
+    """Checked arguments of a call on the dense recurrence's state S (or its
+    gradient), named `name`: dtype code, sizes and the tensors' pairs."""
+    import torch
+
+    f32 = torch.float32
+    if S.dim() != 4:
+        raise ValueError(f"{name} must be [B, H, d_k, d_v], got {tuple(S.shape)}")
+    if q.dim() != 3 + time:
+        raise ValueError("q and k must be " + ("[B, Hk, T, d_k]" if time else "[B, Hk, d_k]"))
+    B, H, d_k, d_v = S.shape
+    Hk = q.shape[1]
+    T = (q.shape[2],) if time else ()
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{name} has {H} heads, not a multiple of q's {Hk}")
+    args = [_arg(S, f32, (B, H, d_k, d_v), name), _arg(q, q.dtype, (B, Hk, *T, d_k), "q"),
+            _arg(k, q.dtype, (B, Hk, *T, d_k), "k"), _arg(v, q.dtype, (B, H, *T, d_v), "v"),
+            _arg(g, f32, (B, H, *T), "g")]
+    return _value_dtype(q.dtype), (B, H, Hk, d_k, d_v, *T), args
+
+
+def _workspace(workspace, need, empty):
+    """(name, tensor) and bytes of a call's workspace, made unless the caller
+    gives one; (None, 0) where the call needs none."""
+    import torch
+
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = empty((need,), torch.uint8, mine=True)
+    return (_arg(workspace, None, None, "workspace"),
+            workspace.numel() * workspace.element_size())
+
+
+def _linear_tape(dtype, T):
+    """Chunks of T steps (one state of the tape each)."""
+    chunk = 64 if dtype == SDM_BF16 else 32
+    return (T + chunk - 1) // chunk
+
+
+def _linear_scan(S, q, k, v, g, out, tape, want_tape, workspace, stream):
+    import torch
+
+    dt, sizes, args = _linear_args(S, "S", q, k, v, g, True)
+    B, H, Hk, d_k, d_v, T = sizes
+    empty = _empty_on(stream, S.device)
+    if out is None:
+        out = empty((B, H, T, d_v), q.dtype)
+    outs = [_arg(out, q.dtype, (B, H, T, d_v), "out"), None]
+    if want_tape:
+        shape = (B, H, _linear_tape(dt, T), d_k, d_v)
+        if tape is None:
+            tape = empty(shape, torch.float32)
+        outs[1] = _arg(tape, torch.float32, shape, "tape")
+    ws, nbytes = _workspace(
+        workspace, int(lib().sdm_linear_scan_workspace_size(dt, B, H, d_k, d_v, T)), empty)
+    pS, *ptrs = _gpu(*args, *outs, ws)
+    _call(lib().sdm_linear_scan, S, stream, pS, dt, *sizes, *ptrs, nbytes)
+    return out, tape
+
+
+def linear_scan(S, q, k, v, g, out=None, workspace=None, stream=None):
+    """T steps of the dense recurrence S_t = exp(g_t) S_{t-1} + k_t v_t^T,
+    out_t = S_t^T q_t on S [B,H,d_k,d_v] (fp32, in place).  q, k [B,Hk,T,d_k]
+    (Hk divides H: heads share them in order) and v [B,H,T,d_v], float32 or
+    bfloat16; g [B,H,T] float32, normally <= 0 (-inf: the step forgets the
+    state).  Returns out [B,H,T,d_v] of q's type."""
+    return _linear_scan(S, q, k, v, g, out, None, False, workspace, stream)[0]
+
+
+def linear_scan_train(S, q, k, v, g, out=None, tape=None, workspace=None, stream=None):
+    """linear_scan() that also keeps the state before each chunk of C steps (64
+    for bfloat16, 32 for float32): returns (out, tape [B,H,ceil(T/C),d_k,d_v])."""
+    return _linear_scan(S, q, k, v, g, out, tape, True, workspace, stream)
+
+
+def linear_step(S, q, k, v, g, out=None, stream=None):
+    """One token of every memory: linear_scan() without a time axis (q, k
+    [B,Hk,d_k]; v [B,H,d_v]; g [B,H]).  Returns out [B,H,d_v]."""
+    dt, sizes, args = _linear_args(S, "S", q, k, v, g, False)
+    shape = (sizes[0], sizes[1], sizes[4])
+    if out is None:
+        out = _empty_on(stream, S.device)(shape, q.dtype)
+    pS, *ptrs = _gpu(*args, _arg(out, q.dtype, shape, "out"))
+    _call(lib().sdm_linear_step, S, stream, pS, dt, *sizes, *ptrs)
+    return out
+
+
+def linear_backward(q, k, v, g, tape, dout, G, workspace=None, out=None, stream=None):
+    """Reverse pass of linear_scan_train: G [B,H,d_k,d_v] (dL/d final state)
+    becomes dL/d initial state in place.  Returns a dict dq, dk [B,Hk,T,d_k], dv
+    [B,H,T,d_v] of q's type and dg [B,H,T] float32.  out = such a dict writes
+    into caller tensors."""
+    import torch
+
+    f32 = torch.float32
+    dt, sizes, (aG, *ins) = _linear_args(G, "G", q, k, v, g, True)
+    B, H, Hk, d_k, d_v, T = sizes
+    ins += [_arg(tape, f32, (B, H, _linear_tape(dt, T), d_k, d_v), "tape"),
+            _arg(dout, q.dtype, (B, H, T, d_v), "dout"), aG]
+    shapes = {"dq": (q.dtype, (B, Hk, T, d_k)), "dk": (q.dtype, (B, Hk, T, d_k)),
+              "dv": (q.dtype, (B, H, T, d_v)), "dg": (f32, (B, H, T))}
+    empty = _empty_on(stream, G.device)
+    if out is None:
+        out = {n: empty(shape, t) for n, (t, shape) in shapes.items()}
+    ins += [_arg(out[n], t, shape, n) for n, (t, shape) in shapes.items()]
+    ws, nbytes = _workspace(
+        workspace, int(lib().sdm_linear_backward_workspace_size(dt, *sizes)), empty)
+    ptrs = _gpu(*ins, ws)
+    _call(lib().sdm_linear_backward, G, stream, dt, *sizes, *ptrs, nbytes)
+    return out
+
+
+def _norm_sizes(y, heads):
+    """(B, H, T, d) and the shape of the outputs of rows y."""
+    if heads:
+        if y.dim() != 4:
+            raise ValueError(f"y must be [B, H, T, d], got {tuple(y.shape)}")
+        B, H, T, d = y.shape
+        return (B, H, T, d), (B, T, H * d)
+    if y.dim() < 1:
+        raise ValueError("y must have a last dimension d")
+    return (1, 1, _units(y.shape[:-1]), y.shape[-1]), tuple(y.shape)
+
+
+def norm(y, w, z=None, x=None, scale: float = 1.0, eps: float = 1e-6, dtype=None, next_w=None,
+         heads: bool = False, out=None, stream=None):
+    """x + scale * silu(z) * w * y / sqrt(mean(y^2) + eps) per row of y [..., d]
+    (float32 or bfloat16); w [d] float32; gate z and residual x may be None.
+    heads=True: y is [B,H,T,d], normalised per head, and z, x and out are
+    [B,T,H*d]; otherwise they are shaped as y.  They have one type: dtype, or
+    x's, z's or y's.  With next_w [d] (not with heads=True) returns (out, next):
+    the next block's norm of the same rows.  out = a tensor (or that pair)
+    writes into caller tensors; it may be x."""
+    import torch
+
+    sizes, shape = _norm_sizes(y, heads)
+    B, H, T, d = sizes
+    if next_w is not None and heads:
+        raise ValueError("next_w needs whole rows (heads=False)")
+    if dtype is None:
+        dtype = next((t.dtype for t in (x, z) if t is not None), y.dtype)
+    ty, to = _value_dtype(y.dtype), _value_dtype(dtype)
+    behind = None
+    if out is None:
+        empty = _empty_on(stream, y.device)
+        out = empty(shape, dtype)
+        behind = empty(shape, dtype) if next_w is not None else None
+    elif next_w is not None:
+        out, behind = out
+    like = [None if t is None else _arg(t, dtype, shape, n) for n, t in (("z", z), ("x", x))]
+    py, pw, pz, px, po, pnw, pn = _gpu(
+        _arg(y, y.dtype, tuple(y.shape), "y"), _arg(w, torch.float32, (d,), "w"), *like,
+        _arg(out, dtype, shape, "out"),
+        None if next_w is None else _arg(next_w, torch.float32, (d,), "next_w"),
+        None if next_w is None else _arg(behind, dtype, shape, "next"))
+    _call(lib().sdm_norm, y, stream, py, ty, pw, pz, px, scale, eps, B, H, T, d, po, to, pnw, pn)
+    return out if next_w is None else (out, behind)
+
+
+def norm_backward(dout, y, w, z=None, scale: float = 1.0, eps: float = 1e-6, skip=None,
+                  heads: bool = False, workspace=None, out=None, stream=None):
+    """Gradients of norm(): a dict dy (like y), dw [d] float32 and, with a gate,
+    dz (like z); the residual's is dout itself.  skip (like y) is a gradient
+    that reaches y past the norm, added to dy.  dout and z have one type.
+    out = such a dict writes into caller tensors."""
+    import torch
+
+    sizes, shape = _norm_sizes(y, heads)
+    B, H, T, d = sizes
+    ty, to = _value_dtype(y.dtype), _value_dtype(dout.dtype)
+    at = tuple(y.shape)
+    ins = [_arg(dout, dout.dtype, shape, "dout"), _arg(y, y.dtype, at, "y"),
+           _arg(w, torch.float32, (d,), "w"),
+           None if z is None else _arg(z, dout.dtype, shape, "z"),
+           None if skip is None else _arg(skip, y.dtype, at, "skip")]
+    empty = _empty_on(stream, y.device)
+    shapes = {"dy": (y.dtype, at), "dw": (torch.float32, (d,))}
+    if z is not None:
+        shapes["dz"] = (dout.dtype, shape)
+    if out is None:
+        out = {n: empty(s, t) for n, (t, s) in shapes.items()}
+    outs = [_arg(out[n], t, s, n) for n, (t, s) in shapes.items()]
+    if z is None:
+        outs.append(None)
+    ws, nbytes = _workspace(
+        workspace, int(lib().sdm_norm_backward_workspace_size(B, H, T, d)), empty)
+    po, py, pw, pz, pskip, *outs = _gpu(*ins, *outs, ws)
+    _call(lib().sdm_norm_backward, y, stream, po, to, py, ty, pw, pz, pskip, scale, eps, B, H, T,
+          d, *outs, nbytes)
     return out

@@ -16,7 +16,9 @@ LIB = os.path.join(HERE, "libsdm.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "api_mx.hip", "select.hip", "scan.hip", "init.hip", "decode.hip",
            "backward.hip", "scratch.hip", "project.hip", "scan_planned.hip", "mx4.hip",
-           "project_mx4.hip", "tape8.hip", "backward8.hip"]
+           "project_mx4.hip", "tape8.hip", "backward8.hip", "api_dense.hip", "linear.hip",
+           "linear_bf16.hip", "linear_f32.hip", "linear_backward_bf16.hip",
+           "linear_backward_f32.hip", "norm.hip"]
 HIPCC = "/opt/rocm/bin/hipcc"
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

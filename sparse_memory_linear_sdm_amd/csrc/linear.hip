@@ -1,0 +1,260 @@
+// The dense recurrence with a decay for each head: the host side of the chunked
+// kernels, the sums over segments and over heads that share keys, and the step
+// of a single token.
+#include "dense.h"
+#include "linear_tile.h"
+
+namespace sdm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// What each segment starts from: the call's state carried through the
+// segments before it (behind it, in reverse).  seg_state[m][i] holds what
+// segment i adds; afterwards what it starts from.
+__global__ __launch_bounds__(kThreads) void linear_segments_kernel(float* seg_state,
+                                                                   const double* seg_log,
+                                                                   const float* S, int64_t total,
+                                                                   int elems, int nseg,
+                                                                   bool reverse) {
+  const int64_t at = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (at >= total) return;
+  const int64_t m = at / elems, e = at % elems;
+  f32x4 run = *reinterpret_cast<const f32x4*>(S + at);
+  float* p = seg_state + m * nseg * elems + e;
+  const double* lg = seg_log + m * nseg;
+  constexpr int kAhead = 8;
+  for (int i0 = 0; i0 < nseg; i0 += kAhead) {
+    f32x4 own[kAhead];
+    float decay[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = reverse ? nseg - 1 - (i0 + j) : i0 + j;
+      if (i0 + j < nseg - 1) {  // the last of the order passes nothing on
+        own[j] = *reinterpret_cast<const f32x4*>(p + (int64_t)i * elems);
+        decay[j] = exp2f((float)lg[i]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = reverse ? nseg - 1 - (i0 + j) : i0 + j;
+      if (i0 + j < nseg) *reinterpret_cast<f32x4*>(p + (int64_t)i * elems) = run;
+      if (i0 + j < nseg - 1) run = run * decay[j] + own[j];
+    }
+  }
+}
+
+// Gradients of shared keys: the sum over the heads that share them, in their
+// order, rounded once.
+template <class T>
+__global__ __launch_bounds__(kThreads) void linear_share_kernel(const float* part, T* out,
+                                                                int64_t total, int64_t per_head,
+                                                                int share) {
+  const int64_t at = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (at >= total) return;
+  const float* p = part + at / per_head * per_head * share + at % per_head;
+  f32x4 sum = *reinterpret_cast<const f32x4*>(p);
+  for (int i = 1; i < share; ++i) sum += *reinterpret_cast<const f32x4*>(p + i * per_head);
+  lin::Tile<T>::store4(out + at, sum);
+}
+
+template <class T>
+hipError_t launch_share(const float* part, void* out, int64_t key_heads, int64_t per_head,
+                        int share, hipStream_t stream) {
+  const int64_t total = key_heads * per_head;
+  hipLaunchKernelGGL((linear_share_kernel<T>), dim3((unsigned)((total / 4 + kThreads - 1) / kThreads)),
+                     dim3(kThreads), 0, stream, part, (T*)out, total, per_head, share);
+  return hipGetLastError();
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+size_t segment_bytes(int64_t BH, int nseg, int elems) {
+  if (nseg == 1) return 0;
+  return align256((size_t)BH * nseg * elems * 4) + align256((size_t)BH * nseg * 8);
+}
+
+void place_segments(LinearArgs& a, int elems, char*& ws) {
+  if (a.nseg == 1) return;
+  a.seg_state = (float*)ws;
+  ws += align256((size_t)a.BH * a.nseg * elems * 4);
+  a.seg_log = (double*)ws;
+  ws += align256((size_t)a.BH * a.nseg * 8);
+}
+
+hipError_t launch_segments(const LinearArgs& a, int elems, bool reverse, hipStream_t stream) {
+  const int64_t total = (int64_t)a.BH * elems;
+  hipLaunchKernelGGL(linear_segments_kernel, dim3((unsigned)((total / 4 + kThreads - 1) / kThreads)),
+                     dim3(kThreads), 0, stream, a.seg_state, a.seg_log, a.S, total, elems, a.nseg,
+                     reverse);
+  return hipGetLastError();
+}
+
+hipError_t launch_chunks(const LinearArgs& a, int dtype, int d_k, int d_v, int mode,
+                         hipStream_t stream) {
+  return dtype == 1 ? launch_linear_bf16(a, d_k, d_v, mode, stream)
+                    : launch_linear_f32(a, d_k, d_v, mode, stream);
+}
+
+void set_segments(LinearArgs& a, int dtype, bool backward) {
+  const int chunk = linear_chunk(dtype);
+  a.nchunk = (int)((a.T + chunk - 1) / chunk);
+  a.nseg = linear_segments(dtype, a.BH, a.T, backward);
+  a.seg_chunks = (a.nchunk + a.nseg - 1) / a.nseg;
+  a.nseg = (a.nchunk + a.seg_chunks - 1) / a.seg_chunks;
+}
+
+// ---- one token of every memory: S = exp(g) S + k v^T, out = S^T q.  Bound by
+// the state, read and written once.  A workgroup takes all rows of CT columns;
+// its loads are in flight together.
+template <class T, int DK, int DV, int CT>
+__global__ __launch_bounds__(kThreads) void linear_step_kernel(float* S, const T* q, const T* k,
+                                                               const T* v, const float* g, T* out,
+                                                               int share) {
+  constexpr int kLanes = CT / 4;                 // lanes of a row piece
+  constexpr int kRows = kThreads / kLanes;       // rows at a time
+  constexpr int kN = DK / kRows;
+  static_assert(DK % kRows == 0, "whole passes");
+  __shared__ float sq[DK], sk[DK];
+  __shared__ f32x4 sum[kThreads / kWave][kLanes < kWave ? kLanes : kWave];
+  const int tid = threadIdx.x;
+  const int64_t m = blockIdx.x / (DV / CT);
+  const int c0 = (int)(blockIdx.x % (DV / CT)) * CT + (tid % kLanes) * 4;
+  const int r0 = tid / kLanes;
+  float* Sm = S + m * DK * DV + c0;
+  f32x4 s[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+    s[i] = *reinterpret_cast<const f32x4*>(Sm + (r0 + i * kRows) * DV);
+  const int64_t key = m / share * DK;
+  if (tid < DK / 4) {
+    const f32x4 a = lin::Tile<T>::load4(q + key + tid * 4);
+    *reinterpret_cast<f32x4*>(sq + tid * 4) = a;
+  } else if (tid >= kThreads - DK / 4) {
+    const int i = tid - (kThreads - DK / 4);
+    *reinterpret_cast<f32x4*>(sk + i * 4) = lin::Tile<T>::load4(k + key + i * 4);
+  }
+  const f32x4 vv = lin::Tile<T>::load4(v + m * DV + c0);
+  const float a = expf(g[m]);
+  __syncthreads();
+  f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int r = r0 + i * kRows;
+    s[i] = s[i] * a + vv * sk[r];
+    *reinterpret_cast<f32x4*>(Sm + r * DV) = s[i];
+    o += s[i] * sq[r];
+  }
+  // rows of the wavefront, then its sums in their order
+#pragma unroll
+  for (int x = kLanes; x < kWave; x <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] += __shfl_xor(o[j], x);
+  const int lane = lane_id(), w = tid / kWave;
+  if (lane < kLanes) sum[w][lane] = o;
+  __syncthreads();
+  if (tid < kLanes) {
+    o = sum[0][tid];
+#pragma unroll
+    for (int i = 1; i < kThreads / kWave; ++i) o += sum[i][tid];
+    lin::Tile<T>::store4(out + m * DV + c0, o);
+  }
+}
+
+template <class T, int DK, int DV>
+hipError_t launch_step(float* S, int BH, int share, const void* q, const void* k, const void* v,
+                       const float* g, void* out, hipStream_t stream) {
+  constexpr int CT = 32;
+  hipLaunchKernelGGL((linear_step_kernel<T, DK, DV, CT>), dim3((unsigned)BH * (DV / CT)),
+                     dim3(kThreads), 0, stream, S, (const T*)q, (const T*)k, (const T*)v, g,
+                     (T*)out, share);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_step_type(float* S, int BH, int share, int d_k, int d_v, const void* q,
+                            const void* k, const void* v, const float* g, void* out,
+                            hipStream_t s) {
+  switch (d_k * 1000 + d_v) {
+    case 32032: return launch_step<T, 32, 32>(S, BH, share, q, k, v, g, out, s);
+    case 32064: return launch_step<T, 32, 64>(S, BH, share, q, k, v, g, out, s);
+    case 32128: return launch_step<T, 32, 128>(S, BH, share, q, k, v, g, out, s);
+    case 64032: return launch_step<T, 64, 32>(S, BH, share, q, k, v, g, out, s);
+    case 64064: return launch_step<T, 64, 64>(S, BH, share, q, k, v, g, out, s);
+    case 64128: return launch_step<T, 64, 128>(S, BH, share, q, k, v, g, out, s);
+    case 128032: return launch_step<T, 128, 32>(S, BH, share, q, k, v, g, out, s);
+    case 128064: return launch_step<T, 128, 64>(S, BH, share, q, k, v, g, out, s);
+    default: return launch_step<T, 128, 128>(S, BH, share, q, k, v, g, out, s);
+  }
+}
+
+}  // namespace
+
+int linear_segments(int dtype, int64_t BH, int64_t T, bool backward) {
+  const int64_t chunks = (T + linear_chunk(dtype) - 1) / linear_chunk(dtype);
+  const int64_t want = (512 + BH - 1) / BH, most = chunks / 4;
+  const int64_t n = want < most ? want : most;
+  return n < 1 ? 1 : (int)n;
+}
+
+size_t linear_scan_workspace_bytes(int dtype, int64_t BH, int d_k, int d_v, int64_t T) {
+  return segment_bytes(BH, linear_segments(dtype, BH, T, false), d_k * d_v);
+}
+
+size_t linear_backward_workspace_bytes(int dtype, int64_t BH, int share, int d_k, int d_v,
+                                       int64_t T) {
+  const size_t part = share > 1 ? 2 * align256((size_t)BH * T * d_k * 4) : 0;
+  return part + segment_bytes(BH, linear_segments(dtype, BH, T, true), d_k * d_v);
+}
+
+hipError_t launch_linear_scan(LinearArgs a, int dtype, int d_k, int d_v, void* ws,
+                              hipStream_t stream) {
+  set_segments(a, dtype, false);
+  char* p = (char*)ws;
+  place_segments(a, d_k * d_v, p);
+  hipError_t rc;
+  if (a.nseg > 1) {
+    if ((rc = launch_chunks(a, dtype, d_k, d_v, 1, stream)) != hipSuccess) return rc;
+    if ((rc = launch_segments(a, d_k * d_v, false, stream)) != hipSuccess) return rc;
+  }
+  return launch_chunks(a, dtype, d_k, d_v, 0, stream);
+}
+
+hipError_t launch_linear_backward(LinearArgs a, int dtype, int d_k, int d_v, void* ws,
+                                  hipStream_t stream) {
+  set_segments(a, dtype, true);
+  char* p = (char*)ws;
+  place_segments(a, d_k * d_v, p);
+  const int64_t per_head = a.T * d_k;
+  if (a.share > 1) {
+    a.dq_part = (float*)p;
+    p += align256((size_t)a.BH * per_head * 4);
+    a.dk_part = (float*)p;
+  }
+  hipError_t rc;
+  if (a.nseg > 1) {
+    if ((rc = launch_chunks(a, dtype, d_k, d_v, 2, stream)) != hipSuccess) return rc;
+    if ((rc = launch_segments(a, d_k * d_v, true, stream)) != hipSuccess) return rc;
+  }
+  rc = dtype == 1 ? launch_linear_backward_bf16(a, d_k, d_v, stream)
+                  : launch_linear_backward_f32(a, d_k, d_v, stream);
+  if (rc != hipSuccess || a.share == 1) return rc;
+  const int64_t key_heads = a.BH / a.share;
+  for (int i = 0; i < 2 && rc == hipSuccess; ++i) {
+    const float* part = i ? a.dk_part : a.dq_part;
+    void* out = i ? a.dk : a.dq;
+    rc = dtype == 1 ? launch_share<uint16_t>(part, out, key_heads, per_head, a.share, stream)
+                    : launch_share<float>(part, out, key_heads, per_head, a.share, stream);
+  }
+  return rc;
+}
+
+hipError_t launch_linear_step(float* S, int dtype, int BH, int share, int d_k, int d_v,
+                              const void* q, const void* k, const void* v, const float* g,
+                              void* out, hipStream_t stream) {
+  return dtype == 1
+             ? launch_step_type<uint16_t>(S, BH, share, d_k, d_v, q, k, v, g, out, stream)
+             : launch_step_type<float>(S, BH, share, d_k, d_v, q, k, v, g, out, stream);
+}
+
+}  // namespace sdm

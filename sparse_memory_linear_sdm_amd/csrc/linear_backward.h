@@ -1,0 +1,367 @@
+// Reverse pass of the dense recurrence with a decay for each head, in the
+// forward's chunks (linear_scan.h), last to first.  With S the state before a
+// chunk (from the tape), G the gradient of the state behind it, C its last
+// step, L_t the sum of g through step t, D_ts = exp(L_t - L_s) for s <= t and
+// 0 above:
+//   dq_t = exp(L_t) S do_t         + sum over s of (do_t . v_s) D_ts k_s
+//   dk_s = exp(L_C - L_s) G v_s    + sum over t of (do_t . v_s) D_ts q_t
+//   dv_s = exp(L_C - L_s) G^T k_s  + sum over t of (q_t . k_s) D_ts do_t
+//   G'   = exp(L_C) G              + sum over t of exp(L_t) q_t do_t^T
+// A step's decay scales every path from a step before it to one at or after
+// it, so its gradient is the sum of those paths:
+//   dg_t = sum over i >= t > j of W_ij, W_ij = (q_i . k_j)(do_i . v_j) D_ij
+//        + sum over i >= t of e_i      e_i = exp(L_i) q_i . S do_i
+//        + sum over j < t of f_j       f_j = exp(L_C - L_j) k_j . G v_j
+//        + exp(L_C) <S, G>
+// Nothing here cancels over more than one chunk; the first line is taken as
+// the difference of the rows' and columns' sums of W behind t.
+//
+// One workgroup walks a memory's chunks (or a segment's).  G is kept twice in
+// its accumulators, by rows of k and by rows of v: it enters products along
+// either index, and an accumulator tile is an operand along its rows.  Each
+// wavefront holds 16 columns of both.
+#pragma once
+#include "dense.h"
+#include "linear_tile.h"
+
+namespace sdm {
+namespace lin {
+
+template <class T, int DK, int DV>
+struct BackwardShape {
+  static constexpr int kWaves = DK == 128 || DV == 128 ? 8 : 4;
+  static constexpr int kThreads = kWaves * kWave;
+};
+
+template <class T, int DK, int DV>
+__global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_backward_kernel(
+    LinearArgs A) {
+  typedef Tile<T> X;
+  typedef typename X::Frag Frag;
+  constexpr int C = X::kChunk;
+  constexpr int NW = BackwardShape<T, DK, DV>::kWaves, NT = NW * kWave;
+  typedef Block<T, DK, NT> BlockK;
+  typedef Block<T, DV, NT> BlockV;
+  constexpr int ldk = BlockK::kLd, ldv = BlockV::kLd, ldp = C + X::kPad;
+  constexpr int kTT = C / 16, kKT = DK / 16, kVT = DV / 16;
+  static_assert(kKT <= NW && kVT <= NW, "one column tile a wavefront");
+  __shared__ __align__(16) T sq[C * ldk];
+  __shared__ __align__(16) T sk[C * ldk];
+  __shared__ __align__(16) T sv[C * ldv];
+  __shared__ __align__(16) T so[C * ldv];   // dout
+  __shared__ __align__(16) T sp[C * ldp];   // (q_t . k_s) D_ts, rows t
+  __shared__ __align__(16) T sdp[C * ldp];  // (do_t . v_s) D_ts, rows t
+  __shared__ Decays<C> sd[2];
+  __shared__ float srow[kTT][C], scol[kTT][C];  // sums of W by tiles
+  __shared__ float se[kKT][C], sf[kKT][C], sx[kKT];
+
+  const int lane = lane_id(), col = lane & 15, g4 = 4 * (lane >> 4);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t pid = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int bh = (int)(pid / A.nseg), seg = (int)(pid % A.nseg);
+  const int c_first = seg * A.seg_chunks;
+  const int c_end = c_first + A.seg_chunks < A.nchunk ? c_first + A.seg_chunks : A.nchunk;
+  const int64_t key_row = (int64_t)(bh / A.share) * A.T, row = (int64_t)bh * A.T;
+  const T* gq = (const T*)A.q + key_row * DK;
+  const T* gk = (const T*)A.k + key_row * DK;
+  const T* gv = (const T*)A.v + row * DV;
+  const T* go = (const T*)A.dout + row * DV;
+  const float* gg = A.g + row;
+  const bool has_k = w < kKT, has_v = w < kVT;
+  const int k0 = w * 16, v0 = w * 16;  // this wavefront's columns of k and of v
+
+  f32x4 Gk[kKT];  // rows of k, columns v0 .. v0 + 15
+  f32x4 Gv[kVT];  // rows of v, columns k0 .. k0 + 15
+  const float* from = A.nseg > 1 ? A.seg_state + ((int64_t)bh * A.nseg + seg) * DK * DV
+                                 : A.S + (int64_t)bh * DK * DV;
+#pragma unroll
+  for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      Gk[kt][i] = has_v ? from[(kt * 16 + g4 + i) * DV + v0 + col] : 0.0f;
+#pragma unroll
+  for (int vt = 0; vt < kVT; ++vt) {
+    Gv[vt] = f32x4{0, 0, 0, 0};
+    if (has_k) Gv[vt] = *reinterpret_cast<const f32x4*>(from + (k0 + col) * DV + vt * 16 + g4);
+  }
+
+  BlockK bq, bk;
+  BlockV bv, bo;
+  auto rows_of = [&](int c) {
+    const int64_t left = A.T - (int64_t)c * C;
+    return left < C ? (int)left : C;
+  };
+  auto load = [&](int c) {
+    const int64_t t0 = (int64_t)c * C;
+    const int valid = rows_of(c);
+    bq.load(gq + t0 * DK, valid);
+    bk.load(gk + t0 * DK, valid);
+    bv.load(gv + t0 * DV, valid);
+    bo.load(go + t0 * DV, valid);
+  };
+  auto step_log = [&](int c) {
+    return lane < rows_of(c) ? log2_decay(gg[(int64_t)c * C + lane]) : 0.0;
+  };
+  load(c_end - 1);
+  if (w == NW - 1) scan_decays<C>(step_log(c_end - 1), sd[(c_end - 1) & 1]);
+
+  for (int c = c_end - 1; c >= c_first; --c) {
+    const Decays<C>& d = sd[c & 1];
+    const int64_t t0 = (int64_t)c * C;
+    const int valid = rows_of(c);
+    bq.store(sq);
+    bk.store(sk);
+    bv.store(sv);
+    bo.store(so);
+    // the state before the chunk, rows k0 .. k0 + 15, as operands along v
+    f32x8 S[DV / 32];
+    if (has_k) {
+      const float* tape = A.tape + ((int64_t)bh * A.nchunk + c) * DK * DV + (k0 + col) * DV + g4;
+#pragma unroll
+      for (int vb = 0; vb < DV / 32; ++vb)
+        S[vb] = Tile<float>::pack(*reinterpret_cast<const f32x4*>(tape + vb * 32),
+                                  *reinterpret_cast<const f32x4*>(tape + vb * 32 + 16));
+    }
+    __syncthreads();
+    double next_log = 0.0;
+    if (c > c_first) {
+      load(c - 1);
+      if (w == NW - 1) next_log = step_log(c - 1);
+    }
+    // ---- pairs of steps: P, dP and the sums of W
+    constexpr int kUnits = kTT == 4 ? 12 : 4;
+    for (int u = w; u < kUnits; u += NW) {
+      const int tt = u < 4 ? u >> 1 : 2 + ((u - 4) >> 2), st = u < 4 ? u & 1 : (u - 4) & 3;
+      f32x4 p = {0, 0, 0, 0}, dp = {0, 0, 0, 0};
+      const int t = tt * 16 + col, s = st * 16 + g4;
+      if (st <= tt) {
+#pragma unroll
+        for (int kb = 0; kb < DK / 32; ++kb)
+          p = X::mma(X::rows(sk, ldk, st * 16, kb * 32), X::rows(sq, ldk, tt * 16, kb * 32), p);
+#pragma unroll
+        for (int vb = 0; vb < DV / 32; ++vb)
+          dp = X::mma(X::rows(sv, ldv, st * 16, vb * 32), X::rows(so, ldv, tt * 16, vb * 32), dp);
+        float by_row = 0.0f, by_col[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float dec = s + j <= t ? decay_between<C>(d, t, s + j) : 0.0f;
+          const float W = s + j < t ? p[j] * dp[j] * dec : 0.0f;
+          p[j] = s + j <= t ? p[j] * dec : 0.0f;
+          dp[j] = s + j <= t ? dp[j] * dec : 0.0f;
+          by_row += W;
+          by_col[j] = W;
+        }
+        by_row += __shfl_xor(by_row, 16);
+        by_row += __shfl_xor(by_row, 32);
+        if (lane < 16) srow[st][t] = by_row;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1)
+            by_col[j] += __uint_as_float(lane_xor(__float_as_uint(by_col[j]), o));
+          if (col == 0) scol[tt][s + j] = by_col[j];
+        }
+      }
+      X::store4(sp + t * ldp + s, p);
+      X::store4(sdp + t * ldp + s, dp);
+    }
+    if (c > c_first && w == NW - 1) scan_decays<C>(next_log, sd[(c - 1) & 1]);
+    // ---- the state's parts of the gradients, transposed: a lane holds four
+    // consecutive values of one step
+    f32x4 dq[kTT], dk[kTT], dv[kTT];
+#pragma unroll
+    for (int i = 0; i < kTT; ++i) dq[i] = dk[i] = dv[i] = f32x4{0, 0, 0, 0};
+    if (has_k) {
+      float x = 0.0f;
+#pragma unroll
+      for (int vb = 0; vb < DV / 32; ++vb) {
+        // S and G enter dg with fp32's precision, in parts
+        Frag sp3[X::kParts], gp3[X::kParts];
+        const f32x8 G = Tile<float>::pack(Gv[2 * vb], Gv[2 * vb + 1]);
+        X::split(S[vb], sp3);
+        X::split(G, gp3);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x += S[vb][j] * G[j];
+#pragma unroll
+        for (int i = 0; i < kTT; ++i) {
+          const Frag o = X::rows(so, ldv, i * 16, vb * 32), v = X::rows(sv, ldv, i * 16, vb * 32);
+#pragma unroll
+          for (int p = 0; p < X::kParts; ++p) {
+            dq[i] = X::mma(sp3[p], o, dq[i]);
+            dk[i] = X::mma(gp3[p], v, dk[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTT; ++i) {
+        const int t = i * 16 + col;
+        dq[i] *= d.into[t];
+        dk[i] *= d.onto[t];
+        const f32x4 q = X::load4(sq + t * ldk + k0 + g4), k = X::load4(sk + t * ldk + k0 + g4);
+        float e = 0.0f, f = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          e += q[j] * dq[i][j];
+          f += k[j] * dk[i][j];
+        }
+        e += __shfl_xor(e, 16);
+        e += __shfl_xor(e, 32);
+        f += __shfl_xor(f, 16);
+        f += __shfl_xor(f, 32);
+        if (lane < 16) {
+          se[w][t] = e;
+          sf[w][t] = f;
+        }
+      }
+      x = wave_sum_f32(x);
+      if (lane == 0) sx[w] = x;
+    }
+    if (has_v) {
+#pragma unroll
+      for (int kb = 0; kb < DK / 32; ++kb) {
+        const Frag G = X::pack(Gk[2 * kb], Gk[2 * kb + 1]);
+#pragma unroll
+        for (int i = 0; i < kTT; ++i) dv[i] = X::mma(G, X::rows(sk, ldk, i * 16, kb * 32), dv[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kTT; ++i) dv[i] *= d.onto[i * 16 + col];
+    }
+    __syncthreads();
+    // ---- the pairs' parts, and the state's gradient before the chunk
+    const float whole = d.whole;
+    f32x8 into[C / 32];
+#pragma unroll
+    for (int tb = 0; tb < C / 32; ++tb)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) into[tb][j] = d.into[tb * 32 + 16 * (j / 4) + g4 + j % 4];
+    if (has_k) {
+      Frag kc[C / 32], qc[C / 32];
+#pragma unroll
+      for (int b = 0; b < C / 32; ++b) {
+        kc[b] = X::cols(sk, ldk, b * 32, k0);
+        qc[b] = X::cols(sq, ldk, b * 32, k0);
+      }
+#pragma unroll
+      for (int i = 0; i < kTT; ++i) {
+#pragma unroll
+        for (int b = 0; b < C / 32; ++b) {
+          if (b <= i / 2) dq[i] = X::mma(kc[b], X::rows(sdp, ldp, i * 16, b * 32), dq[i]);
+          if (b >= i / 2) dk[i] = X::mma(qc[b], X::cols(sdp, ldp, b * 32, i * 16), dk[i]);
+        }
+        const int t = i * 16 + col;
+        if (t < valid) {
+          if (A.share == 1) {
+            X::store4((T*)A.dq + (row + t0 + t) * DK + k0 + g4, dq[i]);
+            X::store4((T*)A.dk + (row + t0 + t) * DK + k0 + g4, dk[i]);
+          } else {
+            *reinterpret_cast<f32x4*>(A.dq_part + (row + t0 + t) * DK + k0 + g4) = dq[i];
+            *reinterpret_cast<f32x4*>(A.dk_part + (row + t0 + t) * DK + k0 + g4) = dk[i];
+          }
+        }
+      }
+      Frag part[C / 32][X::kParts];
+#pragma unroll
+      for (int b = 0; b < C / 32; ++b) X::split(X::widen(qc[b]) * into[b], part[b]);
+#pragma unroll
+      for (int vt = 0; vt < kVT; ++vt) {
+        Gv[vt] *= whole;
+#pragma unroll
+        for (int b = 0; b < C / 32; ++b) {
+          const Frag o = X::cols(so, ldv, b * 32, vt * 16);
+#pragma unroll
+          for (int p = 0; p < X::kParts; ++p) Gv[vt] = X::mma(o, part[b][p], Gv[vt]);
+        }
+      }
+    }
+    if (has_v) {
+      Frag oc[C / 32];
+#pragma unroll
+      for (int b = 0; b < C / 32; ++b) oc[b] = X::cols(so, ldv, b * 32, v0);
+#pragma unroll
+      for (int i = 0; i < kTT; ++i) {
+#pragma unroll
+        for (int b = i / 2; b < C / 32; ++b)
+          dv[i] = X::mma(oc[b], X::cols(sp, ldp, b * 32, i * 16), dv[i]);
+        const int t = i * 16 + col;
+        if (t < valid) X::store4((T*)A.dv + (row + t0 + t) * DV + v0 + g4, dv[i]);
+      }
+      Frag part[C / 32][X::kParts];
+#pragma unroll
+      for (int b = 0; b < C / 32; ++b) X::split(X::widen(oc[b]) * into[b], part[b]);
+#pragma unroll
+      for (int kt = 0; kt < kKT; ++kt) {
+        Gk[kt] *= whole;
+#pragma unroll
+        for (int b = 0; b < C / 32; ++b) {
+          const Frag q = X::cols(sq, ldk, b * 32, kt * 16);
+#pragma unroll
+          for (int p = 0; p < X::kParts; ++p) Gk[kt] = X::mma(q, part[b][p], Gk[kt]);
+        }
+      }
+    }
+    if (w == 0) {  // dg of step `lane`
+      double behind = 0.0, before = 0.0, x = 0.0;
+      if (lane < C) {
+        const int tile = lane >> 4;
+#pragma unroll
+        for (int i = 0; i < kTT; ++i) {
+          if (i <= tile) behind += (double)srow[i][lane];
+          if (i >= tile) behind -= (double)scol[i][lane];
+        }
+#pragma unroll
+        for (int i = 0; i < kKT; ++i) {
+          behind += (double)se[i][lane];
+          before += (double)sf[i][lane];
+          x += (double)sx[i];
+        }
+      }
+      const double f = before;
+#pragma unroll
+      for (int o = 1; o < C; o <<= 1) {
+        const double u = __shfl_down(behind, o), v = __shfl_up(before, o);
+        if (lane + o < C) behind += u;
+        if (lane >= o) before += v;
+      }
+      if (lane < valid) {
+        // a step that forgets everything has no path across it: exactly 0
+        const bool none = gg[t0 + lane] <= -128.0f;
+        A.dg[row + t0 + lane] = none ? 0.0f : (float)(behind + (before - f) + x * (double)whole);
+      }
+    }
+    __syncthreads();  // the LDS blocks are read
+  }
+
+  if (seg == 0 && has_v) {
+    float* to = A.S + (int64_t)bh * DK * DV;
+#pragma unroll
+    for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to[(kt * 16 + g4 + i) * DV + v0 + col] = Gk[kt][i];
+  }
+}
+
+template <class T, int DK, int DV>
+hipError_t launch_backward(const LinearArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((linear_backward_kernel<T, DK, DV>),
+                     dim3((unsigned)((int64_t)a.BH * a.nseg)),
+                     dim3(BackwardShape<T, DK, DV>::kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_backward_type(const LinearArgs& a, int d_k, int d_v, hipStream_t s) {
+  switch (d_k * 1000 + d_v) {
+    case 32032: return launch_backward<T, 32, 32>(a, s);
+    case 32064: return launch_backward<T, 32, 64>(a, s);
+    case 32128: return launch_backward<T, 32, 128>(a, s);
+    case 64032: return launch_backward<T, 64, 32>(a, s);
+    case 64064: return launch_backward<T, 64, 64>(a, s);
+    case 64128: return launch_backward<T, 64, 128>(a, s);
+    case 128032: return launch_backward<T, 128, 32>(a, s);
+    case 128064: return launch_backward<T, 128, 64>(a, s);
+    default: return launch_backward<T, 128, 128>(a, s);
+  }
+}
+
+}  // namespace lin
+}  // namespace sdm

@@ -1,0 +1,8 @@
+// Reverse pass of the dense recurrence (linear_backward.h) for bf16.
+#include "linear_backward.h"
+
+namespace sdm {
+hipError_t launch_linear_backward_bf16(const LinearArgs& a, int d_k, int d_v, hipStream_t stream) {
+  return lin::launch_backward_type<uint16_t>(a, d_k, d_v, stream);
+}
+}  // namespace sdm

@@ -1,0 +1,314 @@
+// Root-mean-square norms before and after a block, with the gate and the
+// residual that go with them, and their gradients.  Per row y of d values:
+//   r = 1 / sqrt(mean(y^2) + eps),  out = x + scale * silu(z) * w * y r
+// and, if asked for, the next block's norm of the same row before out is
+// rounded.  With n = y r, a = silu(z), s = sigmoid(z), D = scale * dout:
+//   dz = D n w s (1 + z (1 - s)),   dw = sum over rows of D a n
+//   dy = r (D a w - n mean(D a w n)) + skip
+// Rows of y come as the block's outputs do: [rows, d], or [B, H, T, d] whose
+// outputs are wanted as [B, T, H d].
+//
+// Bound by memory: every value is read once into registers (8 at a time per
+// lane), sums are fp32.  Rows of up to 512 values take a power of two of lanes,
+// 256-thread workgroups several rows; longer rows take a workgroup each.
+#include "dense.h"
+#include "device_common.h"
+
+namespace sdm {
+namespace {
+
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kNarrow = 256;      // threads of a workgroup of short rows
+constexpr int kNarrowMax = 512;   // values of a short row
+constexpr int kWideMax = 1024;    // threads of a long row
+
+template <class T>
+__device__ __forceinline__ f32x8 load8(const void* p, int64_t at) {
+  if constexpr (sizeof(T) == 2) {
+    return __builtin_convertvector(
+        __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>((const uint16_t*)p + at)),
+        f32x8);
+  } else {
+    const f32x4* f = reinterpret_cast<const f32x4*>((const float*)p + at);
+    return __builtin_shufflevector(f[0], f[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void store8(void* p, int64_t at, f32x8 v) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<u32x4*>((uint16_t*)p + at) =
+        __builtin_bit_cast(u32x4, __builtin_convertvector(v, bf16x8));
+  } else {
+    f32x4* f = reinterpret_cast<f32x4*>((float*)p + at);
+    f[0] = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+    f[1] = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+  }
+}
+
+__device__ __forceinline__ float sum8(f32x8 v) {
+  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+// Sum over a row's lanes: `lanes` of them (a power of two up to 64) or, WIDE,
+// the whole workgroup.  Every lane gets the same bits.
+template <bool WIDE>
+__device__ __forceinline__ float row_sum(float v, int lanes, float* lds) {
+  if (!WIDE) {
+    for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor(v, o);
+    return v;
+  }
+  v = wave_sum_f32(v);
+  if (lane_id() == 0) lds[threadIdx.x / kWave] = v;
+  __syncthreads();
+  float s = lds[0];
+  for (int i = 1; i < (int)(blockDim.x / kWave); ++i) s += lds[i];
+  __syncthreads();  // lds is free again
+  return s;
+}
+
+// Row r of the outputs (b, t, h), as a row of y.
+__device__ __forceinline__ int64_t y_row(const NormArgs& A, uint32_t r) {
+  if (A.H == 1) return r;
+  const uint32_t H = A.H, T = (uint32_t)A.T, bt = r / H, h = r % H, b = bt / T, t = bt % T;
+  return ((int64_t)b * H + h) * T + t;
+}
+
+template <class Ty, class To, int V, bool WIDE>
+__global__ __launch_bounds__(WIDE ? kWideMax : kNarrow) void norm_kernel(NormArgs A, int lanes) {
+  __shared__ float lds[kWideMax / kWave];
+  const int nvec = A.d / 8;
+  const int group = WIDE ? 0 : threadIdx.x / lanes, me = WIDE ? threadIdx.x : threadIdx.x % lanes;
+  const int per_block = WIDE ? 1 : kNarrow / lanes, L = WIDE ? (int)blockDim.x : lanes;
+  // every lane of a wavefront runs the same passes (the sums exchange lanes)
+  for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < A.rows;
+       r0 += (int64_t)gridDim.x * per_block) {
+    const int64_t r = r0 + group;
+    const bool here = r < A.rows;
+    const int64_t yr = here ? y_row(A, (uint32_t)r) * A.d : 0, at = r * A.d;
+    f32x8 y[V];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = me + i * L;
+      y[i] = here && j < nvec ? load8<Ty>(A.y, yr + j * 8) : f32x8{0, 0, 0, 0, 0, 0, 0, 0};
+    }
+    f32x8 z[V], x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = me + i * L;
+      if (here && j < nvec) {
+        if (A.z) z[i] = load8<To>(A.z, at + j * 8);
+        if (A.x) x[i] = load8<To>(A.x, at + j * 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) ss += sum8(y[i] * y[i]);
+    const float rs = A.scale / sqrtf(row_sum<WIDE>(ss, lanes, lds) / (float)A.d + A.eps);
+    ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = me + i * L;
+      if (!here || j >= nvec) continue;
+      y[i] = y[i] * rs * load8<float>(A.w, j * 8);
+      if (A.z) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[i][e] *= z[i][e] * sigmoid(z[i][e]);
+      }
+      if (A.x) y[i] += x[i];
+      store8<To>(A.out, at + j * 8, y[i]);
+      ss += sum8(y[i] * y[i]);
+    }
+    if (A.next_w) {
+      const float rn = 1.0f / sqrtf(row_sum<WIDE>(ss, lanes, lds) / (float)A.d + A.eps);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int j = me + i * L;
+        if (here && j < nvec) store8<To>(A.next, at + j * 8, y[i] * rn * load8<float>(A.next_w, j * 8));
+      }
+    }
+  }
+}
+
+// Each workgroup takes rows blockIdx, blockIdx + blocks, ... and leaves its
+// sum of dw in part[blockIdx].
+template <class Ty, class To, int V, bool WIDE>
+__global__ __launch_bounds__(WIDE ? kWideMax / 2 : kNarrow) void norm_backward_kernel(NormArgs A,
+                                                                                   int lanes) {
+  __shared__ float lds[kWideMax / kWave];
+  __shared__ __align__(16) float sum[WIDE ? 8 : kNarrow * 8];
+  const int nvec = A.d / 8;
+  const int group = WIDE ? 0 : threadIdx.x / lanes, me = WIDE ? threadIdx.x : threadIdx.x % lanes;
+  const int per_block = WIDE ? 1 : kNarrow / lanes, L = WIDE ? (int)blockDim.x : lanes;
+  f32x8 w[V], dw[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int j = me + i * L;
+    dw[i] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
+    w[i] = j < nvec ? load8<float>(A.w, j * 8) : dw[i];
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < A.rows;
+       r0 += (int64_t)gridDim.x * per_block) {
+    const int64_t r = r0 + group;
+    const bool here = r < A.rows;
+    const int64_t yr = here ? y_row(A, (uint32_t)r) * A.d : 0, at = r * A.d;
+    f32x8 y[V], D[V], z[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = me + i * L;
+      const bool in = here && j < nvec;
+      const f32x8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
+      y[i] = in ? load8<Ty>(A.y, yr + j * 8) : zero;
+      D[i] = in ? load8<To>(A.dout, at + j * 8) * A.scale : zero;
+      z[i] = in && A.z ? load8<To>(A.z, at + j * 8) : zero;
+    }
+    float ss = 0.0f, sd = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      f32x8 a = D[i] * w[i];
+      if (A.z) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] *= z[i][e] * sigmoid(z[i][e]);
+      }
+      ss += sum8(y[i] * y[i]);
+      sd += sum8(a * y[i]);
+    }
+    ss = row_sum<WIDE>(ss, lanes, lds);
+    sd = row_sum<WIDE>(sd, lanes, lds);
+    const float rs = 1.0f / sqrtf(ss / (float)A.d + A.eps);
+    const float mean = sd * rs / (float)A.d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = me + i * L;
+      if (!here || j >= nvec) continue;
+      const f32x8 n = y[i] * rs;
+      f32x8 a = D[i];
+      if (A.z) {
+        f32x8 dz;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float s = sigmoid(z[i][e]);
+          dz[e] = D[i][e] * n[e] * w[i][e] * (s * (1.0f + z[i][e] * (1.0f - s)));
+          a[e] *= z[i][e] * s;
+        }
+        store8<To>(A.dz, at + j * 8, dz);
+      }
+      dw[i] += a * n;
+      f32x8 dy = (a * w[i] - n * mean) * rs;
+      if (A.skip) dy += load8<Ty>(A.skip, yr + j * 8);
+      store8<Ty>(A.dy, yr + j * 8, dy);
+    }
+  }
+  float* part = A.part + (int64_t)blockIdx.x * A.d;
+  if (WIDE) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (me + i * L < nvec) store8<float>(part, (me + i * L) * 8, dw[i]);
+    return;
+  }
+  store8<float>(sum, threadIdx.x * 8, dw[0]);
+  __syncthreads();
+  if (group == 0 && me < nvec) {
+    for (int k = 1; k < per_block; ++k) dw[0] += load8<float>(sum, (k * lanes + me) * 8);
+    store8<float>(part, me * 8, dw[0]);
+  }
+}
+
+// dw = sum of the workgroups' parts, in a fixed order: 64 columns a workgroup,
+// 16 rows of parts at a time.
+__global__ __launch_bounds__(256) void norm_dw_kernel(const float* part, float* dw, int d,
+                                                      int blocks) {
+  __shared__ f32x4 lds[16][16];
+  const int cl = threadIdx.x % 16, rl = threadIdx.x / 16, c = blockIdx.x * 64 + cl * 4;
+  f32x4 s = {0, 0, 0, 0};
+  if (c < d)
+    for (int b = rl; b < blocks; b += 16)
+      s += *reinterpret_cast<const f32x4*>(part + (int64_t)b * d + c);
+  lds[rl][cl] = s;
+  __syncthreads();
+  if (rl == 0 && c < d) {
+    for (int i = 1; i < 16; ++i) s += lds[i][cl];
+    *reinterpret_cast<f32x4*>(dw + c) = s;
+  }
+}
+
+int row_lanes(int d) {  // of a short row
+  int lanes = 1;
+  while (lanes * 8 < d) lanes *= 2;
+  return lanes;
+}
+
+int wide_threads(int d, int V) { return (d / 8 + V * kWave - 1) / (V * kWave) * kWave; }
+
+template <class Ty, class To>
+hipError_t norm_types(const NormArgs& a, hipStream_t s) {
+  constexpr int64_t kMaxBlocks = (int64_t)1 << 20;
+  if (a.d <= kNarrowMax) {
+    const int lanes = row_lanes(a.d);
+    const int64_t want = (a.rows + kNarrow / lanes - 1) / (kNarrow / lanes);
+    const int64_t blocks = want < kMaxBlocks ? want : kMaxBlocks;
+    hipLaunchKernelGGL((norm_kernel<Ty, To, 1, false>), dim3((unsigned)blocks), dim3(kNarrow), 0, s,
+                       a, lanes);
+    return hipGetLastError();
+  }
+  const dim3 blocks((unsigned)(a.rows < kMaxBlocks ? a.rows : kMaxBlocks));
+  if (a.d <= 8 * kWideMax)
+    hipLaunchKernelGGL((norm_kernel<Ty, To, 1, true>), blocks, dim3(wide_threads(a.d, 1)), 0, s, a, 0);
+  else
+    hipLaunchKernelGGL((norm_kernel<Ty, To, 2, true>), blocks, dim3(wide_threads(a.d, 2)), 0, s, a, 0);
+  return hipGetLastError();
+}
+
+template <class Ty, class To>
+hipError_t norm_backward_types(const NormArgs& a, hipStream_t s) {
+  const int64_t n = norm_backward_blocks(a.rows, a.d);
+  const dim3 blocks((unsigned)n);
+  if (n == 0)
+    ;  // no rows: dw is 0
+  else if (a.d <= kNarrowMax)
+    hipLaunchKernelGGL((norm_backward_kernel<Ty, To, 1, false>), blocks, dim3(kNarrow), 0, s, a,
+                       row_lanes(a.d));
+  else if (a.d <= 8 * 512)
+    hipLaunchKernelGGL((norm_backward_kernel<Ty, To, 1, true>), blocks, dim3(wide_threads(a.d, 1)),
+                       0, s, a, 0);
+  else if (a.d <= 8 * 1024)
+    hipLaunchKernelGGL((norm_backward_kernel<Ty, To, 2, true>), blocks, dim3(wide_threads(a.d, 2)),
+                       0, s, a, 0);
+  else
+    hipLaunchKernelGGL((norm_backward_kernel<Ty, To, 4, true>), blocks, dim3(wide_threads(a.d, 4)),
+                       0, s, a, 0);
+  hipError_t rc = hipGetLastError();
+  if (rc != hipSuccess) return rc;
+  hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((a.d + 63) / 64)), dim3(256), 0, s, a.part,
+                     a.dw, a.d, (int)n);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, int y_dtype, int out_dtype, hipStream_t s) {
+  if (y_dtype == 1)
+    return out_dtype == 1 ? norm_types<uint16_t, uint16_t>(a, s) : norm_types<uint16_t, float>(a, s);
+  return out_dtype == 1 ? norm_types<float, uint16_t>(a, s) : norm_types<float, float>(a, s);
+}
+
+// Workgroups of the reverse pass, each of which leaves d partial sums.
+int64_t norm_backward_blocks(int64_t rows, int d) {
+  const int per_block = d <= kNarrowMax ? kNarrow / row_lanes(d) : 1;
+  const int64_t want = (rows + per_block - 1) / per_block, most = 512;
+  return want < most ? want : most;
+}
+
+hipError_t launch_norm_backward(const NormArgs& a, int y_dtype, int out_dtype, hipStream_t s) {
+  if (y_dtype == 1)
+    return out_dtype == 1 ? norm_backward_types<uint16_t, uint16_t>(a, s)
+                          : norm_backward_types<uint16_t, float>(a, s);
+  return out_dtype == 1 ? norm_backward_types<float, uint16_t>(a, s)
+                        : norm_backward_types<float, float>(a, s);
+}
+
+}  // namespace sdm
