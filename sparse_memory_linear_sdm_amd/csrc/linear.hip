@@ -32,7 +32,7 @@ __global__ __launch_bounds__(kThreads) void linear_segments_kernel(float* seg_st
       const int i = reverse ? nseg - 1 - (i0 + j) : i0 + j;
       if (i0 + j < nseg - 1) {  // the last of the order passes nothing on
         own[j] = *reinterpret_cast<const f32x4*>(p + (int64_t)i * elems);
-        decay[j] = exp2f((float)lg[i]);
+        decay[j] = lin::pow2((float)lg[i]);
       }
     }
 #pragma unroll

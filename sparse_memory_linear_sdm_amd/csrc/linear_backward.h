@@ -42,23 +42,23 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
   constexpr int NW = BackwardShape<T, DK, DV>::kWaves, NT = NW * kWave;
   typedef Block<T, DK, NT> BlockK;
   typedef Block<T, DV, NT> BlockV;
-  constexpr int ldk = BlockK::kLd, ldv = BlockV::kLd, ldp = C + X::kPad;
+  constexpr int kSizeP = C * X::template kLd<C>;
   constexpr int kTT = C / 16, kKT = DK / 16, kVT = DV / 16;
   static_assert(kKT <= NW && kVT <= NW, "one column tile a wavefront");
-  __shared__ __align__(16) T sq[C * ldk];
-  __shared__ __align__(16) T sk[C * ldk];
-  __shared__ __align__(16) T sv[C * ldv];
-  __shared__ __align__(16) T so[C * ldv];   // dout
-  __shared__ __align__(16) T sp[C * ldp];   // (q_t . k_s) D_ts, rows t
-  __shared__ __align__(16) T sdp[C * ldp];  // (do_t . v_s) D_ts, rows t
+  __shared__ __align__(16) T sq[BlockK::kSize];
+  __shared__ __align__(16) T sk[BlockK::kSize];
+  __shared__ __align__(16) T sv[BlockV::kSize];
+  __shared__ __align__(16) T so[BlockV::kSize];   // dout
+  __shared__ __align__(16) T sp[kSizeP];   // (q_t . k_s) D_ts, rows t
+  __shared__ __align__(16) T sdp[kSizeP];  // (do_t . v_s) D_ts, rows t
   __shared__ Decays<C> sd[2];
   __shared__ float srow[kTT][C], scol[kTT][C];  // sums of W by tiles
   __shared__ float se[kKT][C], sf[kKT][C], sx[kKT];
 
   const int lane = lane_id(), col = lane & 15, g4 = 4 * (lane >> 4);
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t pid = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int bh = (int)(pid / A.nseg), seg = (int)(pid % A.nseg);
+  const uint32_t pid = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int bh = (int)(pid / (uint32_t)A.nseg), seg = (int)(pid % (uint32_t)A.nseg);
   const int c_first = seg * A.seg_chunks;
   const int c_end = c_first + A.seg_chunks < A.nchunk ? c_first + A.seg_chunks : A.nchunk;
   const int64_t key_row = (int64_t)(bh / A.share) * A.T, row = (int64_t)bh * A.T;
@@ -87,9 +87,10 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
 
   BlockK bq, bk;
   BlockV bv, bo;
+  // steps of chunk c, 0 before the first one
   auto rows_of = [&](int c) {
     const int64_t left = A.T - (int64_t)c * C;
-    return left < C ? (int)left : C;
+    return c < c_first ? 0 : left < C ? (int)left : C;
   };
   auto load = [&](int c) {
     const int64_t t0 = (int64_t)c * C;
@@ -99,11 +100,17 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
     bv.load(gv + t0 * DV, valid);
     bo.load(go + t0 * DV, valid);
   };
-  auto step_log = [&](int c) {
-    return lane < rows_of(c) ? log2_decay(gg[(int64_t)c * C + lane]) : 0.0;
+  float step_g = 0.0f;  // of step `lane`
+  auto load_g = [&](int c) {
+    step_g = __builtin_bit_cast(
+        float, __builtin_amdgcn_raw_buffer_load_b32(
+                   buffer(gg + (int64_t)c * C, (uint32_t)rows_of(c) * 4), lane * 4, 0, 0));
   };
   load(c_end - 1);
-  if (w == NW - 1) scan_decays<C>(step_log(c_end - 1), sd[(c_end - 1) & 1]);
+  load_g(c_end - 1);
+  arrive(Gk);
+  arrive(Gv);
+  if (w == NW - 1) scan_decays<C>(log2_decay(step_g), sd[(c_end - 1) & 1]);
 
   for (int c = c_end - 1; c >= c_first; --c) {
     const Decays<C>& d = sd[c & 1];
@@ -123,11 +130,9 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
                                   *reinterpret_cast<const f32x4*>(tape + vb * 32 + 16));
     }
     __syncthreads();
-    double next_log = 0.0;
-    if (c > c_first) {
-      load(c - 1);
-      if (w == NW - 1) next_log = step_log(c - 1);
-    }
+    load(c - 1);
+    const float this_g = step_g;
+    load_g(c - 1);
     // ---- pairs of steps: P, dP and the sums of W
     constexpr int kUnits = kTT == 4 ? 12 : 4;
     for (int u = w; u < kUnits; u += NW) {
@@ -137,19 +142,19 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
       if (st <= tt) {
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb)
-          p = X::mma(X::rows(sk, ldk, st * 16, kb * 32), X::rows(sq, ldk, tt * 16, kb * 32), p);
+          p = X::mma(X::template rows<DK>(sk, st * 16, kb * 32), X::template rows<DK>(sq, tt * 16, kb * 32), p);
 #pragma unroll
         for (int vb = 0; vb < DV / 32; ++vb)
-          dp = X::mma(X::rows(sv, ldv, st * 16, vb * 32), X::rows(so, ldv, tt * 16, vb * 32), dp);
+          dp = X::mma(X::template rows<DV>(sv, st * 16, vb * 32), X::template rows<DV>(so, tt * 16, vb * 32), dp);
         float by_row = 0.0f, by_col[4];
+        const f32x4 decay = decay_between<C>(d, t, s);
+        const f32x4 raw = dp;
+        p = decayed(p, decay, t, s);
+        dp = decayed(dp, decay, t, s);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float dec = s + j <= t ? decay_between<C>(d, t, s + j) : 0.0f;
-          const float W = s + j < t ? p[j] * dp[j] * dec : 0.0f;
-          p[j] = s + j <= t ? p[j] * dec : 0.0f;
-          dp[j] = s + j <= t ? dp[j] * dec : 0.0f;
-          by_row += W;
-          by_col[j] = W;
+          by_col[j] = s + j < t ? p[j] * raw[j] : 0.0f;
+          by_row += by_col[j];
         }
         by_row += __shfl_xor(by_row, 16);
         by_row += __shfl_xor(by_row, 32);
@@ -162,10 +167,10 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
           if (col == 0) scol[tt][s + j] = by_col[j];
         }
       }
-      X::store4(sp + t * ldp + s, p);
-      X::store4(sdp + t * ldp + s, dp);
+      X::store4(sp + X::template at<C>(t, s), p);
+      X::store4(sdp + X::template at<C>(t, s), dp);
     }
-    if (c > c_first && w == NW - 1) scan_decays<C>(next_log, sd[(c - 1) & 1]);
+    if (w == NW - 1) scan_decays<C>(log2_decay(step_g), sd[(c - 1) & 1]);
     // ---- the state's parts of the gradients, transposed: a lane holds four
     // consecutive values of one step
     f32x4 dq[kTT], dk[kTT], dv[kTT];
@@ -184,7 +189,7 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
         for (int j = 0; j < 8; ++j) x += S[vb][j] * G[j];
 #pragma unroll
         for (int i = 0; i < kTT; ++i) {
-          const Frag o = X::rows(so, ldv, i * 16, vb * 32), v = X::rows(sv, ldv, i * 16, vb * 32);
+          const Frag o = X::template rows<DV>(so, i * 16, vb * 32), v = X::template rows<DV>(sv, i * 16, vb * 32);
 #pragma unroll
           for (int p = 0; p < X::kParts; ++p) {
             dq[i] = X::mma(sp3[p], o, dq[i]);
@@ -197,7 +202,8 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
         const int t = i * 16 + col;
         dq[i] *= d.into[t];
         dk[i] *= d.onto[t];
-        const f32x4 q = X::load4(sq + t * ldk + k0 + g4), k = X::load4(sk + t * ldk + k0 + g4);
+        const f32x4 q = X::load4(sq + X::template at<DK>(t, k0 + g4)),
+                    k = X::load4(sk + X::template at<DK>(t, k0 + g4));
         float e = 0.0f, f = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -221,7 +227,7 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
       for (int kb = 0; kb < DK / 32; ++kb) {
         const Frag G = X::pack(Gk[2 * kb], Gk[2 * kb + 1]);
 #pragma unroll
-        for (int i = 0; i < kTT; ++i) dv[i] = X::mma(G, X::rows(sk, ldk, i * 16, kb * 32), dv[i]);
+        for (int i = 0; i < kTT; ++i) dv[i] = X::mma(G, X::template rows<DK>(sk, i * 16, kb * 32), dv[i]);
       }
 #pragma unroll
       for (int i = 0; i < kTT; ++i) dv[i] *= d.onto[i * 16 + col];
@@ -235,28 +241,32 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
 #pragma unroll
       for (int j = 0; j < 8; ++j) into[tb][j] = d.into[tb * 32 + 16 * (j / 4) + g4 + j % 4];
     if (has_k) {
+      const bool shared = A.share > 1;
+      const int64_t at0 = (row + t0) * DK;
+      const uint32_t bytes = valid * DK * (shared ? 4 : (int)sizeof(T));
+      const __amdgpu_buffer_rsrc_t
+          out_q = buffer(shared ? (void*)(A.dq_part + at0) : (void*)((T*)A.dq + at0), bytes),
+          out_k = buffer(shared ? (void*)(A.dk_part + at0) : (void*)((T*)A.dk + at0), bytes);
       Frag kc[C / 32], qc[C / 32];
 #pragma unroll
       for (int b = 0; b < C / 32; ++b) {
-        kc[b] = X::cols(sk, ldk, b * 32, k0);
-        qc[b] = X::cols(sq, ldk, b * 32, k0);
+        kc[b] = X::template cols<DK>(sk, b * 32, k0);
+        qc[b] = X::template cols<DK>(sq, b * 32, k0);
       }
 #pragma unroll
       for (int i = 0; i < kTT; ++i) {
 #pragma unroll
         for (int b = 0; b < C / 32; ++b) {
-          if (b <= i / 2) dq[i] = X::mma(kc[b], X::rows(sdp, ldp, i * 16, b * 32), dq[i]);
-          if (b >= i / 2) dk[i] = X::mma(qc[b], X::cols(sdp, ldp, b * 32, i * 16), dk[i]);
+          if (b <= i / 2) dq[i] = X::mma(kc[b], X::template rows<C>(sdp, i * 16, b * 32), dq[i]);
+          if (b >= i / 2) dk[i] = X::mma(qc[b], X::template cols<C>(sdp, b * 32, i * 16), dk[i]);
         }
-        const int t = i * 16 + col;
-        if (t < valid) {
-          if (A.share == 1) {
-            X::store4((T*)A.dq + (row + t0 + t) * DK + k0 + g4, dq[i]);
-            X::store4((T*)A.dk + (row + t0 + t) * DK + k0 + g4, dk[i]);
-          } else {
-            *reinterpret_cast<f32x4*>(A.dq_part + (row + t0 + t) * DK + k0 + g4) = dq[i];
-            *reinterpret_cast<f32x4*>(A.dk_part + (row + t0 + t) * DK + k0 + g4) = dk[i];
-          }
+        const int at = (i * 16 + col) * DK + k0 + g4;
+        if (A.share == 1) {
+          X::store4(out_q, at, dq[i]);
+          X::store4(out_k, at, dk[i]);
+        } else {
+          Tile<float>::store4(out_q, at, dq[i]);
+          Tile<float>::store4(out_k, at, dk[i]);
         }
       }
       Frag part[C / 32][X::kParts];
@@ -267,23 +277,24 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
         Gv[vt] *= whole;
 #pragma unroll
         for (int b = 0; b < C / 32; ++b) {
-          const Frag o = X::cols(so, ldv, b * 32, vt * 16);
+          const Frag o = X::template cols<DV>(so, b * 32, vt * 16);
 #pragma unroll
           for (int p = 0; p < X::kParts; ++p) Gv[vt] = X::mma(o, part[b][p], Gv[vt]);
         }
       }
     }
     if (has_v) {
+      const __amdgpu_buffer_rsrc_t out_v =
+          buffer((T*)A.dv + (row + t0) * DV, (uint32_t)(valid * DV * (int)sizeof(T)));
       Frag oc[C / 32];
 #pragma unroll
-      for (int b = 0; b < C / 32; ++b) oc[b] = X::cols(so, ldv, b * 32, v0);
+      for (int b = 0; b < C / 32; ++b) oc[b] = X::template cols<DV>(so, b * 32, v0);
 #pragma unroll
       for (int i = 0; i < kTT; ++i) {
 #pragma unroll
         for (int b = i / 2; b < C / 32; ++b)
-          dv[i] = X::mma(oc[b], X::cols(sp, ldp, b * 32, i * 16), dv[i]);
-        const int t = i * 16 + col;
-        if (t < valid) X::store4((T*)A.dv + (row + t0 + t) * DV + v0 + g4, dv[i]);
+          dv[i] = X::mma(oc[b], X::template cols<C>(sp, b * 32, i * 16), dv[i]);
+        X::store4(out_v, (i * 16 + col) * DV + v0 + g4, dv[i]);
       }
       Frag part[C / 32][X::kParts];
 #pragma unroll
@@ -293,7 +304,7 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
         Gk[kt] *= whole;
 #pragma unroll
         for (int b = 0; b < C / 32; ++b) {
-          const Frag q = X::cols(sq, ldk, b * 32, kt * 16);
+          const Frag q = X::template cols<DK>(sq, b * 32, kt * 16);
 #pragma unroll
           for (int p = 0; p < X::kParts; ++p) Gk[kt] = X::mma(q, part[b][p], Gk[kt]);
         }
@@ -324,7 +335,7 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
       }
       if (lane < valid) {
         // a step that forgets everything has no path across it: exactly 0
-        const bool none = gg[t0 + lane] <= -128.0f;
+        const bool none = this_g <= -128.0f;
         A.dg[row + t0 + lane] = none ? 0.0f : (float)(behind + (before - f) + x * (double)whole);
       }
     }

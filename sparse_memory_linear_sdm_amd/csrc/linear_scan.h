@@ -6,9 +6,9 @@
 //   S'    = exp(L_C) S       + sum over s of exp(L_C - L_s) k_s v_s^T
 // (all exponents <= 0 for decays), as products of 16 x 16 tiles.
 //
-// One workgroup of four wavefronts walks the chunks of a memory, or of one
-// segment of it; the state stays in its accumulators, each wavefront holding
-// all d_k rows of d_v / 4 columns.  Where memories are few, the steps are cut
+// One workgroup walks the chunks of a memory, or of one segment of it; the
+// state stays in its accumulators, each wavefront holding all d_k rows of 16
+// columns.  Where memories are few, the steps are cut
 // into segments: a first kernel (modes 1 and 2) finds what each segment adds to
 // the state, another adds these up (linear.hip), then each segment starts from
 // its own state.
@@ -19,31 +19,36 @@
 namespace sdm {
 namespace lin {
 
-constexpr int kScanThreads = 256;
+constexpr int kScanWaves = 4, kScanThreads = kScanWaves * kWave;
 
+// MODE: 0 the scan, 3 the scan that keeps its tape, 1 and 2 the state alone,
+// forward and in reverse.
 template <class T, int DK, int DV, int MODE>
-__global__ __launch_bounds__(kScanThreads) void linear_kernel(LinearArgs A) {
+__global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
   typedef Tile<T> X;
   typedef typename X::Frag Frag;
   constexpr int C = X::kChunk;
-  constexpr bool kOut = MODE == 0;   // outputs, not the state alone
+  constexpr bool kOut = MODE == 0 || MODE == 3;  // outputs, not the state alone
+  constexpr bool kTape = MODE == 3;
   constexpr bool kReverse = MODE == 2;
-  typedef Block<T, DK, kScanThreads> BlockK;
-  typedef Block<T, DV, kScanThreads> BlockV;
-  constexpr int ldk = BlockK::kLd, ldv = BlockV::kLd, ldp = C + X::kPad;
+  constexpr int NW = kScanWaves, NT = kScanThreads;
+  typedef Block<T, DK, NT> BlockK;
+  typedef Block<T, DV, NT> BlockV;
+  constexpr int kSizeP = C * X::template kLd<C>;
   constexpr int kTT = C / 16;                       // tiles of steps
   constexpr int kKT = DK / 16;                      // tiles of state rows
-  constexpr int kCT = DV >= 64 ? DV / 64 : 1;       // tiles of state columns per wavefront
-  __shared__ __align__(16) T sq[kOut ? C * ldk : 8];
-  __shared__ __align__(16) T sk[C * ldk];
-  __shared__ __align__(16) T sv[C * ldv];
-  __shared__ __align__(16) T sp[kOut ? C * ldp : 8];  // q_t . k_s and its decay, rows t
+  constexpr int kCT = DV > 16 * NW ? DV / (16 * NW) : 1;  // tiles of state columns per wavefront
+  __shared__ __align__(16) T sq[kOut ? BlockK::kSize : 8];
+  __shared__ __align__(16) T sk[BlockK::kSize];
+  __shared__ __align__(16) T sv[BlockV::kSize];
+  __shared__ __align__(16) T sp[kOut ? kSizeP : 8];  // q_t . k_s and its decay, rows t
   __shared__ Decays<C> sd[2];
+  __shared__ float sg[C];  // g of the next chunk
 
   const int lane = lane_id(), col = lane & 15, g4 = 4 * (lane >> 4);
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t pid = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int bh = (int)(pid / A.nseg), seg = (int)(pid % A.nseg);
+  const uint32_t pid = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int bh = (int)(pid / (uint32_t)A.nseg), seg = (int)(pid % (uint32_t)A.nseg);
   const int c_first = seg * A.seg_chunks;
   const int c_end = c_first + A.seg_chunks < A.nchunk ? c_first + A.seg_chunks : A.nchunk;
   const int n = c_end - c_first;
@@ -54,8 +59,8 @@ __global__ __launch_bounds__(kScanThreads) void linear_kernel(LinearArgs A) {
   const T* gv = (kReverse ? (const T*)A.dout : (const T*)A.v) + row * DV;
   const float* gg = A.g + row;
 
-  const int ct0 = w * kCT;  // first of this wavefront's column tiles
-  const bool mine = ct0 < DV / 16;
+  const int v0 = w * kCT * 16;  // this wavefront holds columns v0 .. v0 + 16 kCT - 1
+  const bool mine = v0 < DV;
   f32x4 S[kKT][kCT];
   const float* from = nullptr;
   if (kOut) from = A.nseg > 1 ? A.seg_state + ((int64_t)bh * A.nseg + seg) * DK * DV
@@ -66,28 +71,47 @@ __global__ __launch_bounds__(kScanThreads) void linear_kernel(LinearArgs A) {
     for (int ct = 0; ct < kCT; ++ct)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        S[kt][ct][i] = kOut && mine ? from[(kt * 16 + g4 + i) * DV + (ct0 + ct) * 16 + col] : 0.0f;
+        S[kt][ct][i] = kOut && mine ? from[(kt * 16 + g4 + i) * DV + v0 + ct * 16 + col] : 0.0f;
+
+  auto store_state = [&](float* to) {
+    const __amdgpu_buffer_rsrc_t b = buffer(to, DK * DV * 4);
+    const int at = (g4 * DV + v0 + col) * 4;
+#pragma unroll
+    for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+      for (int ct = 0; ct < kCT; ++ct)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[kt][ct][i]), b, at + ct * 64,
+                                                (kt * 16 + i) * DV * 4, 0);
+  };
 
   BlockK bq, bk;
   BlockV bv;
   auto chunk_of = [&](int i) { return kReverse ? c_end - 1 - i : c_first + i; };
-  auto rows_of = [&](int c) {
-    const int64_t left = A.T - (int64_t)c * C;
-    return left < C ? (int)left : C;
+  // steps of the i-th chunk, 0 behind the last one
+  auto rows_of = [&](int i) {
+    const int64_t left = A.T - (int64_t)chunk_of(i) * C;
+    return i >= n ? 0 : left < C ? (int)left : C;
   };
-  auto load = [&](int c) {
-    const int64_t t0 = (int64_t)c * C;
-    const int valid = rows_of(c);
+  auto load = [&](int i) {
+    const int64_t t0 = (int64_t)chunk_of(i) * C;
+    const int valid = rows_of(i);
     if (kOut) bq.load(gq + t0 * DK, valid);
     bk.load(gk + t0 * DK, valid);
     bv.load(gv + t0 * DV, valid);
   };
-  auto step_log = [&](int c) {  // of step `lane`
-    return lane < rows_of(c) ? log2_decay(gg[(int64_t)c * C + lane]) : 0.0;
+  auto g_of = [&](int i) {  // of step `lane` of the i-th chunk
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_raw_buffer_load_b32(
+                   buffer(gg + (int64_t)chunk_of(i) * C, (uint32_t)rows_of(i) * 4), lane * 4, 0, 0));
   };
   double total = 0.0;
-  load(chunk_of(0));
-  if (w == 0) total = scan_decays<C>(step_log(chunk_of(0)), sd[0]);
+  load(0);
+  if (w == 0) total = scan_decays<C>(log2_decay(g_of(0)), sd[0]);
+  float step_g = g_of(1);
+#pragma unroll
+  for (int kt = 0; kt < kKT; ++kt) arrive(S[kt]);
 
   for (int i = 0; i < n; ++i) {
     const int c = chunk_of(i);
@@ -95,56 +119,43 @@ __global__ __launch_bounds__(kScanThreads) void linear_kernel(LinearArgs A) {
     if (kOut) bq.store(sq);
     bk.store(sk);
     bv.store(sv);
+    if (w == 0 && lane < C) sg[lane] = step_g;
     __syncthreads();
-    double next_log = 0.0;
-    if (i + 1 < n) {
-      load(chunk_of(i + 1));
-      if (w == 0) next_log = step_log(chunk_of(i + 1));
-    }
+    load(i + 1);
+    step_g = g_of(i + 2);
     if (kOut) {
-      // this wavefront's tiles of (q_t . k_s) decay(s, t), s <= t, in rows s:
-      // four consecutive s of step t per lane
-      constexpr int kUnits = kTT == 4 ? 4 : 1;
+      // (q_t . k_s) decay(s, t), s <= t: this wavefront's tiles in rows s, four
+      // consecutive s of step t per lane
+      constexpr int kUnits = kTT == 4 ? 12 : 4;  // tiles that a product below reads
+      static_assert(kUnits % NW == 0, "as many for every wavefront");
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        const int tt = kTT == 4 ? w : w >> 1, st = kTT == 4 ? u : w & 1;
-        if (st > (tt | 1)) continue;  // no product below reads it
+      for (int u0 = 0; u0 < kUnits; u0 += NW) {
+        const int u = u0 + w;
+        const int tt = u < 4 ? u >> 1 : 2 + ((u - 4) >> 2), st = u < 4 ? u & 1 : (u - 4) & 3;
         f32x4 p = {0, 0, 0, 0};
-        if (st <= tt) {
+        const int t = tt * 16 + col, s = st * 16 + g4;
 #pragma unroll
-          for (int kb = 0; kb < DK / 32; ++kb)
-            p = X::mma(X::rows(sk, ldk, st * 16, kb * 32), X::rows(sq, ldk, tt * 16, kb * 32), p);
-          const int t = tt * 16 + col, s = st * 16 + g4;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) p[j] = s + j <= t ? p[j] * decay_between<C>(d, t, s + j) : 0.0f;
-        }
-        X::store4(sp + (tt * 16 + col) * ldp + st * 16 + g4, p);
+        for (int kb = 0; kb < DK / 32; ++kb)
+          p = X::mma(X::template rows<DK>(sk, st * 16, kb * 32),
+                     X::template rows<DK>(sq, tt * 16, kb * 32), p);
+        p = decayed(p, decay_between<C>(d, t, s), t, s);
+        X::store4(sp + X::template at<C>(t, s), p);
       }
+      __syncthreads();
     }
-    if (i + 1 < n && w == 0) total += scan_decays<C>(next_log, sd[(i + 1) & 1]);
-    if (kOut) __syncthreads();
+    if (w == 0) total += scan_decays<C>(lane < C ? log2_decay(sg[lane]) : 0.0, sd[(i + 1) & 1]);
     if (mine) {
-      if (kOut && A.tape) {
-        float* tape = A.tape + ((int64_t)bh * A.nchunk + c) * DK * DV;
-#pragma unroll
-        for (int kt = 0; kt < kKT; ++kt)
-#pragma unroll
-          for (int ct = 0; ct < kCT; ++ct)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tape[(kt * 16 + g4 + j) * DV + (ct0 + ct) * 16 + col] = S[kt][ct][j];
+      if (kTape) {
+        store_state(A.tape + ((int64_t)bh * A.nchunk + c) * DK * DV);
       }
       Frag V[kCT][C / 32];
-#pragma unroll
-      for (int ct = 0; ct < kCT; ++ct)
-#pragma unroll
-        for (int sb = 0; sb < C / 32; ++sb) V[ct][sb] = X::cols(sv, ldv, sb * 32, (ct0 + ct) * 16);
+      schedule_end();
       if (kOut) {
         // outputs transposed: rows are columns of v, so a lane holds four
         // consecutive values of step t.  The state enters rounded to T (bf16: the
         // outputs are rounded to it as well), the accumulators keep fp32.
-        const int64_t t0 = (int64_t)c * C;
-        const int valid = rows_of(c);
+        const __amdgpu_buffer_rsrc_t out = buffer((T*)A.out + (row + (int64_t)c * C) * DV,
+                                                  (uint32_t)(rows_of(i) * DV * (int)sizeof(T)));
         f32x4 o[kTT][kCT];
 #pragma unroll
         for (int tt = 0; tt < kTT; ++tt)
@@ -152,16 +163,29 @@ __global__ __launch_bounds__(kScanThreads) void linear_kernel(LinearArgs A) {
           for (int ct = 0; ct < kCT; ++ct) o[tt][ct] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) {
-          Frag s[kCT];
+          Frag q[kTT];
 #pragma unroll
-          for (int ct = 0; ct < kCT; ++ct) s[ct] = X::pack(S[2 * kb][ct], S[2 * kb + 1][ct]);
+          for (int tt = 0; tt < kTT; ++tt) q[tt] = X::template rows<DK>(sq, tt * 16, kb * 32);
 #pragma unroll
-          for (int tt = 0; tt < kTT; ++tt) {
-            const Frag q = X::rows(sq, ldk, tt * 16, kb * 32);
+          for (int ct = 0; ct < kCT; ++ct) {
+            const Frag s = X::pack(S[2 * kb][ct], S[2 * kb + 1][ct]);
 #pragma unroll
-            for (int ct = 0; ct < kCT; ++ct) o[tt][ct] = X::mma(s[ct], q, o[tt][ct]);
+            for (int tt = 0; tt < kTT; ++tt) o[tt][ct] = X::mma(s, q[tt], o[tt][ct]);
           }
         }
+        // reads one block of products ahead
+        schedule_reads<kTT * X::kRowReads>();
+#pragma unroll
+        for (int kb = 0; kb < DK / 32; ++kb) {
+          schedule_reads<kTT * X::kRowReads>();
+          schedule_products<kTT * kCT * X::kProducts>();
+        }
+        schedule_end();
+#pragma unroll
+        for (int ct = 0; ct < kCT; ++ct)
+#pragma unroll
+          for (int sb = 0; sb < C / 32; ++sb)
+            V[ct][sb] = X::template cols<DV>(sv, sb * 32, v0 + ct * 16);
 #pragma unroll
         for (int tt = 0; tt < kTT; ++tt) {
           const float into = d.into[tt * 16 + col];
@@ -169,43 +193,53 @@ __global__ __launch_bounds__(kScanThreads) void linear_kernel(LinearArgs A) {
           for (int ct = 0; ct < kCT; ++ct) o[tt][ct] *= into;
 #pragma unroll
           for (int sb = 0; sb <= tt / 2; ++sb) {
-            const Frag p = X::rows(sp, ldp, tt * 16, sb * 32);
+            const Frag p = X::template rows<C>(sp, tt * 16, sb * 32);
 #pragma unroll
             for (int ct = 0; ct < kCT; ++ct) o[tt][ct] = X::mma(V[ct][sb], p, o[tt][ct]);
           }
-          const int t = tt * 16 + col;
-          if (t < valid) {
-            T* out = (T*)A.out + (row + t0 + t) * DV;
 #pragma unroll
-            for (int ct = 0; ct < kCT; ++ct) X::store4(out + (ct0 + ct) * 16 + g4, o[tt][ct]);
-          }
+          for (int ct = 0; ct < kCT; ++ct)
+            X::store4(out, (tt * 16 + col) * DV + v0 + ct * 16 + g4, o[tt][ct]);
         }
+      } else {
+#pragma unroll
+        for (int ct = 0; ct < kCT; ++ct)
+#pragma unroll
+          for (int sb = 0; sb < C / 32; ++sb)
+            V[ct][sb] = X::template cols<DV>(sv, sb * 32, v0 + ct * 16);
       }
       // the state: v (dout in reverse) scaled by its decay, in parts
       const float* scale = kReverse ? d.into : d.onto;
       Frag part[kCT][C / 32][X::kParts];
 #pragma unroll
       for (int sb = 0; sb < C / 32; ++sb) {
-        f32x8 a;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = scale[sb * 32 + 16 * (j / 4) + g4 + j % 4];
+        const f32x8 a = Tile<float>::pack(*reinterpret_cast<const f32x4*>(scale + sb * 32 + g4),
+                                          *reinterpret_cast<const f32x4*>(scale + sb * 32 + 16 + g4));
 #pragma unroll
         for (int ct = 0; ct < kCT; ++ct) X::split(X::widen(V[ct][sb]) * a, part[ct][sb]);
       }
       const float whole = d.whole;
+      schedule_end();
 #pragma unroll
       for (int kt = 0; kt < kKT; ++kt) {
 #pragma unroll
         for (int ct = 0; ct < kCT; ++ct) S[kt][ct] *= whole;
 #pragma unroll
         for (int sb = 0; sb < C / 32; ++sb) {
-          const Frag k = X::cols(sk, ldk, sb * 32, kt * 16);
+          const Frag k = X::template cols<DK>(sk, sb * 32, kt * 16);
 #pragma unroll
-          for (int p = 0; p < X::kParts; ++p)
+          for (int j = 0; j < X::kParts; ++j)
 #pragma unroll
-            for (int ct = 0; ct < kCT; ++ct) S[kt][ct] = X::mma(k, part[ct][sb][p], S[kt][ct]);
+            for (int ct = 0; ct < kCT; ++ct) S[kt][ct] = X::mma(k, part[ct][sb][j], S[kt][ct]);
         }
       }
+      schedule_reads<2 * X::kColReads>();  // two fragments ahead
+#pragma unroll
+      for (int i = 0; i < kKT * (C / 32); ++i) {
+        schedule_reads<X::kColReads>();
+        schedule_products<X::kParts * kCT * X::kProducts>();
+      }
+      schedule_end();
     }
     __syncthreads();  // the LDS blocks are read
   }
@@ -217,21 +251,15 @@ __global__ __launch_bounds__(kScanThreads) void linear_kernel(LinearArgs A) {
   } else if (seg == A.nseg - 1) {
     to = A.S + (int64_t)bh * DK * DV;
   }
-  if (to && mine) {
-#pragma unroll
-    for (int kt = 0; kt < kKT; ++kt)
-#pragma unroll
-      for (int ct = 0; ct < kCT; ++ct)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          to[(kt * 16 + g4 + i) * DV + (ct0 + ct) * 16 + col] = S[kt][ct][i];
-  }
+  if (to && mine) store_state(to);
 }
 
 template <class T, int DK, int DV>
 hipError_t launch_mode(const LinearArgs& a, int mode, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)a.BH * a.nseg)), block(kScanThreads);
-  if (mode == 0)
+  if (mode == 0 && a.tape)
+    hipLaunchKernelGGL((linear_kernel<T, DK, DV, 3>), grid, block, 0, stream, a);
+  else if (mode == 0)
     hipLaunchKernelGGL((linear_kernel<T, DK, DV, 0>), grid, block, 0, stream, a);
   else if (mode == 1)
     hipLaunchKernelGGL((linear_kernel<T, DK, DV, 1>), grid, block, 0, stream, a);

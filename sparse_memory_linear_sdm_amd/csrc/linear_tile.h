@@ -21,39 +21,50 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// LDS rows are padded by 16 bytes: rows start 4 banks apart (of 64), so that
-// both kinds of fragment reads spread evenly over the banks.
+// LDS matrices of rows of D values, padded by 16 bytes: rows start 4 banks apart
+// (of 64), so that reads along rows and fp32's along columns touch every bank
+// once, at addresses with constant distances.  (bf16's transposed reads meet
+// twice in a bank.  16-byte segments that change places by the row avoid that
+// and cost more in address arithmetic and in register moves.)
 template <class T>
 struct Tile;
 
 template <>
 struct Tile<uint16_t> {
   static constexpr int kChunk = 64;  // steps
-  static constexpr int kPad = 8;     // values
+  template <int D>
+  static constexpr int kLd = D + 8;  // values from row to row
+  template <int D>
+  static __device__ __forceinline__ int at(int row, int col) {
+    return row * kLd<D> + col;
+  }
   // Parts of a scaled operand whose product must keep fp32's precision: a bf16
   // part holds 8 of the 24 bits.
   static constexpr int kParts = 3;
+  static constexpr int kRowReads = 1, kColReads = 2, kProducts = 1;  // instructions
   typedef bf16x8 Frag;
 
   static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
   // Row `row0 + l % 16` of an LDS matrix, inner values k0 .. k0 + 31 along it.
-  static __device__ __forceinline__ Frag rows(const uint16_t* m, int ld, int row0, int k0) {
+  template <int D>
+  static __device__ __forceinline__ Frag rows(const uint16_t* m, int row0, int k0) {
     const int l = lane_id();
-    const uint16_t* p = m + (row0 + (l & 15)) * ld + k0 + 4 * (l >> 4);
+    const uint16_t* p = m + at<D>(row0 + (l & 15), k0 + 4 * (l >> 4));
     const bf16x4 a = *reinterpret_cast<const bf16x4*>(p);
     const bf16x4 b = *reinterpret_cast<const bf16x4*>(p + 16);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
   // Column `col0 + l % 16`, inner values k0 .. k0 + 31 down the rows: transposed
   // reads (16 lanes read 4 rows of 16 values, each gets one column).
-  static __device__ __forceinline__ Frag cols(const uint16_t* m, int ld, int k0, int col0) {
+  template <int D>
+  static __device__ __forceinline__ Frag cols(const uint16_t* m, int k0, int col0) {
     typedef __attribute__((address_space(3))) s16x4* lds_ptr;
     const int l = lane_id();
-    const uint16_t* p = m + (k0 + 4 * (l >> 4) + ((l & 15) >> 2)) * ld + col0 + 4 * (l & 3);
+    const uint16_t* p = m + at<D>(k0 + 4 * (l >> 4) + ((l & 15) >> 2), col0 + 4 * (l & 3));
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 16 * ld));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 16 * kLd<D>));
     return __builtin_shufflevector(__builtin_bit_cast(bf16x4, a), __builtin_bit_cast(bf16x4, b),
                                    0, 1, 2, 3, 4, 5, 6, 7);
   }
@@ -64,7 +75,7 @@ struct Tile<uint16_t> {
   static __device__ __forceinline__ f32x8 widen(Frag a) {
     return __builtin_convertvector(a, f32x8);
   }
-  // x as the sum of kParts operands, to within 2^-26 of it
+  // x as the sum of kParts operands, to within 2^-24 of it
   static __device__ __forceinline__ void split(f32x8 x, Frag* part) {
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
@@ -75,6 +86,10 @@ struct Tile<uint16_t> {
   static __device__ __forceinline__ void store4(uint16_t* p, f32x4 x) {
     *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(x, bf16x4);
   }
+  static __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t b, int at, f32x4 x) {
+    __builtin_amdgcn_raw_buffer_store_b64(
+        __builtin_bit_cast(u32x2, __builtin_convertvector(x, bf16x4)), b, at * 2, 0, 0);
+  }
   static __device__ __forceinline__ f32x4 load4(const uint16_t* p) {
     return __builtin_convertvector(*reinterpret_cast<const bf16x4*>(p), f32x4);
   }
@@ -83,8 +98,14 @@ struct Tile<uint16_t> {
 template <>
 struct Tile<float> {
   static constexpr int kChunk = 32;
-  static constexpr int kPad = 4;
+  template <int D>
+  static constexpr int kLd = D + 4;
+  template <int D>
+  static __device__ __forceinline__ int at(int row, int col) {
+    return row * kLd<D> + col;
+  }
   static constexpr int kParts = 1;
+  static constexpr int kRowReads = 2, kColReads = 8, kProducts = 8;
   typedef f32x8 Frag;
 
   static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
@@ -92,17 +113,19 @@ struct Tile<float> {
     for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
     return c;
   }
-  static __device__ __forceinline__ Frag rows(const float* m, int ld, int row0, int k0) {
+  template <int D>
+  static __device__ __forceinline__ Frag rows(const float* m, int row0, int k0) {
     const int l = lane_id();
-    const float* p = m + (row0 + (l & 15)) * ld + k0 + 4 * (l >> 4);
+    const float* p = m + at<D>(row0 + (l & 15), k0 + 4 * (l >> 4));
     return pack(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16));
   }
-  static __device__ __forceinline__ Frag cols(const float* m, int ld, int k0, int col0) {
+  template <int D>
+  static __device__ __forceinline__ Frag cols(const float* m, int k0, int col0) {
     const int l = lane_id();
-    const float* p = m + (k0 + 4 * (l >> 4)) * ld + col0 + (l & 15);
+    const float* p = m + at<D>(k0 + 4 * (l >> 4), col0 + (l & 15));
     Frag f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = p[(16 * (j / 4) + j % 4) * ld];
+    for (int j = 0; j < 8; ++j) f[j] = p[(16 * (j / 4) + j % 4) * kLd<D>];
     return f;
   }
   static __device__ __forceinline__ Frag pack(f32x4 a, f32x4 b) {
@@ -113,52 +136,87 @@ struct Tile<float> {
   static __device__ __forceinline__ void store4(float* p, f32x4 x) {
     *reinterpret_cast<f32x4*>(p) = x;
   }
+  static __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t b, int at, f32x4 x) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, at * 4, 0, 0);
+  }
   static __device__ __forceinline__ f32x4 load4(const float* p) {
     return *reinterpret_cast<const f32x4*>(p);
   }
 };
 
+constexpr int kBufWord3 = 0x00020000;  // raw buffer access, gfx9 family
+
+// `bytes` bytes from p on: loads behind them give zeros, stores there nothing.
+// Both are the same in all lanes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  const uint64_t u = (uint64_t)uniform_u32((uint32_t)(a >> 32)) << 32 | uniform_u32((uint32_t)a);
+  return __builtin_amdgcn_make_buffer_rsrc((void*)u, 0, uniform_u32(bytes), kBufWord3);
+}
+
 // One [kChunk, D] block of a [T, D] array: 16-byte pieces through registers
-// into LDS rows of D + kPad values, zeros behind the last step.
+// into an LDS matrix, zeros behind the last step.
 template <class T, int D, int THREADS>
 struct Block {
   static constexpr int kC = Tile<T>::kChunk;
-  static constexpr int kLd = D + Tile<T>::kPad;
+  static constexpr int kSize = kC * Tile<T>::template kLd<D>;
   static constexpr int kRowPieces = D * (int)sizeof(T) / 16;
   static constexpr int kPieces = kC * kRowPieces;
   static constexpr int kN = (kPieces + THREADS - 1) / THREADS;
   u32x4 r[kN];
 
   __device__ __forceinline__ void load(const T* base, int valid_rows) {
+    const __amdgpu_buffer_rsrc_t b = buffer(base, (uint32_t)(valid_rows * D * (int)sizeof(T)));
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int p = threadIdx.x + i * THREADS;
-      r[i] = u32x4{0, 0, 0, 0};
-      if (p < kPieces && p / kRowPieces < valid_rows)
-        r[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base) + p * 16);
-    }
+    for (int i = 0; i < kN; ++i)
+      r[i] = __builtin_amdgcn_raw_buffer_load_b128(b, (threadIdx.x + i * THREADS) * 16, 0, 0);
   }
   __device__ __forceinline__ void store(T* lds) const {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int p = threadIdx.x + i * THREADS;
-      if (p < kPieces)
-        *reinterpret_cast<u32x4*>(lds + (p / kRowPieces) * kLd +
-                                  (p % kRowPieces) * (16 / (int)sizeof(T))) = r[i];
+      if ((i + 1) * THREADS <= kPieces || p < kPieces)
+        *reinterpret_cast<u32x4*>(lds + Tile<T>::template at<D>(p / kRowPieces,
+                                                                (p % kRowPieces) *
+                                                                    (16 / (int)sizeof(T)))) = r[i];
     }
   }
 };
+
+// Waits for loads that are on their way into x.  (At a loop's entry: the
+// compiler waits for registers loaded before a loop inside it, and so for the
+// loads that the loop has just sent out.)
+template <int N>
+__device__ __forceinline__ void arrive(f32x4 (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(x[i]));
+}
+
+// Orders of the instructions of a stretch of code between two calls of
+// schedule_end(): the next n LDS reads, the next n matrix instructions.
+template <int N>
+__device__ __forceinline__ void schedule_reads() {
+  __builtin_amdgcn_sched_group_barrier(0x100, N, 0);
+}
+template <int N>
+__device__ __forceinline__ void schedule_products() {
+  __builtin_amdgcn_sched_group_barrier(0x008, N, 0);
+}
+__device__ __forceinline__ void schedule_end() { __builtin_amdgcn_sched_barrier(0); }
 
 // Decays of one chunk.  The sums of logarithms are formed in 64 bits and kept
 // as two floats, so that the decay between two steps has fp32's precision
 // whatever other steps of the chunk forget.
 template <int C>
-struct Decays {
+struct alignas(16) Decays {
   float hi[C], lo[C];  // log2 of the decay from the chunk's start through step t
   float into[C];       // that decay
   float onto[C];       // decay behind step t to the chunk's end
   float whole;         // of the whole chunk
 };
+
+// 2^x, 0 below 2^-126
+__device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // log2 of one step's decay.  Below 2^-184 = exp(-128) it is 0 in fp32 with
 // any number of further steps; so is -infinity's, without infinities here.
@@ -166,37 +224,76 @@ __device__ __forceinline__ double log2_decay(float g) {
   return (double)(g < -128.0f ? -128.0f : g) * 1.4426950408889634;
 }
 
+// x of lane l - N in its row of 16, 0.0 where there is none
+template <int N>
+__device__ __forceinline__ double row_shr(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, 0x110 + N, 0xF, 0xF, true);
+  const uint32_t hi =
+      (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), 0x110 + N, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
 // By one whole wavefront, step `lane`'s x (0 behind the last step and in lanes
 // at or past C): fills d and returns the chunk's sum.
 template <int C>
 __device__ __forceinline__ double scan_decays(double x, Decays<C>& d) {
   const int l = lane_id();
+  x += row_shr<1>(x);
+  x += row_shr<2>(x);
+  x += row_shr<4>(x);
+  x += row_shr<8>(x);
+  double below = 0.0, sum = lane_value(x, 15);
 #pragma unroll
-  for (int o = 1; o < C; o <<= 1) {
-    const double y = __shfl_up(x, o);
-    if (l >= o) x += y;
+  for (int r = 1; r < C / 16; ++r) {
+    if (l >> 4 == r) below = sum;
+    sum += lane_value(x, r * 16 + 15);
   }
-  const double sum = __shfl(x, C - 1);
+  x += below;
   if (l < C) {
     const float hi = (float)x;
     d.hi[l] = hi;
     d.lo[l] = (float)(x - (double)hi);
-    d.into[l] = exp2f(hi);
-    d.onto[l] = exp2f((float)(sum - x));
-    if (l == 0) d.whole = exp2f((float)sum);
+    d.into[l] = pow2(hi);
+    d.onto[l] = pow2((float)(sum - x));
+    if (l == 0) d.whole = pow2((float)sum);
   }
   return sum;
 }
 
-// decay behind step s through step t >= s
+// decays behind steps s .. s + 3 through step t, 0 for steps behind t
 template <int C>
-__device__ __forceinline__ float decay_between(const Decays<C>& d, int t, int s) {
-  return exp2f((d.hi[t] - d.hi[s]) + (d.lo[t] - d.lo[s]));
+__device__ __forceinline__ f32x4 decay_between(const Decays<C>& d, int t, int s) {
+  const f32x4 hi = *reinterpret_cast<const f32x4*>(d.hi + s);
+  const f32x4 lo = *reinterpret_cast<const f32x4*>(d.lo + s);
+  const float thi = d.hi[t], tlo = d.lo[t];
+  f32x4 x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float e = pow2((thi - hi[j]) + (tlo - lo[j]));
+    x[j] = s + j <= t ? e : 0.0f;
+  }
+  return x;
+}
+
+// p * decay where there is one: what later steps hold (their decay is 0) does
+// not enter
+__device__ __forceinline__ f32x4 decayed(f32x4 p, f32x4 decay, int t, int s) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p[j] = s + j <= t ? p[j] * decay[j] : 0.0f;
+  return p;
 }
 
 // A contiguous range of memories per XCD (workgroups go to the 8 XCDs in turn),
 // so that heads that share keys share an L2.
-__device__ __forceinline__ int64_t xcd_contiguous(int64_t block, int64_t n) {
+__device__ __forceinline__ uint32_t xcd_contiguous(uint32_t block, uint32_t n) {
   return n % 8 == 0 ? (block & 7) * (n / 8) + (block >> 3) : block;
 }
 
