@@ -96,10 +96,10 @@ hipError_t launch_chunks(const LinearArgs& a, int dtype, int d_k, int d_v, int m
                     : launch_linear_f32(a, d_k, d_v, mode, stream);
 }
 
-void set_segments(LinearArgs& a, int dtype, bool backward) {
+void set_segments(LinearArgs& a, int dtype, int d_k, int d_v, bool backward) {
   const int chunk = linear_chunk(dtype);
   a.nchunk = (int)((a.T + chunk - 1) / chunk);
-  a.nseg = linear_segments(dtype, a.BH, a.T, backward);
+  a.nseg = linear_segments(dtype, a.BH, a.T, d_k, d_v, backward);
   a.seg_chunks = (a.nchunk + a.nseg - 1) / a.nseg;
   a.nseg = (a.nchunk + a.seg_chunks - 1) / a.seg_chunks;
 }
@@ -190,26 +190,30 @@ hipError_t launch_step_type(float* S, int BH, int share, int d_k, int d_v, const
 
 }  // namespace
 
-int linear_segments(int dtype, int64_t BH, int64_t T, bool backward) {
+// Segments of a memory's steps: as many as give every compute unit its
+// workgroups (two of the forward's a unit, one of the reverse pass' where heads
+// are 128 wide, two otherwise; one more memory's worth would run alone in a
+// second round), of at least four chunks.
+int linear_segments(int dtype, int64_t BH, int64_t T, int d_k, int d_v, bool backward) {
   const int64_t chunks = (T + linear_chunk(dtype) - 1) / linear_chunk(dtype);
-  const int64_t want = (512 + BH - 1) / BH, most = chunks / 4;
+  const int64_t want = (backward && (d_k == 128 || d_v == 128) ? 256 : 512) / BH, most = chunks / 4;
   const int64_t n = want < most ? want : most;
   return n < 1 ? 1 : (int)n;
 }
 
 size_t linear_scan_workspace_bytes(int dtype, int64_t BH, int d_k, int d_v, int64_t T) {
-  return segment_bytes(BH, linear_segments(dtype, BH, T, false), d_k * d_v);
+  return segment_bytes(BH, linear_segments(dtype, BH, T, d_k, d_v, false), d_k * d_v);
 }
 
 size_t linear_backward_workspace_bytes(int dtype, int64_t BH, int share, int d_k, int d_v,
                                        int64_t T) {
   const size_t part = share > 1 ? 2 * align256((size_t)BH * T * d_k * 4) : 0;
-  return part + segment_bytes(BH, linear_segments(dtype, BH, T, true), d_k * d_v);
+  return part + segment_bytes(BH, linear_segments(dtype, BH, T, d_k, d_v, true), d_k * d_v);
 }
 
 hipError_t launch_linear_scan(LinearArgs a, int dtype, int d_k, int d_v, void* ws,
                               hipStream_t stream) {
-  set_segments(a, dtype, false);
+  set_segments(a, dtype, d_k, d_v, false);
   char* p = (char*)ws;
   place_segments(a, d_k * d_v, p);
   hipError_t rc;
@@ -222,7 +226,7 @@ hipError_t launch_linear_scan(LinearArgs a, int dtype, int d_k, int d_v, void* w
 
 hipError_t launch_linear_backward(LinearArgs a, int dtype, int d_k, int d_v, void* ws,
                                   hipStream_t stream) {
-  set_segments(a, dtype, true);
+  set_segments(a, dtype, d_k, d_v, true);
   char* p = (char*)ws;
   place_segments(a, d_k * d_v, p);
   const int64_t per_head = a.T * d_k;

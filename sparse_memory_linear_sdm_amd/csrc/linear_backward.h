@@ -48,12 +48,16 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
   __shared__ __align__(16) T sq[BlockK::kSize];
   __shared__ __align__(16) T sk[BlockK::kSize];
   __shared__ __align__(16) T sv[BlockV::kSize];
-  __shared__ __align__(16) T so[BlockV::kSize];   // dout
-  __shared__ __align__(16) T sp[kSizeP];   // (q_t . k_s) D_ts, rows t
-  __shared__ __align__(16) T sdp[kSizeP];  // (do_t . v_s) D_ts, rows t
+  __shared__ __align__(16) T so[BlockV::kSize];  // dout
+  __shared__ __align__(16) T sp[kSizeP];         // (q_t . k_s) D_ts, rows t
+  __shared__ __align__(16) T sdp[kSizeP];        // (do_t . v_s) D_ts, rows t
   __shared__ Decays<C> sd[2];
-  __shared__ float srow[kTT][C], scol[kTT][C];  // sums of W by tiles
-  __shared__ float se[kKT][C], sf[kKT][C], sx[kKT];
+  // what dg is summed from, for this chunk and the one before it
+  struct Paths {
+    float row[kTT][C], col[kTT][C];    // sums of W by tiles
+    float e[kKT][C], f[kKT][C], x[kKT];  // by wavefronts; x: exp(L_C) <S, G>
+  };
+  __shared__ Paths paths[2];
 
   const int lane = lane_id(), col = lane & 15, g4 = 4 * (lane >> 4);
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -67,8 +71,9 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
   const T* gv = (const T*)A.v + row * DV;
   const T* go = (const T*)A.dout + row * DV;
   const float* gg = A.g + row;
-  const bool has_k = w < kKT, has_v = w < kVT;
-  const int k0 = w * 16, v0 = w * 16;  // this wavefront's columns of k and of v
+  // this wavefront's columns of k and of v
+  const bool has_k = kKT == NW || w < kKT, has_v = kVT == NW || w < kVT;
+  const int k0 = w * 16, v0 = w * 16;
 
   f32x4 Gk[kKT];  // rows of k, columns v0 .. v0 + 15
   f32x4 Gv[kVT];  // rows of v, columns k0 .. k0 + 15
@@ -100,146 +105,120 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
     bv.load(gv + t0 * DV, valid);
     bo.load(go + t0 * DV, valid);
   };
-  float step_g = 0.0f;  // of step `lane`
-  auto load_g = [&](int c) {
-    step_g = __builtin_bit_cast(
+  auto g_of = [&](int c) {  // of step `lane` of chunk c
+    return __builtin_bit_cast(
         float, __builtin_amdgcn_raw_buffer_load_b32(
                    buffer(gg + (int64_t)c * C, (uint32_t)rows_of(c) * 4), lane * 4, 0, 0));
   };
+  // the state before the chunk, rows k0 .. k0 + 15, as operands along v
+  f32x4 S[kVT];
+  auto load_state = [&](int c) {
+    const __amdgpu_buffer_rsrc_t b = buffer(A.tape + ((int64_t)bh * A.nchunk + c) * DK * DV,
+                                            c < c_first ? 0 : DK * DV * 4);
+#pragma unroll
+    for (int vt = 0; vt < kVT; ++vt)
+      S[vt] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                            b, ((k0 + col) * DV + g4 + vt * 16) * 4, 0, 0));
+  };
+  // dg of chunk c, by one wavefront
+  auto gate = [&](int c, float g) {
+    const Paths& p = paths[c & 1];
+    double behind = 0.0, before = 0.0, x = 0.0;
+    if (lane < C) {
+      const int tile = lane >> 4;
+#pragma unroll
+      for (int i = 0; i < kTT; ++i) {
+        if (i <= tile) behind += (double)p.row[i][lane];
+        if (i >= tile) behind -= (double)p.col[i][lane];
+      }
+#pragma unroll
+      for (int i = 0; i < kKT; ++i) {
+        behind += (double)p.e[i][lane];
+        before += (double)p.f[i][lane];
+        x += (double)p.x[i];
+      }
+    }
+    const double f = before;
+#pragma unroll
+    for (int o = 1; o < C; o <<= 1) {
+      const double u = __shfl_down(behind, o), v = __shfl_up(before, o);
+      if (lane + o < C) behind += u;
+      if (lane >= o) before += v;
+    }
+    // a step that forgets everything has no path across it: exactly 0
+    const float dg = g <= -128.0f ? 0.0f : (float)(behind + (before - f) + x);
+    __builtin_amdgcn_raw_buffer_store_b32(
+        __float_as_uint(dg), buffer(A.dg + row + (int64_t)c * C, (uint32_t)rows_of(c) * 4),
+        lane * 4, 0, 0);
+  };
+
+  // g runs one chunk further ahead than the blocks, its sums come first
+  float g_now = g_of(c_end - 1), g_next = g_of(c_end - 2), g_last = 0.0f;
   load(c_end - 1);
-  load_g(c_end - 1);
+  if (has_k) load_state(c_end - 1);
+  if (w == NW - 1) scan_decays<C>(log2_decay(g_now), sd[(c_end - 1) & 1]);
   arrive(Gk);
   arrive(Gv);
-  if (w == NW - 1) scan_decays<C>(log2_decay(step_g), sd[(c_end - 1) & 1]);
 
   for (int c = c_end - 1; c >= c_first; --c) {
     const Decays<C>& d = sd[c & 1];
+    Paths& path = paths[c & 1];
     const int64_t t0 = (int64_t)c * C;
     const int valid = rows_of(c);
     bq.store(sq);
     bk.store(sk);
     bv.store(sv);
     bo.store(so);
-    // the state before the chunk, rows k0 .. k0 + 15, as operands along v
-    f32x8 S[DV / 32];
-    if (has_k) {
-      const float* tape = A.tape + ((int64_t)bh * A.nchunk + c) * DK * DV + (k0 + col) * DV + g4;
-#pragma unroll
-      for (int vb = 0; vb < DV / 32; ++vb)
-        S[vb] = Tile<float>::pack(*reinterpret_cast<const f32x4*>(tape + vb * 32),
-                                  *reinterpret_cast<const f32x4*>(tape + vb * 32 + 16));
-    }
     __syncthreads();
+    const float g_ahead = g_of(c - 2);
     load(c - 1);
-    const float this_g = step_g;
-    load_g(c - 1);
+    if (w == NW / 2 && c + 1 < c_end) gate(c + 1, g_last);
     // ---- pairs of steps: P, dP and the sums of W
-    constexpr int kUnits = kTT == 4 ? 12 : 4;
-    for (int u = w; u < kUnits; u += NW) {
+    constexpr int kUnits = kTT == 4 ? 12 : 4;  // tiles that a product below reads
+#pragma unroll
+    for (int u0 = 0; u0 < kUnits; u0 += NW) {
+      const int u = u0 + w;
+      if (u0 + NW > kUnits && u >= kUnits) continue;
       const int tt = u < 4 ? u >> 1 : 2 + ((u - 4) >> 2), st = u < 4 ? u & 1 : (u - 4) & 3;
       f32x4 p = {0, 0, 0, 0}, dp = {0, 0, 0, 0};
       const int t = tt * 16 + col, s = st * 16 + g4;
-      if (st <= tt) {
 #pragma unroll
-        for (int kb = 0; kb < DK / 32; ++kb)
-          p = X::mma(X::template rows<DK>(sk, st * 16, kb * 32), X::template rows<DK>(sq, tt * 16, kb * 32), p);
+      for (int kb = 0; kb < DK / 32; ++kb)
+        p = X::mma(X::template rows<DK>(sk, st * 16, kb * 32),
+                   X::template rows<DK>(sq, tt * 16, kb * 32), p);
 #pragma unroll
-        for (int vb = 0; vb < DV / 32; ++vb)
-          dp = X::mma(X::template rows<DV>(sv, st * 16, vb * 32), X::template rows<DV>(so, tt * 16, vb * 32), dp);
-        float by_row = 0.0f, by_col[4];
-        const f32x4 decay = decay_between<C>(d, t, s);
-        const f32x4 raw = dp;
-        p = decayed(p, decay, t, s);
-        dp = decayed(dp, decay, t, s);
+      for (int vb = 0; vb < DV / 32; ++vb)
+        dp = X::mma(X::template rows<DV>(sv, st * 16, vb * 32),
+                    X::template rows<DV>(so, tt * 16, vb * 32), dp);
+      const f32x4 decay = decay_between<C>(d, t, s);
+      const f32x4 raw = dp;
+      p = decayed(p, decay, t, s);
+      dp = decayed(dp, decay, t, s);
+      float by_row = 0.0f, by_col[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          by_col[j] = s + j < t ? p[j] * raw[j] : 0.0f;
-          by_row += by_col[j];
-        }
-        by_row += __shfl_xor(by_row, 16);
-        by_row += __shfl_xor(by_row, 32);
-        if (lane < 16) srow[st][t] = by_row;
+      for (int j = 0; j < 4; ++j) {
+        by_col[j] = s + j < t ? p[j] * raw[j] : 0.0f;
+        by_row += by_col[j];
+      }
+      by_row += __uint_as_float(lane_xor(__float_as_uint(by_row), 16));
+      by_row += __uint_as_float(lane_xor(__float_as_uint(by_row), 32));
+      if (lane < 16) path.row[st][t] = by_row;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int o = 1; o < 16; o <<= 1)
-            by_col[j] += __uint_as_float(lane_xor(__float_as_uint(by_col[j]), o));
-          if (col == 0) scol[tt][s + j] = by_col[j];
-        }
+        for (int o = 1; o < 16; o <<= 1)
+          by_col[j] += __uint_as_float(lane_xor(__float_as_uint(by_col[j]), o));
+        if (col == 0) path.col[tt][s + j] = by_col[j];
       }
       X::store4(sp + X::template at<C>(t, s), p);
       X::store4(sdp + X::template at<C>(t, s), dp);
     }
-    if (w == NW - 1) scan_decays<C>(log2_decay(step_g), sd[(c - 1) & 1]);
-    // ---- the state's parts of the gradients, transposed: a lane holds four
-    // consecutive values of one step
-    f32x4 dq[kTT], dk[kTT], dv[kTT];
-#pragma unroll
-    for (int i = 0; i < kTT; ++i) dq[i] = dk[i] = dv[i] = f32x4{0, 0, 0, 0};
-    if (has_k) {
-      float x = 0.0f;
-#pragma unroll
-      for (int vb = 0; vb < DV / 32; ++vb) {
-        // S and G enter dg with fp32's precision, in parts
-        Frag sp3[X::kParts], gp3[X::kParts];
-        const f32x8 G = Tile<float>::pack(Gv[2 * vb], Gv[2 * vb + 1]);
-        X::split(S[vb], sp3);
-        X::split(G, gp3);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x += S[vb][j] * G[j];
-#pragma unroll
-        for (int i = 0; i < kTT; ++i) {
-          const Frag o = X::template rows<DV>(so, i * 16, vb * 32), v = X::template rows<DV>(sv, i * 16, vb * 32);
-#pragma unroll
-          for (int p = 0; p < X::kParts; ++p) {
-            dq[i] = X::mma(sp3[p], o, dq[i]);
-            dk[i] = X::mma(gp3[p], v, dk[i]);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kTT; ++i) {
-        const int t = i * 16 + col;
-        dq[i] *= d.into[t];
-        dk[i] *= d.onto[t];
-        const f32x4 q = X::load4(sq + X::template at<DK>(t, k0 + g4)),
-                    k = X::load4(sk + X::template at<DK>(t, k0 + g4));
-        float e = 0.0f, f = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          e += q[j] * dq[i][j];
-          f += k[j] * dk[i][j];
-        }
-        e += __shfl_xor(e, 16);
-        e += __shfl_xor(e, 32);
-        f += __shfl_xor(f, 16);
-        f += __shfl_xor(f, 32);
-        if (lane < 16) {
-          se[w][t] = e;
-          sf[w][t] = f;
-        }
-      }
-      x = wave_sum_f32(x);
-      if (lane == 0) sx[w] = x;
-    }
-    if (has_v) {
-#pragma unroll
-      for (int kb = 0; kb < DK / 32; ++kb) {
-        const Frag G = X::pack(Gk[2 * kb], Gk[2 * kb + 1]);
-#pragma unroll
-        for (int i = 0; i < kTT; ++i) dv[i] = X::mma(G, X::template rows<DK>(sk, i * 16, kb * 32), dv[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < kTT; ++i) dv[i] *= d.onto[i * 16 + col];
-    }
+    if (w == NW - 1) scan_decays<C>(log2_decay(g_next), sd[(c - 1) & 1]);
     __syncthreads();
-    // ---- the pairs' parts, and the state's gradient before the chunk
+
+    // ---- the gradients, transposed (a lane holds four consecutive values of one
+    // step): the state's part, then the pairs'.  Then G before the chunk.
     const float whole = d.whole;
-    f32x8 into[C / 32];
-#pragma unroll
-    for (int tb = 0; tb < C / 32; ++tb)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) into[tb][j] = d.into[tb * 32 + 16 * (j / 4) + g4 + j % 4];
     if (has_k) {
       const bool shared = A.share > 1;
       const int64_t at0 = (row + t0) * DK;
@@ -247,31 +226,97 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
       const __amdgpu_buffer_rsrc_t
           out_q = buffer(shared ? (void*)(A.dq_part + at0) : (void*)((T*)A.dq + at0), bytes),
           out_k = buffer(shared ? (void*)(A.dk_part + at0) : (void*)((T*)A.dk + at0), bytes);
-      Frag kc[C / 32], qc[C / 32];
+      f32x4 a[kTT];
+      auto store_rows = [&](__amdgpu_buffer_rsrc_t out) {
+        if (shared) {
 #pragma unroll
-      for (int b = 0; b < C / 32; ++b) {
-        kc[b] = X::template cols<DK>(sk, b * 32, k0);
-        qc[b] = X::template cols<DK>(sq, b * 32, k0);
+          for (int i = 0; i < kTT; ++i)
+            Tile<float>::store4(out, (i * 16 + col) * DK + k0 + g4, a[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTT; ++i) X::store4(out, (i * 16 + col) * DK + k0 + g4, a[i]);
+        }
+      };
+      float x = 0.0f;
+      // dq.  S and G enter dg with fp32's precision, in parts
+#pragma unroll
+      for (int i = 0; i < kTT; ++i) a[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int vb = 0; vb < DV / 32; ++vb) {
+        const f32x8 s = Tile<float>::pack(S[2 * vb], S[2 * vb + 1]);
+        const f32x8 G = Tile<float>::pack(Gv[2 * vb], Gv[2 * vb + 1]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x += s[j] * G[j];
+        Frag part[X::kParts];
+        X::split(s, part);
+#pragma unroll
+        for (int i = 0; i < kTT; ++i) {
+          const Frag o = X::template rows<DV>(so, i * 16, vb * 32);
+#pragma unroll
+          for (int p = 0; p < X::kParts; ++p) a[i] = X::mma(part[p], o, a[i]);
+        }
       }
+      load_state(c - 1);
+      x = wave_sum_f32(x);
+      if (lane == 0) path.x[w] = x * whole;
+      {
+        Frag kc[C / 32];
+#pragma unroll
+        for (int b = 0; b < C / 32; ++b) kc[b] = X::template cols<DK>(sk, b * 32, k0);
+#pragma unroll
+        for (int i = 0; i < kTT; ++i) {
+          const int t = i * 16 + col;
+          a[i] *= d.into[t];
+          const f32x4 q = X::load4(sq + X::template at<DK>(t, k0 + g4));
+          float e = (q[0] * a[i][0] + q[1] * a[i][1]) + (q[2] * a[i][2] + q[3] * a[i][3]);
+          e += __uint_as_float(lane_xor(__float_as_uint(e), 16));
+          e += __uint_as_float(lane_xor(__float_as_uint(e), 32));
+          if (lane < 16) path.e[w][t] = e;
+#pragma unroll
+          for (int b = 0; b <= i / 2; ++b)
+            a[i] = X::mma(kc[b], X::template rows<C>(sdp, i * 16, b * 32), a[i]);
+        }
+        store_rows(out_q);
+      }
+      // dk
+#pragma unroll
+      for (int i = 0; i < kTT; ++i) a[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int vb = 0; vb < DV / 32; ++vb) {
+        Frag part[X::kParts];
+        X::split(Tile<float>::pack(Gv[2 * vb], Gv[2 * vb + 1]), part);
+#pragma unroll
+        for (int i = 0; i < kTT; ++i) {
+          const Frag v = X::template rows<DV>(sv, i * 16, vb * 32);
+#pragma unroll
+          for (int p = 0; p < X::kParts; ++p) a[i] = X::mma(part[p], v, a[i]);
+        }
+      }
+      Frag qc[C / 32];
+#pragma unroll
+      for (int b = 0; b < C / 32; ++b) qc[b] = X::template cols<DK>(sq, b * 32, k0);
 #pragma unroll
       for (int i = 0; i < kTT; ++i) {
+        const int t = i * 16 + col;
+        a[i] *= d.onto[t];
+        const f32x4 k = X::load4(sk + X::template at<DK>(t, k0 + g4));
+        float f = (k[0] * a[i][0] + k[1] * a[i][1]) + (k[2] * a[i][2] + k[3] * a[i][3]);
+        f += __uint_as_float(lane_xor(__float_as_uint(f), 16));
+        f += __uint_as_float(lane_xor(__float_as_uint(f), 32));
+        if (lane < 16) path.f[w][t] = f;
 #pragma unroll
-        for (int b = 0; b < C / 32; ++b) {
-          if (b <= i / 2) dq[i] = X::mma(kc[b], X::template rows<C>(sdp, i * 16, b * 32), dq[i]);
-          if (b >= i / 2) dk[i] = X::mma(qc[b], X::template cols<C>(sdp, b * 32, i * 16), dk[i]);
-        }
-        const int at = (i * 16 + col) * DK + k0 + g4;
-        if (A.share == 1) {
-          X::store4(out_q, at, dq[i]);
-          X::store4(out_k, at, dk[i]);
-        } else {
-          Tile<float>::store4(out_q, at, dq[i]);
-          Tile<float>::store4(out_k, at, dk[i]);
-        }
+        for (int b = i / 2; b < C / 32; ++b)
+          a[i] = X::mma(qc[b], X::template cols<C>(sdp, b * 32, i * 16), a[i]);
       }
+      store_rows(out_k);
       Frag part[C / 32][X::kParts];
 #pragma unroll
-      for (int b = 0; b < C / 32; ++b) X::split(X::widen(qc[b]) * into[b], part[b]);
+      for (int b = 0; b < C / 32; ++b)
+        X::split(X::widen(qc[b]) *
+                     Tile<float>::pack(*reinterpret_cast<const f32x4*>(d.into + b * 32 + g4),
+                                       *reinterpret_cast<const f32x4*>(d.into + b * 32 + 16 + g4)),
+                 part[b]);
+      schedule_end();
 #pragma unroll
       for (int vt = 0; vt < kVT; ++vt) {
         Gv[vt] *= whole;
@@ -282,23 +327,53 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
           for (int p = 0; p < X::kParts; ++p) Gv[vt] = X::mma(o, part[b][p], Gv[vt]);
         }
       }
+      schedule_reads<4 * X::kColReads>();  // four fragments ahead
+#pragma unroll
+      for (int j = 0; j < kVT * (C / 32); ++j) {
+        schedule_reads<X::kColReads>();
+        schedule_products<X::kParts * X::kProducts>();
+      }
+      schedule_end();
     }
     if (has_v) {
       const __amdgpu_buffer_rsrc_t out_v =
           buffer((T*)A.dv + (row + t0) * DV, (uint32_t)(valid * DV * (int)sizeof(T)));
+      f32x4 a[kTT];
+#pragma unroll
+      for (int i = 0; i < kTT; ++i) a[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int kb = 0; kb < DK / 32; ++kb) {
+        const Frag G = X::pack(Gk[2 * kb], Gk[2 * kb + 1]);
+#pragma unroll
+        for (int i = 0; i < kTT; ++i)
+          a[i] = X::mma(G, X::template rows<DK>(sk, i * 16, kb * 32), a[i]);
+      }
+      schedule_reads<2 * kTT * X::kRowReads>();
+#pragma unroll
+      for (int kb = 0; kb < DK / 32; ++kb) {
+        schedule_reads<kTT * X::kRowReads>();
+        schedule_products<kTT * X::kProducts>();
+      }
+      schedule_end();
       Frag oc[C / 32];
 #pragma unroll
       for (int b = 0; b < C / 32; ++b) oc[b] = X::template cols<DV>(so, b * 32, v0);
 #pragma unroll
       for (int i = 0; i < kTT; ++i) {
+        a[i] *= d.onto[i * 16 + col];
 #pragma unroll
         for (int b = i / 2; b < C / 32; ++b)
-          dv[i] = X::mma(oc[b], X::template cols<C>(sp, b * 32, i * 16), dv[i]);
-        X::store4(out_v, (i * 16 + col) * DV + v0 + g4, dv[i]);
+          a[i] = X::mma(oc[b], X::template cols<C>(sp, b * 32, i * 16), a[i]);
+        X::store4(out_v, (i * 16 + col) * DV + v0 + g4, a[i]);
       }
       Frag part[C / 32][X::kParts];
 #pragma unroll
-      for (int b = 0; b < C / 32; ++b) X::split(X::widen(oc[b]) * into[b], part[b]);
+      for (int b = 0; b < C / 32; ++b)
+        X::split(X::widen(oc[b]) *
+                     Tile<float>::pack(*reinterpret_cast<const f32x4*>(d.into + b * 32 + g4),
+                                       *reinterpret_cast<const f32x4*>(d.into + b * 32 + 16 + g4)),
+                 part[b]);
+      schedule_end();
 #pragma unroll
       for (int kt = 0; kt < kKT; ++kt) {
         Gk[kt] *= whole;
@@ -309,45 +384,29 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
           for (int p = 0; p < X::kParts; ++p) Gk[kt] = X::mma(q, part[b][p], Gk[kt]);
         }
       }
+      schedule_reads<4 * X::kColReads>();
+#pragma unroll
+      for (int j = 0; j < kKT * (C / 32); ++j) {
+        schedule_reads<X::kColReads>();
+        schedule_products<X::kParts * X::kProducts>();
+      }
+      schedule_end();
     }
-    if (w == 0) {  // dg of step `lane`
-      double behind = 0.0, before = 0.0, x = 0.0;
-      if (lane < C) {
-        const int tile = lane >> 4;
-#pragma unroll
-        for (int i = 0; i < kTT; ++i) {
-          if (i <= tile) behind += (double)srow[i][lane];
-          if (i >= tile) behind -= (double)scol[i][lane];
-        }
-#pragma unroll
-        for (int i = 0; i < kKT; ++i) {
-          behind += (double)se[i][lane];
-          before += (double)sf[i][lane];
-          x += (double)sx[i];
-        }
-      }
-      const double f = before;
-#pragma unroll
-      for (int o = 1; o < C; o <<= 1) {
-        const double u = __shfl_down(behind, o), v = __shfl_up(before, o);
-        if (lane + o < C) behind += u;
-        if (lane >= o) before += v;
-      }
-      if (lane < valid) {
-        // a step that forgets everything has no path across it: exactly 0
-        const bool none = this_g <= -128.0f;
-        A.dg[row + t0 + lane] = none ? 0.0f : (float)(behind + (before - f) + x * (double)whole);
-      }
-    }
+    g_last = g_now;
+    g_now = g_next;
+    g_next = g_ahead;
     __syncthreads();  // the LDS blocks are read
   }
+  if (w == NW / 2) gate(c_first, g_last);
 
   if (seg == 0 && has_v) {
-    float* to = A.S + (int64_t)bh * DK * DV;
+    const __amdgpu_buffer_rsrc_t to = buffer(A.S + (int64_t)bh * DK * DV, DK * DV * 4);
 #pragma unroll
     for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) to[(kt * 16 + g4 + i) * DV + v0 + col] = Gk[kt][i];
+      for (int i = 0; i < 4; ++i)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(Gk[kt][i]), to,
+                                              (g4 * DV + v0 + col) * 4, (kt * 16 + i) * DV * 4, 0);
   }
 }
 
