@@ -62,6 +62,13 @@ hipError_t launch_linear_backward_f32(const LinearArgs& a, int d_k, int d_v, hip
 
 // Norm rows of d values (a multiple of 8, at most kNormMaxD).
 constexpr int kNormMaxD = 16384;
+struct NormDivisor {
+  uint32_t mul;
+  int shift;
+  __device__ __forceinline__ uint32_t of(uint32_t n) const {
+    return (uint32_t)((uint64_t)n * mul >> shift);
+  }
+};
 struct NormArgs {
   const void* y;
   const float* w;
@@ -80,9 +87,10 @@ struct NormArgs {
   int64_t rows;        // B * T * H
   int64_t T;
   int H, d;
+  NormDivisor by_h, by_t;  // set by the launchers
 };
-hipError_t launch_norm(const NormArgs& a, int y_dtype, int out_dtype, hipStream_t stream);
+hipError_t launch_norm(NormArgs a, int y_dtype, int out_dtype, hipStream_t stream);
 int64_t norm_backward_blocks(int64_t rows, int d);
-hipError_t launch_norm_backward(const NormArgs& a, int y_dtype, int out_dtype, hipStream_t stream);
+hipError_t launch_norm_backward(NormArgs a, int y_dtype, int out_dtype, hipStream_t stream);
 
 }  // namespace sdm
