@@ -51,17 +51,24 @@ int check_workspace(const void* ws, size_t bytes, size_t need) {
   return SDM_OK;
 }
 
+constexpr int64_t kNormRows = (int64_t)1 << 31;
+
+bool norm_d_ok(int d) { return d >= 8 && d <= sdm::kNormMaxD && d % 8 == 0; }
+
+bool norm_rows_ok(int B, int H, int64_t T) {
+  return T < kNormRows && (int64_t)B * H < kNormRows && (int64_t)B * H * T < kNormRows;
+}
+
 int check_norm_sizes(int y_dtype, int out_dtype, float eps, int B, int H, int64_t T, int d) {
   if (!value_dtype(y_dtype) || !value_dtype(out_dtype))
     return fail(SDM_ERR_INVALID, "dtypes must be SDM_F32 or SDM_BF16 (got %d, %d)", y_dtype,
                 out_dtype);
-  if (B < 0 || H < 1 || T < 0) return fail(SDM_ERR_INVALID, "B, T must be >= 0 and H >= 1");
-  if (d < 8 || d > sdm::kNormMaxD || d % 8 != 0)
+  if (B < 0 || H < 1 || T < 0) return fail(SDM_ERR_INVALID, "B and T must be >= 0 and H >= 1");
+  if (!norm_d_ok(d))
     return fail(SDM_ERR_UNSUPPORTED, "d must be a multiple of 8 in [8, %d] (got %d)",
                 sdm::kNormMaxD, d);
   if (!(eps >= 0.0f)) return fail(SDM_ERR_INVALID, "eps must be >= 0");
-  if (T >= ((int64_t)1 << 31) || (int64_t)B * H >= ((int64_t)1 << 31) ||
-      (int64_t)B * H * T >= ((int64_t)1 << 31))
+  if (!norm_rows_ok(B, H, T))
     return fail(SDM_ERR_UNSUPPORTED, "B*H*T must be below 2^31 rows per call");
   return SDM_OK;
 }
@@ -199,7 +206,7 @@ int sdm_norm(const void* y, int y_dtype, const float* w, const void* z, const vo
 }
 
 size_t sdm_norm_backward_workspace_size(int B, int H, int64_t T, int d) {
-  if (check_norm_sizes(SDM_F32, SDM_F32, 0.0f, B, H, T, d)) return 0;
+  if (B < 0 || H < 1 || T < 0 || !norm_d_ok(d) || !norm_rows_ok(B, H, T)) return 0;
   return (size_t)sdm::norm_backward_blocks((int64_t)B * H * T, d) * d * sizeof(float);
 }
 
