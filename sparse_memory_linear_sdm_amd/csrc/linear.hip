@@ -11,59 +11,79 @@ constexpr int kThreads = 256;
 
 // What each segment starts from: the call's state carried through the
 // segments before it (behind it, in reverse).  seg_state[m][i] holds what
-// segment i adds; afterwards what it starts from.
+// segment i adds; afterwards what it starts from.  A thread takes four values
+// of kPer consecutive segments; kGroups threads share a memory's segments, and
+// carry the state over each other's by sums and decays in LDS.  (One thread
+// through 128 segments of 4 memories took 45 us.)
+template <int kGroups, int kPer>
 __global__ __launch_bounds__(kThreads) void linear_segments_kernel(float* seg_state,
                                                                    const double* seg_log,
                                                                    const float* S, int64_t total,
                                                                    int elems, int nseg,
                                                                    bool reverse) {
-  const int64_t at = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-  if (at >= total) return;
-  const int64_t m = at / elems, e = at % elems;
+  constexpr int kLanes = kThreads / kGroups;
+  __shared__ f32x4 sums[kGroups][kLanes];
+  __shared__ float decays[kGroups][kLanes];
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int64_t at = ((int64_t)blockIdx.x * kLanes + lane) * 4;  // whole workgroups: total is
+  const int64_t m = at / elems, e = at % elems;                  // a multiple of 4 kLanes
   f32x4 run = *reinterpret_cast<const f32x4*>(S + at);
   float* p = seg_state + m * nseg * elems + e;
   const double* lg = seg_log + m * nseg;
-  constexpr int kAhead = 8;
-  for (int i0 = 0; i0 < nseg; i0 += kAhead) {
-    f32x4 own[kAhead];
-    float decay[kAhead];
+  const int i0 = group * kPer;
+  f32x4 own[kPer];
+  float decay[kPer];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = reverse ? nseg - 1 - (i0 + j) : i0 + j;
-      if (i0 + j < nseg - 1) {  // the last of the order passes nothing on
-        own[j] = *reinterpret_cast<const f32x4*>(p + (int64_t)i * elems);
-        decay[j] = lin::pow2((float)lg[i]);
-      }
+  for (int j = 0; j < kPer; ++j) {
+    const int i = reverse ? nseg - 1 - (i0 + j) : i0 + j;
+    own[j] = f32x4{0, 0, 0, 0};
+    decay[j] = 1.0f;
+    if (i0 + j < nseg - 1) {  // the last of the order passes nothing on
+      own[j] = *reinterpret_cast<const f32x4*>(p + (int64_t)i * elems);
+      decay[j] = lin::pow2((float)lg[i]);
     }
+  }
+  if (kGroups > 1) {
+    f32x4 sum = own[0];
+    float d = decay[0];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = reverse ? nseg - 1 - (i0 + j) : i0 + j;
-      if (i0 + j < nseg) *reinterpret_cast<f32x4*>(p + (int64_t)i * elems) = run;
-      if (i0 + j < nseg - 1) run = run * decay[j] + own[j];
+    for (int j = 1; j < kPer; ++j) {
+      sum = sum * decay[j] + own[j];
+      d *= decay[j];
     }
+    sums[group][lane] = sum;
+    decays[group][lane] = d;
+    __syncthreads();
+    for (int i = 0; i < group; ++i) run = run * decays[i][lane] + sums[i][lane];
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = reverse ? nseg - 1 - (i0 + j) : i0 + j;
+    if (i0 + j < nseg) *reinterpret_cast<f32x4*>(p + (int64_t)i * elems) = run;
+    run = run * decay[j] + own[j];
   }
 }
 
 // Gradients of shared keys: the sum over the heads that share them, in their
-// order, rounded once.
+// order, rounded once.  blockIdx.y: dq, dk.
 template <class T>
-__global__ __launch_bounds__(kThreads) void linear_share_kernel(const float* part, T* out,
-                                                                int64_t total, int64_t per_head,
-                                                                int share) {
+__global__ __launch_bounds__(kThreads) void linear_share_kernel(LinearArgs A, int64_t total,
+                                                                int64_t per_head) {
   const int64_t at = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
   if (at >= total) return;
-  const float* p = part + at / per_head * per_head * share + at % per_head;
+  const float* p = (blockIdx.y ? A.dk_part : A.dq_part) + at / per_head * per_head * A.share +
+                   at % per_head;
   f32x4 sum = *reinterpret_cast<const f32x4*>(p);
-  for (int i = 1; i < share; ++i) sum += *reinterpret_cast<const f32x4*>(p + i * per_head);
-  lin::Tile<T>::store4(out + at, sum);
+  for (int i = 1; i < A.share; ++i) sum += *reinterpret_cast<const f32x4*>(p + i * per_head);
+  lin::Tile<T>::store4((T*)(blockIdx.y ? A.dk : A.dq) + at, sum);
 }
 
 template <class T>
-hipError_t launch_share(const float* part, void* out, int64_t key_heads, int64_t per_head,
-                        int share, hipStream_t stream) {
-  const int64_t total = key_heads * per_head;
-  hipLaunchKernelGGL((linear_share_kernel<T>), dim3((unsigned)((total / 4 + kThreads - 1) / kThreads)),
-                     dim3(kThreads), 0, stream, part, (T*)out, total, per_head, share);
+hipError_t launch_share(const LinearArgs& a, int64_t per_head, hipStream_t stream) {
+  const int64_t total = a.BH / a.share * per_head;
+  hipLaunchKernelGGL((linear_share_kernel<T>),
+                     dim3((unsigned)((total / 4 + kThreads - 1) / kThreads), 2), dim3(kThreads), 0,
+                     stream, a, total, per_head);
   return hipGetLastError();
 }
 
@@ -82,12 +102,19 @@ void place_segments(LinearArgs& a, int elems, char*& ws) {
   ws += align256((size_t)a.BH * a.nseg * 8);
 }
 
-hipError_t launch_segments(const LinearArgs& a, int elems, bool reverse, hipStream_t stream) {
+template <int kGroups, int kPer>
+hipError_t launch_segments_by(const LinearArgs& a, int elems, bool reverse, hipStream_t stream) {
   const int64_t total = (int64_t)a.BH * elems;
-  hipLaunchKernelGGL(linear_segments_kernel, dim3((unsigned)((total / 4 + kThreads - 1) / kThreads)),
-                     dim3(kThreads), 0, stream, a.seg_state, a.seg_log, a.S, total, elems, a.nseg,
-                     reverse);
+  hipLaunchKernelGGL((linear_segments_kernel<kGroups, kPer>),
+                     dim3((unsigned)(total / (4 * (kThreads / kGroups)))), dim3(kThreads), 0,
+                     stream, a.seg_state, a.seg_log, a.S, total, elems, a.nseg, reverse);
   return hipGetLastError();
+}
+
+hipError_t launch_segments(const LinearArgs& a, int elems, bool reverse, hipStream_t stream) {
+  if (a.nseg <= 8) return launch_segments_by<4, 2>(a, elems, reverse, stream);
+  if (a.nseg <= 32) return launch_segments_by<8, 4>(a, elems, reverse, stream);
+  return launch_segments_by<32, 16>(a, elems, reverse, stream);  // 512 at most
 }
 
 hipError_t launch_chunks(const LinearArgs& a, int dtype, int d_k, int d_v, int mode,
@@ -243,14 +270,8 @@ hipError_t launch_linear_backward(LinearArgs a, int dtype, int d_k, int d_v, voi
   rc = dtype == 1 ? launch_linear_backward_bf16(a, d_k, d_v, stream)
                   : launch_linear_backward_f32(a, d_k, d_v, stream);
   if (rc != hipSuccess || a.share == 1) return rc;
-  const int64_t key_heads = a.BH / a.share;
-  for (int i = 0; i < 2 && rc == hipSuccess; ++i) {
-    const float* part = i ? a.dk_part : a.dq_part;
-    void* out = i ? a.dk : a.dq;
-    rc = dtype == 1 ? launch_share<uint16_t>(part, out, key_heads, per_head, a.share, stream)
-                    : launch_share<float>(part, out, key_heads, per_head, a.share, stream);
-  }
-  return rc;
+  return dtype == 1 ? launch_share<uint16_t>(a, per_head, stream)
+                    : launch_share<float>(a, per_head, stream);
 }
 
 hipError_t launch_linear_step(float* S, int dtype, int BH, int share, int d_k, int d_v,

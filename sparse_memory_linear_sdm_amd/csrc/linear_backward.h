@@ -55,7 +55,8 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
   // what dg is summed from, for this chunk and the one before it
   struct Paths {
     float row[kTT][C], col[kTT][C];    // sums of W by tiles
-    float e[kKT][C], f[kKT][C], x[kKT];  // by wavefronts; x: exp(L_C) <S, G>
+    float e[kKT][4][C], f[kKT][4][C];  // by wavefronts and their lanes' quarters
+    float x[kKT];                      // exp(L_C) <S, G>
   };
   __shared__ Paths paths[2];
 
@@ -133,20 +134,20 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
       }
 #pragma unroll
       for (int i = 0; i < kKT; ++i) {
-        behind += (double)p.e[i][lane];
-        before += (double)p.f[i][lane];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          behind += (double)p.e[i][r][lane];
+          before += (double)p.f[i][r][lane];
+        }
         x += (double)p.x[i];
       }
     }
-    const double f = before;
-#pragma unroll
-    for (int o = 1; o < C; o <<= 1) {
-      const double u = __shfl_down(behind, o), v = __shfl_up(before, o);
-      if (lane + o < C) behind += u;
-      if (lane >= o) before += v;
-    }
+    const double f = before, e = behind;
+    double all, rest;
+    before = prefix_sum<C>(before, rest);
+    behind = prefix_sum<C>(behind, all);
     // a step that forgets everything has no path across it: exactly 0
-    const float dg = g <= -128.0f ? 0.0f : (float)(behind + (before - f) + x);
+    const float dg = g <= -128.0f ? 0.0f : (float)((all - behind + e) + (before - f) + x);
     __builtin_amdgcn_raw_buffer_store_b32(
         __float_as_uint(dg), buffer(A.dg + row + (int64_t)c * C, (uint32_t)rows_of(c) * 4),
         lane * 4, 0, 0);
@@ -249,12 +250,13 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
         for (int j = 0; j < 8; ++j) x += s[j] * G[j];
         Frag part[X::kParts];
         X::split(s, part);
+        Frag o[kTT];
 #pragma unroll
-        for (int i = 0; i < kTT; ++i) {
-          const Frag o = X::template rows<DV>(so, i * 16, vb * 32);
+        for (int i = 0; i < kTT; ++i) o[i] = X::template rows<DV>(so, i * 16, vb * 32);
 #pragma unroll
-          for (int p = 0; p < X::kParts; ++p) a[i] = X::mma(part[p], o, a[i]);
-        }
+        for (int p = 0; p < X::kParts; ++p)
+#pragma unroll
+          for (int i = 0; i < kTT; ++i) a[i] = X::mma(part[p], o[i], a[i]);
       }
       load_state(c - 1);
       x = wave_sum_f32(x);
@@ -268,10 +270,8 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
           const int t = i * 16 + col;
           a[i] *= d.into[t];
           const f32x4 q = X::load4(sq + X::template at<DK>(t, k0 + g4));
-          float e = (q[0] * a[i][0] + q[1] * a[i][1]) + (q[2] * a[i][2] + q[3] * a[i][3]);
-          e += __uint_as_float(lane_xor(__float_as_uint(e), 16));
-          e += __uint_as_float(lane_xor(__float_as_uint(e), 32));
-          if (lane < 16) path.e[w][t] = e;
+          path.e[w][lane >> 4][t] =
+              (q[0] * a[i][0] + q[1] * a[i][1]) + (q[2] * a[i][2] + q[3] * a[i][3]);
 #pragma unroll
           for (int b = 0; b <= i / 2; ++b)
             a[i] = X::mma(kc[b], X::template rows<C>(sdp, i * 16, b * 32), a[i]);
@@ -285,12 +285,13 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
       for (int vb = 0; vb < DV / 32; ++vb) {
         Frag part[X::kParts];
         X::split(Tile<float>::pack(Gv[2 * vb], Gv[2 * vb + 1]), part);
+        Frag v[kTT];
 #pragma unroll
-        for (int i = 0; i < kTT; ++i) {
-          const Frag v = X::template rows<DV>(sv, i * 16, vb * 32);
+        for (int i = 0; i < kTT; ++i) v[i] = X::template rows<DV>(sv, i * 16, vb * 32);
 #pragma unroll
-          for (int p = 0; p < X::kParts; ++p) a[i] = X::mma(part[p], v, a[i]);
-        }
+        for (int p = 0; p < X::kParts; ++p)
+#pragma unroll
+          for (int i = 0; i < kTT; ++i) a[i] = X::mma(part[p], v[i], a[i]);
       }
       Frag qc[C / 32];
 #pragma unroll
@@ -300,10 +301,8 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
         const int t = i * 16 + col;
         a[i] *= d.onto[t];
         const f32x4 k = X::load4(sk + X::template at<DK>(t, k0 + g4));
-        float f = (k[0] * a[i][0] + k[1] * a[i][1]) + (k[2] * a[i][2] + k[3] * a[i][3]);
-        f += __uint_as_float(lane_xor(__float_as_uint(f), 16));
-        f += __uint_as_float(lane_xor(__float_as_uint(f), 32));
-        if (lane < 16) path.f[w][t] = f;
+        path.f[w][lane >> 4][t] =
+            (k[0] * a[i][0] + k[1] * a[i][1]) + (k[2] * a[i][2] + k[3] * a[i][3]);
 #pragma unroll
         for (int b = i / 2; b < C / 32; ++b)
           a[i] = X::mma(qc[b], X::template cols<C>(sdp, b * 32, i * 16), a[i]);

@@ -88,7 +88,10 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
 
   BlockK bq, bk;
   BlockV bv;
-  auto chunk_of = [&](int i) { return kReverse ? c_end - 1 - i : c_first + i; };
+  // The state alone is one weighted sum over the segment's steps, by decays to its
+  // end (from its start, in reverse); chunks are taken from there.
+  constexpr bool kBack = MODE == 1;
+  auto chunk_of = [&](int i) { return kBack ? c_end - 1 - i : c_first + i; };
   // steps of the i-th chunk, 0 behind the last one
   auto rows_of = [&](int i) {
     const int64_t left = A.T - (int64_t)chunk_of(i) * C;
@@ -108,7 +111,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
   };
   double total = 0.0;
   load(0);
-  if (w == 0) total = scan_decays<C>(log2_decay(g_of(0)), sd[0]);
+  if (w == NW - 1) total = scan_decays<C>(log2_decay(g_of(0)), sd[0]);
   float step_g = g_of(1);
 #pragma unroll
   for (int kt = 0; kt < kKT; ++kt) arrive(S[kt]);
@@ -119,7 +122,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
     if (kOut) bq.store(sq);
     bk.store(sk);
     bv.store(sv);
-    if (w == 0 && lane < C) sg[lane] = step_g;
+    if (w == NW - 1 && lane < C) sg[lane] = step_g;
     __syncthreads();
     load(i + 1);
     step_g = g_of(i + 2);
@@ -143,7 +146,9 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
       }
       __syncthreads();
     }
-    if (w == 0) total += scan_decays<C>(lane < C ? log2_decay(sg[lane]) : 0.0, sd[(i + 1) & 1]);
+    if (w == NW - 1)
+      total += scan_decays<C>(lane < C ? log2_decay(sg[lane]) : 0.0, sd[(i + 1) & 1],
+                              kOut ? 0.0 : total, kOut ? 0.0 : total);
     if (mine) {
       if (kTape) {
         store_state(A.tape + ((int64_t)bh * A.nchunk + c) * DK * DV);
@@ -223,7 +228,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
 #pragma unroll
       for (int kt = 0; kt < kKT; ++kt) {
 #pragma unroll
-        for (int ct = 0; ct < kCT; ++ct) S[kt][ct] *= whole;
+        for (int ct = 0; ct < kCT; ++ct)
+          if (kOut) S[kt][ct] *= whole;
 #pragma unroll
         for (int sb = 0; sb < C / 32; ++sb) {
           const Frag k = X::template cols<DK>(sk, sb * 32, kt * 16);
@@ -247,7 +253,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
   float* to = nullptr;
   if (!kOut) {
     to = A.seg_state + ((int64_t)bh * A.nseg + seg) * DK * DV;
-    if (threadIdx.x == 0) A.seg_log[(int64_t)bh * A.nseg + seg] = total;
+    if (threadIdx.x == NT - 1) A.seg_log[(int64_t)bh * A.nseg + seg] = total;
   } else if (seg == A.nseg - 1) {
     to = A.S + (int64_t)bh * DK * DV;
   }

@@ -241,28 +241,39 @@ __device__ __forceinline__ double lane_value(double x, int lane) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// By one whole wavefront, step `lane`'s x (0 behind the last step and in lanes
-// at or past C): fills d and returns the chunk's sum.
+// Sum of the lanes up to this one (of C lanes, by the whole wavefront); sum: of
+// all C.  Lanes at or past C hold 0.
 template <int C>
-__device__ __forceinline__ double scan_decays(double x, Decays<C>& d) {
-  const int l = lane_id();
+__device__ __forceinline__ double prefix_sum(double x, double& sum) {
   x += row_shr<1>(x);
   x += row_shr<2>(x);
   x += row_shr<4>(x);
   x += row_shr<8>(x);
-  double below = 0.0, sum = lane_value(x, 15);
+  double below = 0.0;
+  sum = lane_value(x, 15);
 #pragma unroll
   for (int r = 1; r < C / 16; ++r) {
-    if (l >> 4 == r) below = sum;
+    if (lane_id() >> 4 == r) below = sum;
     sum += lane_value(x, r * 16 + 15);
   }
-  x += below;
+  return x + below;
+}
+
+// By one whole wavefront, step `lane`'s x (0 behind the last step and in lanes
+// at or past C): fills d and returns the chunk's sum.  onto and into reach
+// further by the logarithms `behind` and `before` the chunk.
+template <int C>
+__device__ __forceinline__ double scan_decays(double x, Decays<C>& d, double before = 0.0,
+                                              double behind = 0.0) {
+  const int l = lane_id();
+  double sum;
+  x = prefix_sum<C>(x, sum);
   if (l < C) {
     const float hi = (float)x;
     d.hi[l] = hi;
     d.lo[l] = (float)(x - (double)hi);
-    d.into[l] = pow2(hi);
-    d.onto[l] = pow2((float)(sum - x));
+    d.into[l] = pow2((float)(before + x));
+    d.onto[l] = pow2((float)(behind + (sum - x)));
     if (l == 0) d.whole = pow2((float)sum);
   }
   return sum;
