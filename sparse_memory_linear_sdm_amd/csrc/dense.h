@@ -39,7 +39,7 @@ struct LinearArgs {
   int seg_chunks;
 };
 
-int linear_segments(int dtype, int64_t BH, int64_t T, int d_k, int d_v, bool backward);
+int linear_segments(int dtype, int64_t BH, int64_t T, bool backward);
 size_t linear_scan_workspace_bytes(int dtype, int64_t BH, int d_k, int d_v, int64_t T);
 size_t linear_backward_workspace_bytes(int dtype, int64_t BH, int share, int d_k, int d_v,
                                        int64_t T);

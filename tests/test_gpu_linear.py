@@ -106,6 +106,18 @@ def test_scan_in_segments(T, dtype):
     check_forward(a, *run_scan(a))
 
 
+@pytest.mark.parametrize("dtype,H,T", [(F32, 64, 300), (BF16, 64, 600), (F32, 40, 430), (F32, 128, 2080),
+                                      (BF16, 128, 4100)])
+def test_segments_of_several_chunks(dtype, H, T):
+    a = make(1, H, H // 4, T, 32, 32, dtype, seed=T, grads=T < 1000)
+    if T < 1000:
+        out, S, _, grads, G = run_train(a)
+        check_reverse(a, grads, G)
+    else:
+        out, S = run_scan(a)
+    check_forward(a, out, S)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("g", [0.0, -0.0, -1e-6, -100.0, -127.9, -math.inf, -3e38])
 def test_scan_of_one_decay(g, dtype):
