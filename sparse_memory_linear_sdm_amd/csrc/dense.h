@@ -39,6 +39,12 @@ struct LinearArgs {
   int seg_chunks;
 };
 
+// Up to this many segments, each adds up the states of those before it (behind
+// it, in reverse) by itself; more are joined by a kernel of their own, since
+// their states would be read too often (16 segments: 123 MB for 16 memories of
+// 128 x 128).
+constexpr int kOwnSegments = 8;
+
 int linear_segments(int dtype, int64_t BH, int64_t T, bool backward);
 size_t linear_scan_workspace_bytes(int dtype, int64_t BH, int d_k, int d_v, int64_t T);
 size_t linear_backward_workspace_bytes(int dtype, int64_t BH, int share, int d_k, int d_v,

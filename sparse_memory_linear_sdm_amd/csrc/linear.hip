@@ -112,7 +112,7 @@ hipError_t launch_segments_by(const LinearArgs& a, int elems, bool reverse, hipS
 }
 
 hipError_t launch_segments(const LinearArgs& a, int elems, bool reverse, hipStream_t stream) {
-  if (a.nseg <= 8) return launch_segments_by<4, 2>(a, elems, reverse, stream);
+  if (a.nseg <= kOwnSegments) return hipSuccess;
   if (a.nseg <= 32) return launch_segments_by<8, 4>(a, elems, reverse, stream);
   return launch_segments_by<32, 16>(a, elems, reverse, stream);  // 512 at most
 }

@@ -78,19 +78,28 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
 
   f32x4 Gk[kKT];  // rows of k, columns v0 .. v0 + 15
   f32x4 Gv[kVT];  // rows of v, columns k0 .. k0 + 15
-  const float* from = A.nseg > 1 ? A.seg_state + ((int64_t)bh * A.nseg + seg) * DK * DV
-                                 : A.S + (int64_t)bh * DK * DV;
+  auto add_state = [&](const float* from, float decay) {  // G = decay G + from
+    const __amdgpu_buffer_rsrc_t b = buffer(from, DK * DV * 4);
+    if (has_v) {
 #pragma unroll
-  for (int kt = 0; kt < kKT; ++kt)
+      for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      Gk[kt][i] = has_v ? from[(kt * 16 + g4 + i) * DV + v0 + col] : 0.0f;
+        for (int i = 0; i < 4; ++i)
+          Gk[kt][i] = Gk[kt][i] * decay +
+                      buffer_float(b, (g4 * DV + v0 + col) * 4, (kt * 16 + i) * DV * 4);
+    }
+    if (has_k) {
 #pragma unroll
-  for (int vt = 0; vt < kVT; ++vt) {
-    Gv[vt] = f32x4{0, 0, 0, 0};
-    if (has_k) Gv[vt] = *reinterpret_cast<const f32x4*>(from + (k0 + col) * DV + vt * 16 + g4);
-  }
-
+      for (int vt = 0; vt < kVT; ++vt)
+        Gv[vt] = Gv[vt] * decay +
+                 __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                               b, ((k0 + col) * DV + g4 + vt * 16) * 4, 0, 0));
+    }
+  };
+#pragma unroll
+  for (int kt = 0; kt < kKT; ++kt) Gk[kt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int vt = 0; vt < kVT; ++vt) Gv[vt] = f32x4{0, 0, 0, 0};
   BlockK bq, bk;
   BlockV bv, bo;
   // steps of chunk c, 0 before the first one
@@ -157,6 +166,18 @@ __global__ __launch_bounds__((BackwardShape<T, DK, DV>::kThreads)) void linear_b
   float g_now = g_of(c_end - 1), g_next = g_of(c_end - 2), g_last = 0.0f;
   load(c_end - 1);
   if (has_k) load_state(c_end - 1);
+  {
+    const float* states = A.seg_state + (int64_t)bh * A.nseg * DK * DV;
+    if (A.nseg == 1) {
+      add_state(A.S + (int64_t)bh * DK * DV, 0.0f);
+    } else if (A.nseg > kOwnSegments) {
+      add_state(states + (int64_t)seg * DK * DV, 0.0f);
+    } else {
+      add_state(states, 0.0f);  // the call's gradient
+      for (int i = A.nseg - 1; i > seg; --i)
+        add_state(states + (int64_t)i * DK * DV, pow2((float)A.seg_log[(int64_t)bh * A.nseg + i]));
+    }
+  }
   if (w == NW - 1) scan_decays<C>(log2_decay(g_now), sd[(c_end - 1) & 1]);
   arrive(Gk);
   arrive(Gv);

@@ -52,7 +52,14 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
   const int c_first = seg * A.seg_chunks;
   const int c_end = c_first + A.seg_chunks < A.nchunk ? c_first + A.seg_chunks : A.nchunk;
   const int n = c_end - c_first;
-  if (!kOut && (kReverse ? seg == 0 : seg == A.nseg - 1)) return;  // no segment follows it
+  if (!kOut && (kReverse ? seg == 0 : seg == A.nseg - 1)) {
+    // no segment follows it: the call's state takes its place, since the scan
+    // overwrites that while other segments may not have read it
+    const f32x4* own = reinterpret_cast<const f32x4*>(A.S + (int64_t)bh * DK * DV);
+    f32x4* copy = reinterpret_cast<f32x4*>(A.seg_state + ((int64_t)bh * A.nseg + seg) * DK * DV);
+    for (int i = threadIdx.x; i < DK * DV / 4; i += NT) copy[i] = own[i];
+    return;
+  }
   const int64_t key_row = (int64_t)(bh / A.share) * A.T, row = (int64_t)bh * A.T;
   const T* gq = kOut ? (const T*)A.q + key_row * DK : nullptr;
   const T* gk = (kReverse ? (const T*)A.q : (const T*)A.k) + key_row * DK;
@@ -62,17 +69,21 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
   const int v0 = w * kCT * 16;  // this wavefront holds columns v0 .. v0 + 16 kCT - 1
   const bool mine = v0 < DV;
   f32x4 S[kKT][kCT];
-  const float* from = nullptr;
-  if (kOut) from = A.nseg > 1 ? A.seg_state + ((int64_t)bh * A.nseg + seg) * DK * DV
-                              : A.S + (int64_t)bh * DK * DV;
+  auto add_state = [&](const float* from, float decay) {  // S = decay S + from
+    const __amdgpu_buffer_rsrc_t b = buffer(from, DK * DV * 4);
+#pragma unroll
+    for (int kt = 0; kt < kKT; ++kt)
+#pragma unroll
+      for (int ct = 0; ct < kCT; ++ct)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          S[kt][ct][i] = S[kt][ct][i] * decay + buffer_float(b, (g4 * DV + v0 + col) * 4 + ct * 64,
+                                                             (kt * 16 + i) * DV * 4);
+  };
 #pragma unroll
   for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
-    for (int ct = 0; ct < kCT; ++ct)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        S[kt][ct][i] = kOut && mine ? from[(kt * 16 + g4 + i) * DV + v0 + ct * 16 + col] : 0.0f;
-
+    for (int ct = 0; ct < kCT; ++ct) S[kt][ct] = f32x4{0, 0, 0, 0};
   auto store_state = [&](float* to) {
     const __amdgpu_buffer_rsrc_t b = buffer(to, DK * DV * 4);
     const int at = (g4 * DV + v0 + col) * 4;
@@ -111,6 +122,18 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
   };
   double total = 0.0;
   load(0);
+  if (kOut && mine) {
+    const float* states = A.seg_state + (int64_t)bh * A.nseg * DK * DV;
+    if (A.nseg == 1) {
+      add_state(A.S + (int64_t)bh * DK * DV, 0.0f);
+    } else if (A.nseg > kOwnSegments) {
+      add_state(states + (int64_t)seg * DK * DV, 0.0f);
+    } else {
+      add_state(states + (int64_t)(A.nseg - 1) * DK * DV, 0.0f);  // the call's state
+      for (int i = 0; i < seg; ++i)
+        add_state(states + (int64_t)i * DK * DV, pow2((float)A.seg_log[(int64_t)bh * A.nseg + i]));
+    }
+  }
   if (w == NW - 1) total = scan_decays<C>(log2_decay(g_of(0)), sd[0]);
   float step_g = g_of(1);
 #pragma unroll

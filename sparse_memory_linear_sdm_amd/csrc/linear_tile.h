@@ -154,6 +154,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t
   return __builtin_amdgcn_make_buffer_rsrc((void*)u, 0, uniform_u32(bytes), kBufWord3);
 }
 
+__device__ __forceinline__ float buffer_float(__amdgpu_buffer_rsrc_t b, int lane_byte, int byte) {
+  const uint32_t u = __builtin_amdgcn_raw_buffer_load_b32(b, lane_byte, byte, 0);
+  return __uint_as_float(u);
+}
+
 // One [kChunk, D] block of a [T, D] array: 16-byte pieces through registers
 // into an LDS matrix, zeros behind the last step.
 template <class T, int D, int THREADS>
