@@ -229,7 +229,7 @@ int linear_segments(int dtype, int64_t BH, int64_t T, bool backward) {
   const int64_t chunks = (T + linear_chunk(dtype) - 1) / linear_chunk(dtype);
   if (chunks < (backward ? 4 : 8)) return 1;
   int64_t n = 256 / BH;
-  if (!backward && 512 / BH > n && chunks >= 16 * (512 / BH)) n = 512 / BH;
+  if (!backward && BH <= 32 && chunks >= 16 * (512 / BH)) n = 512 / BH;
   if (n > chunks) n = chunks;
   return n < 1 ? 1 : (int)n;
 }
