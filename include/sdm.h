@@ -439,7 +439,8 @@ int sdm_touch_prepare(int B, int H, int64_t N, int64_t T, int W, int R, const in
  * outputs of its chunk of steps (below), earlier ones too, and the later ones.
  * d_k, d_v in {32, 64, 128}; B*H <= 2^20, T < 2^31.  S, q, k, v, out, tape and
  * their gradients 16-byte aligned.  A sequence may be split over consecutive
- * calls (equal up to the order of the fp32 sums). */
+ * calls (equal up to the order of the fp32 sums).  Calls that overlap in time
+ * need workspaces of their own. */
 
 /* Bytes of workspace for sdm_linear_scan (0 where none is needed, for many
  * memories or few steps, and for sizes that are not supported): the states of
