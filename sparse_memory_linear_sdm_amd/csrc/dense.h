@@ -58,9 +58,8 @@ hipError_t launch_linear_step(float* S, int dtype, int BH, int share, int d_k, i
                               void* out, hipStream_t stream);
 
 // The chunked kernels by type (linear_bf16.hip, linear_f32.hip; the reverse
-// pass in linear_backward_*.hip).  mode: 0 the scan, 1 the state after each
-// segment alone, 2 the same for the state's gradient, segments and steps in
-// reverse.
+// pass in linear_backward_*.hip).  mode: 0 the scan, 1 what each segment adds to
+// the state, 2 the same for the state's gradient, segments and steps in reverse.
 hipError_t launch_linear_bf16(const LinearArgs& a, int d_k, int d_v, int mode, hipStream_t stream);
 hipError_t launch_linear_f32(const LinearArgs& a, int d_k, int d_v, int mode, hipStream_t stream);
 hipError_t launch_linear_backward_bf16(const LinearArgs& a, int d_k, int d_v, hipStream_t stream);

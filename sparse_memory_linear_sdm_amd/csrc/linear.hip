@@ -13,8 +13,9 @@ constexpr int kThreads = 256;
 // segments before it (behind it, in reverse).  seg_state[m][i] holds what
 // segment i adds; afterwards what it starts from.  A thread takes four values
 // of kPer consecutive segments; kGroups threads share a memory's segments, and
-// carry the state over each other's by sums and decays in LDS.  (One thread
-// through 128 segments of 4 memories took 45 us.)
+// carry the state over each other's by sums and decays in LDS.  Bound by memory:
+// 32 segments of 16 memories of 128 x 128 (67 MB) 11 us.  (One thread through 128
+// segments of 4 memories took 45 us.)
 template <int kGroups, int kPer>
 __global__ __launch_bounds__(kThreads) void linear_segments_kernel(float* seg_state,
                                                                    const double* seg_log,
@@ -43,19 +44,17 @@ __global__ __launch_bounds__(kThreads) void linear_segments_kernel(float* seg_st
       decay[j] = lin::pow2((float)lg[i]);
     }
   }
-  if (kGroups > 1) {
-    f32x4 sum = own[0];
-    float d = decay[0];
+  f32x4 sum = own[0];
+  float d = decay[0];
 #pragma unroll
-    for (int j = 1; j < kPer; ++j) {
-      sum = sum * decay[j] + own[j];
-      d *= decay[j];
-    }
-    sums[group][lane] = sum;
-    decays[group][lane] = d;
-    __syncthreads();
-    for (int i = 0; i < group; ++i) run = run * decays[i][lane] + sums[i][lane];
+  for (int j = 1; j < kPer; ++j) {
+    sum = sum * decay[j] + own[j];
+    d *= decay[j];
   }
+  sums[group][lane] = sum;
+  decays[group][lane] = d;
+  __syncthreads();
+  for (int i = 0; i < group; ++i) run = run * decays[i][lane] + sums[i][lane];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = reverse ? nseg - 1 - (i0 + j) : i0 + j;
@@ -65,7 +64,8 @@ __global__ __launch_bounds__(kThreads) void linear_segments_kernel(float* seg_st
 }
 
 // Gradients of shared keys: the sum over the heads that share them, in their
-// order, rounded once.  blockIdx.y: dq, dk.
+// order, rounded once (one pass over the parts, bound by memory).  blockIdx.y:
+// dq, dk.
 template <class T>
 __global__ __launch_bounds__(kThreads) void linear_share_kernel(LinearArgs A, int64_t total,
                                                                 int64_t per_head) {
@@ -132,8 +132,10 @@ void set_segments(LinearArgs& a, int dtype, bool backward) {
 }
 
 // ---- one token of every memory: S = exp(g) S + k v^T, out = S^T q.  Bound by
-// the state, read and written once.  A workgroup takes all rows of CT columns;
-// its loads are in flight together.
+// the state, read and written once: 1024 memories of 128 x 128 (134 MB) 20.5 us,
+// 6.6 TB/s; one of 4 memories 2.4.  A workgroup takes all rows of CT columns, its
+// loads in flight together: 64 of them (2048 memories of 64 x 64 11.3 us, by 32
+// columns 12.7; 64 of 128 x 128 3.6 us, 3.4 by 32 columns and 4.1 by 128).
 template <class T, int DK, int DV, int CT>
 __global__ __launch_bounds__(kThreads) void linear_step_kernel(float* S, const T* q, const T* k,
                                                                const T* v, const float* g, T* out,
@@ -143,7 +145,7 @@ __global__ __launch_bounds__(kThreads) void linear_step_kernel(float* S, const T
   constexpr int kN = DK / kRows;
   static_assert(DK % kRows == 0, "whole passes");
   __shared__ float sq[DK], sk[DK];
-  __shared__ f32x4 sum[kThreads / kWave][kLanes < kWave ? kLanes : kWave];
+  __shared__ f32x4 sum[kThreads / kWave][kLanes];
   const int tid = threadIdx.x;
   const int64_t m = blockIdx.x / (DV / CT);
   const int c0 = (int)(blockIdx.x % (DV / CT)) * CT + (tid % kLanes) * 4;
@@ -191,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void linear_step_kernel(float* S, const T
 template <class T, int DK, int DV>
 hipError_t launch_step(float* S, int BH, int share, const void* q, const void* k, const void* v,
                        const float* g, void* out, hipStream_t stream) {
-  constexpr int CT = 32;
+  constexpr int CT = DV < 64 ? DV : 64;
   hipLaunchKernelGGL((linear_step_kernel<T, DK, DV, CT>), dim3((unsigned)BH * (DV / CT)),
                      dim3(kThreads), 0, stream, S, (const T*)q, (const T*)k, (const T*)v, g,
                      (T*)out, share);
@@ -218,7 +220,7 @@ hipError_t launch_step_type(float* S, int BH, int share, int d_k, int d_v, const
 }  // namespace
 
 // Segments of a memory's steps: as many as give every compute unit a workgroup
-// (a chunk is a chain of dependent phases, about 4 us forward and 10 back at
+// (a chunk is a chain of dependent phases, 5 us forward and 17 back at
 // 128 x 128, so chunks go side by side), two where a segment keeps 16 chunks even
 // so (16 memories x 32768 steps, bf16: 204 us with two, 213 with one; 64 x 2048
 // with a tape the other way, 105 and 80).  Segments cost a kernel for their

@@ -7,11 +7,24 @@
 // (all exponents <= 0 for decays), as products of 16 x 16 tiles.
 //
 // One workgroup walks the chunks of a memory, or of one segment of it; the
-// state stays in its accumulators, each wavefront holding all d_k rows of 16
-// columns.  Where memories are few, the steps are cut
+// state stays in its accumulators, each of four wavefronts holding all d_k rows
+// of a quarter of the columns (at least 16).  Where memories are few, the steps are cut
 // into segments: a first kernel (modes 1 and 2) finds what each segment adds to
 // the state, another adds these up (linear.hip), then each segment starts from
 // its own state.
+//
+// Bound by the phases of a chunk, which follow each other (LDS stores, q.k,
+// outputs, state): 128 x 128 bf16, 64 memories x 4096 steps in four segments,
+// 33 us for the segments' states and 80 for the scan (5 us a chunk of 64 steps),
+// where its bytes need 40; 512 memories x 2048 steps 267 us (4.3 TB/s), since two
+// workgroups a compute unit then fill each other's waits, held back by power
+// (1.45 GHz) and LDS.  fp32, 64 x 128, 32 memories x 2047 steps in eight segments:
+// 17 + 40 us; a chunk of 32 steps there is eight times the matrix instructions of
+// bf16's, at twice the cycles each.  Four wavefronts of 32 columns read each
+// fragment of q and k for two products: eight wavefronts of 16 read LDS twice as
+// often (64 x 4096 141 us; 117).  One set of LDS blocks, the next chunk's loads in
+// registers: two sets need one barrier less but leave room for one workgroup a
+// compute unit (125 us).
 #pragma once
 #include "dense.h"
 #include "linear_tile.h"
@@ -236,7 +249,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
           for (int sb = 0; sb < C / 32; ++sb)
             V[ct][sb] = X::template cols<DV>(sv, sb * 32, v0 + ct * 16);
       }
-      // the state: v (dout in reverse) scaled by its decay, in parts
+      // the state: v (dout in reverse) scaled by its decay, in parts (k is bf16
+      // already: the products then hold fp32's precision)
       const float* scale = kReverse ? d.into : d.onto;
       Frag part[kCT][C / 32][X::kParts];
 #pragma unroll

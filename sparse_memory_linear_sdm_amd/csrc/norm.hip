@@ -10,7 +10,13 @@
 //
 // Bound by memory: every value is read once into registers (8 at a time per
 // lane), sums are fp32.  Rows of up to 512 values take a power of two of lanes,
-// 256-thread workgroups several rows; longer rows take a workgroup each.
+// 256-thread workgroups several rows; longer rows take a workgroup each.  Measured:
+//   8192 rows of 8192 bf16 with gate, residual and next norm (671 MB) 126-133 us,
+//     5.1-5.3 TB/s (a copy of that mix, three arrays read and one written, 5.6);
+//   262144 rows of 128, fp32 to gated bf16 by heads (268 MB) 49 us, 5.4 TB/s;
+//   their reverse pass, 131072 rows of bf16 (168 MB) and the sum of dw, 42 + 4 us;
+//   4099 rows of 5128, fp32 from bf16 gradients (294 MB), 66 + 5 us, 4.4 TB/s;
+//   one row of 8192 3 us.
 #include "dense.h"
 #include "device_common.h"
 
