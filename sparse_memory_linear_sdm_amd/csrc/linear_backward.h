@@ -13,8 +13,10 @@
 //        + sum over i >= t of e_i      e_i = exp(L_i) q_i . S do_i
 //        + sum over j < t of f_j       f_j = exp(L_C - L_j) k_j . G v_j
 //        + exp(L_C) <S, G>
-// Nothing here cancels over more than one chunk; the first line is taken as
-// the difference of the rows' and columns' sums of W behind t.
+// No difference of sums is taken: a step that forgets almost everything has a
+// small gradient beside large W on either side.  In 16 x 16 tiles of W, the
+// first line is a part of t's own tile, rows from t on of the tiles left of it,
+// columns before t of those below it, and whole tiles left and below.
 //
 // One workgroup walks a memory's chunks (or a segment's).  G is kept twice in
 // its accumulators, by rows of k and by rows of v: it enters products along
@@ -60,7 +62,9 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
   __shared__ Decays<C> sd[2];
   // what dg is summed from, for this chunk and the one before it
   struct Paths {
-    float row[kTT][C], col[kTT][C];    // sums of W by tiles
+    // sums of W over the rows and columns of its tiles; row[tile of t][t]: the sum
+    // of W_ij, i >= t > j, inside t's tile
+    float row[kTT][C], col[kTT][C];
     float e[kKT][4][C], f[kKT][4][C];  // by wavefronts and their lanes' quarters
     float x[kKT];                      // exp(L_C) <S, G>
   };
@@ -139,30 +143,46 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
   // dg of chunk c, by one wavefront
   auto gate = [&](int c, float g) {
     const Paths& p = paths[c & 1];
-    double behind = 0.0, before = 0.0, x = 0.0;
+    const int tile = lane >> 4;
+    double e = 0.0, f = 0.0, x = 0.0, down = 0.0, left[kTT - 1] = {};
     if (lane < C) {
-      const int tile = lane >> 4;
+      x = (double)p.row[tile][lane];
 #pragma unroll
       for (int i = 0; i < kTT; ++i) {
-        if (i <= tile) behind += (double)p.row[i][lane];
-        if (i >= tile) behind -= (double)p.col[i][lane];
+        if (i < kTT - 1 && i < tile) left[i] = (double)p.row[i][lane];
+        if (i > tile) down += (double)p.col[i][lane];
       }
 #pragma unroll
       for (int i = 0; i < kKT; ++i) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          behind += (double)p.e[i][r][lane];
-          before += (double)p.f[i][r][lane];
+          e += (double)p.e[i][r][lane];
+          f += (double)p.f[i][r][lane];
         }
         x += (double)p.x[i];
       }
     }
-    const double f = before, e = behind;
-    double all, rest;
-    before = prefix_sum<C>(before, rest);
-    behind = prefix_sum<C>(behind, all);
+    // steps from this one on, and before it, in its tile; then whole tiles
+    e = row_sums_up(e);
+    f = row_sums_down(f);
+#pragma unroll
+    for (int i = 0; i < kTT - 1; ++i) {
+      left[i] = row_sums_up(left[i]);
+      x += left[i];
+    }
+    x += e + row_shr<1>(f) + row_shr<1>(row_sums_down(down));
+#pragma unroll
+    for (int r = 0; r < kTT; ++r) {
+      const double e_tile = lane_value(e, r * 16), f_tile = lane_value(f, r * 16 + 15);
+      x += r > tile ? e_tile : r < tile ? f_tile : 0.0;
+#pragma unroll
+      for (int i = 0; i + 1 < r; ++i) {
+        const double w_tile = lane_value(left[i], r * 16);
+        x += i < tile && tile < r ? w_tile : 0.0;
+      }
+    }
     // a step that forgets everything has no path across it: exactly 0
-    const float dg = g <= -128.0f ? 0.0f : (float)((all - behind + e) + (before - f) + x);
+    const float dg = g <= -128.0f ? 0.0f : (float)x;
     __builtin_amdgcn_raw_buffer_store_b32(
         __float_as_uint(dg), buffer(A.dg + row + (int64_t)c * C, (uint32_t)rows_of(c) * 4),
         lane * 4, 0, 0);
@@ -222,22 +242,19 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
       const f32x4 raw = dp;
       p = decayed(p, decay, t, s);
       dp = decayed(dp, decay, t, s);
-      float by_row = 0.0f, by_col[4];
+      // W's sums over rows t .. 15 of the tile by columns, over its columns by rows;
+      // in the diagonal tile the former over the columns before t
+      float by_row = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        by_col[j] = s + j < t ? p[j] * raw[j] : 0.0f;
-        by_row += by_col[j];
+        const float W = s + j < t ? p[j] * raw[j] : 0.0f;
+        const float down = row_sums_up(W);
+        if (col == 0) path.col[tt][s + j] = down;
+        by_row += tt != st ? W : s + j < t ? down : 0.0f;
       }
       by_row += __uint_as_float(lane_xor(__float_as_uint(by_row), 16));
       by_row += __uint_as_float(lane_xor(__float_as_uint(by_row), 32));
       if (lane < 16) path.row[st][t] = by_row;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1)
-          by_col[j] += __uint_as_float(lane_xor(__float_as_uint(by_col[j]), o));
-        if (col == 0) path.col[tt][s + j] = by_col[j];
-      }
       X::store4(sp + X::template at<C>(t, s), p);
       X::store4(sdp + X::template at<C>(t, s), dp);
     }

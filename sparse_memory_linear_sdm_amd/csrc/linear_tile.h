@@ -229,14 +229,46 @@ __device__ __forceinline__ double log2_decay(float g) {
   return (double)(g < -128.0f ? -128.0f : g) * 1.4426950408889634;
 }
 
-// x of lane l - N in its row of 16, 0.0 where there is none
-template <int N>
-__device__ __forceinline__ double row_shr(double x) {
+// x of the lane that the control kDpp names (in a row of 16), 0 where there is none
+template <int kDpp>
+__device__ __forceinline__ float row_move(float x) {
+  return __uint_as_float(
+      (uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(x), kDpp, 0xF, 0xF, true));
+}
+template <int kDpp>
+__device__ __forceinline__ double row_move(double x) {
   const uint64_t b = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, 0x110 + N, 0xF, 0xF, true);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, kDpp, 0xF, 0xF, true);
   const uint32_t hi =
-      (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), 0x110 + N, 0xF, 0xF, true);
+      (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), kDpp, 0xF, 0xF, true);
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// of lane l - N, of lane l + N
+template <int N, class F>
+__device__ __forceinline__ F row_shr(F x) {
+  return row_move<0x110 + N>(x);
+}
+template <int N, class F>
+__device__ __forceinline__ F row_shl(F x) {
+  return row_move<0x100 + N>(x);
+}
+
+// Sums over a row of 16 lanes, of the lanes up to this one and from this one on.
+template <class F>
+__device__ __forceinline__ F row_sums_down(F x) {
+  x += row_shr<1>(x);
+  x += row_shr<2>(x);
+  x += row_shr<4>(x);
+  x += row_shr<8>(x);
+  return x;
+}
+template <class F>
+__device__ __forceinline__ F row_sums_up(F x) {
+  x += row_shl<1>(x);
+  x += row_shl<2>(x);
+  x += row_shl<4>(x);
+  x += row_shl<8>(x);
+  return x;
 }
 
 __device__ __forceinline__ double lane_value(double x, int lane) {
@@ -250,10 +282,7 @@ __device__ __forceinline__ double lane_value(double x, int lane) {
 // all C.  Lanes at or past C hold 0.
 template <int C>
 __device__ __forceinline__ double prefix_sum(double x, double& sum) {
-  x += row_shr<1>(x);
-  x += row_shr<2>(x);
-  x += row_shr<4>(x);
-  x += row_shr<8>(x);
+  x = row_sums_down(x);
   double below = 0.0;
   sum = lane_value(x, 15);
 #pragma unroll

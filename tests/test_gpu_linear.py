@@ -229,6 +229,21 @@ def test_backward_in_segments(T, Hk, dtype):
     check_reverse(a, grads, G)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dk,dv,T,Hk", [(32, 32, 64, 2), (64, 128, 150, 1), (128, 64, 97, 2),
+                                        (32, 64, 700, 2)])
+def test_gradients_of_gates_that_forget_much(dk, dv, T, Hk, dtype):
+    """dg of a step is the sum of the paths across it, in fp32's precision of
+    those: steps that leave 1e-2 to 1e-26 of the state have paths that are as
+    much smaller than the ones beside them."""
+    a = make(1, 2, Hk, T, dk, dv, dtype, seed=T, grads=True)
+    r = torch.Generator().manual_seed(T + dk)
+    hit = torch.rand(a["g"].shape, generator=r) < 0.1
+    a["g"] = torch.where(hit, -5 - 55 * torch.rand(a["g"].shape, generator=r), a["g"])
+    _, _, _, grads, G = run_train(a)
+    check_reverse(a, grads, G)
+
+
 def test_no_steps():
     import sparse_memory_linear_sdm_amd as sdm
 
