@@ -45,7 +45,7 @@ struct LinearArgs {
 // 128 x 128).
 constexpr int kOwnSegments = 8;
 
-int linear_segments(int dtype, int64_t BH, int64_t T, bool backward);
+int linear_segments(int dtype, int64_t BH, int64_t T, int elems, bool backward);
 size_t linear_scan_workspace_bytes(int dtype, int64_t BH, int d_k, int d_v, int64_t T);
 size_t linear_backward_workspace_bytes(int dtype, int64_t BH, int share, int d_k, int d_v,
                                        int64_t T);

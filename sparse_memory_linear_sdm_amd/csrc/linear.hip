@@ -123,10 +123,10 @@ hipError_t launch_chunks(const LinearArgs& a, int dtype, int d_k, int d_v, int m
                     : launch_linear_f32(a, d_k, d_v, mode, stream);
 }
 
-void set_segments(LinearArgs& a, int dtype, bool backward) {
+void set_segments(LinearArgs& a, int dtype, int elems, bool backward) {
   const int chunk = linear_chunk(dtype);
   a.nchunk = (int)((a.T + chunk - 1) / chunk);
-  a.nseg = linear_segments(dtype, a.BH, a.T, backward);
+  a.nseg = linear_segments(dtype, a.BH, a.T, elems, backward);
   a.seg_chunks = (a.nchunk + a.nseg - 1) / a.nseg;
   a.nseg = (a.nchunk + a.seg_chunks - 1) / a.seg_chunks;
 }
@@ -220,16 +220,20 @@ hipError_t launch_step_type(float* S, int BH, int share, int d_k, int d_v, const
 }  // namespace
 
 // Segments of a memory's steps: as many as give every compute unit a workgroup
-// (a chunk is a chain of dependent phases, 5 us forward and 17 back at
-// 128 x 128, so chunks go side by side), two where a segment keeps 16 chunks even
+// (a chunk is a chain of dependent phases, 5 us forward and 17 back at 128 x 128
+// in bf16, so chunks go side by side), two where a segment keeps 16 chunks even
 // so (16 memories x 32768 steps, bf16: 204 us with two, 213 with one; 64 x 2048
 // with a tape the other way, 105 and 80).  Segments cost a kernel for their
-// states and one that joins these, about 8 us: no gain below 8 chunks forward
-// (32 us in one piece at 8, 18 in eight) and 4 back (4 memories x 500 steps of
-// 128 x 128: 104 us by twos, 47 by ones).
-int linear_segments(int dtype, int64_t BH, int64_t T, bool backward) {
+// states and sums of these, 5 to 10 us.  Back they gain from 4 chunks on (4
+// memories x 500 steps of 128 x 128: 104 us by twos, 47 by ones).  Forward, where a
+// chunk takes 2 to 6 us, from 5 on at 128 x 128 if there are four or more (64
+// memories x 300 steps, bf16, 23.5 us in one piece and 22.3 in four; 8 x 201, fp32,
+// 44 and 22; two pieces of 128 x 300 28.7 for 25.0), else from 8 on (8 x 201 of 64 x
+// 32, fp32, seven chunks, 16.0 us in one piece and in seven, and a launch more; 24 x
+// 300 of 32 x 64, bf16, 11.3 and 15.5).
+int linear_segments(int dtype, int64_t BH, int64_t T, int elems, bool backward) {
   const int64_t chunks = (T + linear_chunk(dtype) - 1) / linear_chunk(dtype);
-  if (chunks < (backward ? 4 : 8)) return 1;
+  if (chunks < (backward ? 4 : elems == 128 * 128 && BH <= 64 ? 5 : 8)) return 1;
   int64_t n = 256 / BH;
   if (!backward && BH <= 32 && chunks >= 16 * (512 / BH)) n = 512 / BH;
   if (n > chunks) n = chunks;
@@ -237,18 +241,18 @@ int linear_segments(int dtype, int64_t BH, int64_t T, bool backward) {
 }
 
 size_t linear_scan_workspace_bytes(int dtype, int64_t BH, int d_k, int d_v, int64_t T) {
-  return segment_bytes(BH, linear_segments(dtype, BH, T, false), d_k * d_v);
+  return segment_bytes(BH, linear_segments(dtype, BH, T, d_k * d_v, false), d_k * d_v);
 }
 
 size_t linear_backward_workspace_bytes(int dtype, int64_t BH, int share, int d_k, int d_v,
                                        int64_t T) {
   const size_t part = share > 1 ? 2 * align256((size_t)BH * T * d_k * 4) : 0;
-  return part + segment_bytes(BH, linear_segments(dtype, BH, T, true), d_k * d_v);
+  return part + segment_bytes(BH, linear_segments(dtype, BH, T, d_k * d_v, true), d_k * d_v);
 }
 
 hipError_t launch_linear_scan(LinearArgs a, int dtype, int d_k, int d_v, void* ws,
                               hipStream_t stream) {
-  set_segments(a, dtype, false);
+  set_segments(a, dtype, d_k * d_v, false);
   char* p = (char*)ws;
   place_segments(a, d_k * d_v, p);
   hipError_t rc;
@@ -261,7 +265,7 @@ hipError_t launch_linear_scan(LinearArgs a, int dtype, int d_k, int d_v, void* w
 
 hipError_t launch_linear_backward(LinearArgs a, int dtype, int d_k, int d_v, void* ws,
                                   hipStream_t stream) {
-  set_segments(a, dtype, true);
+  set_segments(a, dtype, d_k * d_v, true);
   char* p = (char*)ws;
   place_segments(a, d_k * d_v, p);
   const int64_t per_head = a.T * d_k;

@@ -118,6 +118,24 @@ def test_segments_of_several_chunks(dtype, H, T):
     check_forward(a, out, S)
 
 
+@pytest.mark.parametrize("dtype,H,T", [(F32, 2, 128), (F32, 2, 129), (F32, 5, 200), (BF16, 2, 256),
+                                      (BF16, 2, 257), (BF16, 5, 400), (BF16, 65, 300)])
+def test_wide_heads_of_few_chunks(dtype, H, T):
+    """Heads of 128 x 128 are cut from five chunks on, for up to 64 memories."""
+    import sparse_memory_linear_sdm_amd as sdm
+
+    chunk = 64 if dtype == BF16 else 32
+    need = sdm.lib().sdm_linear_scan_workspace_size(int(dtype == BF16), 1, H, 128, 128, T)
+    assert (need > 0) == (H <= 64 and T > 4 * chunk)
+    a = make(1, H, H, T, 128, 128, dtype, seed=T, resets=True, grads=H < 65)
+    if H < 65:
+        out, S, _, grads, G = run_train(a)
+        check_reverse(a, grads, G)
+    else:
+        out, S = run_scan(a)
+    check_forward(a, out, S)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("g", [0.0, -0.0, -1e-6, -100.0, -127.9, -math.inf, -3e38])
 def test_scan_of_one_decay(g, dtype):
