@@ -14,7 +14,7 @@
 //   8192 rows of 8192 bf16 with gate, residual and next norm (671 MB) 126-133 us,
 //     5.1-5.3 TB/s (a copy of that mix, three arrays read and one written, 5.6);
 //   262144 rows of 128, fp32 to gated bf16 by heads (268 MB) 49 us, 5.4 TB/s;
-//   their reverse pass, 131072 rows of bf16 (168 MB) and the sum of dw, 42 + 4 us;
+//   their reverse pass, 131072 rows of bf16 (168 MB) and the sum of dw, 36 + 4 us;
 //   4099 rows of 5128, fp32 from bf16 gradients (294 MB), 66 + 5 us, 4.4 TB/s;
 //   one row of 8192 3 us.
 #include "dense.h"
@@ -34,17 +34,35 @@ constexpr int kFewRows = 512;
 // Eight values of a row, read or written once: past the caches (8192 rows of
 // 8192 with gate, residual and next norm 135 us with ordinary accesses, 126).
 template <class T>
-__device__ __forceinline__ f32x8 load8(const void* p, int64_t at) {
-  if constexpr (sizeof(T) == 2) {
-    return __builtin_convertvector(
-        __builtin_bit_cast(bf16x8, __builtin_nontemporal_load(
-                                       reinterpret_cast<const u32x4*>((const uint16_t*)p + at))),
-        f32x8);
-  } else {
-    const f32x4* f = reinterpret_cast<const f32x4*>((const float*)p + at);
-    return __builtin_shufflevector(__builtin_nontemporal_load(f), __builtin_nontemporal_load(f + 1),
-                                   0, 1, 2, 3, 4, 5, 6, 7);
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  u32x4 r;
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    r = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>((const uint16_t*)p + at));
   }
+  __device__ __forceinline__ f32x8 values() const {
+    return __builtin_convertvector(__builtin_bit_cast(bf16x8, r), f32x8);
+  }
+};
+template <>
+struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const f32x4* f = reinterpret_cast<const f32x4*>((const float*)p + at);
+    a = __builtin_nontemporal_load(f);
+    b = __builtin_nontemporal_load(f + 1);
+  }
+  __device__ __forceinline__ f32x8 values() const {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
+template <class T>
+__device__ __forceinline__ f32x8 load8(const void* p, int64_t at) {
+  Raw8<T> r;
+  r.load(p, at);
+  return r.values();
 }
 
 template <class T>
@@ -173,10 +191,16 @@ __global__ __launch_bounds__(WIDE ? kWideMax : kNarrow) void norm_kernel(NormArg
 }
 
 // Each workgroup takes rows blockIdx, blockIdx + blocks, ... and leaves its
-// sum of dw in part[blockIdx].
+// sum of dw in part[blockIdx].  A lane's vector of a bf16 row (eight registers
+// with its gate and gradients) is loaded as it stands, all arrays in one go (131072
+// gated rows of 128 39 us, 42 as separate values), and for long rows before the
+// sums of the row in front of it (20000 of 2048 64 us, 71).  fp32 rows and two
+// vectors a thread have the registers for that only at half the workgroups (4099
+// rows of 5128 76-84 us for 72; 32768 fp32 rows of 256 109 for 103).
 template <class Ty, class To, int V, bool WIDE>
 __global__ __launch_bounds__(WIDE ? kWideMax / 2 : kNarrow) void norm_backward_kernel(NormArgs A,
                                                                                    int lanes) {
+  constexpr bool kRaw = V == 1 && sizeof(Ty) + sizeof(To) == 4, kAhead = kRaw && WIDE;
   __shared__ float lds[2][kWideMax / kWave];
   __shared__ __align__(16) float sum[WIDE ? 8 : kNarrow * 8];
   const int nvec = A.d / 8;
@@ -189,21 +213,41 @@ __global__ __launch_bounds__(WIDE ? kWideMax / 2 : kNarrow) void norm_backward_k
     dw[i] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
     w[i] = j < nvec ? weights8(A.w, j * 8) : dw[i];
   }
+  Raw8<Ty> next_y, next_skip;  // kRaw
+  Raw8<To> next_dout, next_z;
+  const auto fetch = [&](int64_t r) {
+    if (r >= A.rows || me >= nvec) return;
+    const int64_t yr = y_row(A, (uint32_t)r) * A.d, at = r * A.d;
+    next_y.load(A.y, yr + me * 8);
+    next_dout.load(A.dout, at + me * 8);
+    if (A.z) next_z.load(A.z, at + me * 8);
+    if (A.skip) next_skip.load(A.skip, yr + me * 8);
+  };
+  if (kAhead) fetch(blockIdx.x);
   for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < A.rows;
        r0 += (int64_t)gridDim.x * per_block) {
     const int64_t r = r0 + group;
     const bool here = r < A.rows;
     const int64_t yr = here ? y_row(A, (uint32_t)r) * A.d : 0, at = r * A.d;
     f32x8 y[V], D[V], z[V];
+    if (kRaw && !kAhead) fetch(r);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int j = me + i * L;
       const bool in = here && j < nvec;
       const f32x8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
-      y[i] = in ? load8<Ty>(A.y, yr + j * 8) : zero;
-      D[i] = in ? load8<To>(A.dout, at + j * 8) * A.scale : zero;
-      z[i] = in && A.z ? load8<To>(A.z, at + j * 8) : zero;
+      if (kRaw) {
+        y[i] = in ? next_y.values() : zero;
+        D[i] = in ? next_dout.values() * A.scale : zero;
+        z[i] = in && A.z ? next_z.values() : zero;
+      } else {
+        y[i] = in ? load8<Ty>(A.y, yr + j * 8) : zero;
+        D[i] = in ? load8<To>(A.dout, at + j * 8) * A.scale : zero;
+        z[i] = in && A.z ? load8<To>(A.z, at + j * 8) : zero;
+      }
     }
+    const Raw8<Ty> skip = next_skip;
+    if (kAhead) fetch(r0 + gridDim.x);
     float sums[2] = {0.0f, 0.0f};  // y^2, D a w y
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -236,7 +280,7 @@ __global__ __launch_bounds__(WIDE ? kWideMax / 2 : kNarrow) void norm_backward_k
       }
       dw[i] += a * n;
       f32x8 dy = (a * w[i] - n * mean) * rs;
-      if (A.skip) dy += load8<Ty>(A.skip, yr + j * 8);
+      if (A.skip) dy += kRaw ? skip.values() : load8<Ty>(A.skip, yr + j * 8);
       store8<Ty>(A.dy, yr + j * 8, dy);
     }
   }
