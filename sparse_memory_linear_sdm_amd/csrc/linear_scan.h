@@ -97,17 +97,14 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
   for (int kt = 0; kt < kKT; ++kt)
 #pragma unroll
     for (int ct = 0; ct < kCT; ++ct) S[kt][ct] = f32x4{0, 0, 0, 0};
-  auto store_state = [&](float* to) {
-    const __amdgpu_buffer_rsrc_t b = buffer(to, DK * DV * 4);
-    const int at = (g4 * DV + v0 + col) * 4;
+  auto store_rows = [&](__amdgpu_buffer_rsrc_t to, int kt) {
 #pragma unroll
-    for (int kt = 0; kt < kKT; ++kt)
+    for (int ct = 0; ct < kCT; ++ct)
 #pragma unroll
-      for (int ct = 0; ct < kCT; ++ct)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[kt][ct][i]), b, at + ct * 64,
-                                                (kt * 16 + i) * DV * 4, 0);
+      for (int i = 0; i < 4; ++i)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[kt][ct][i]), to,
+                                              (g4 * DV + v0 + col) * 4 + ct * 64,
+                                              (kt * 16 + i) * DV * 4, 0);
   };
 
   BlockK bq, bk;
@@ -186,9 +183,6 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
       total += scan_decays<C>(lane < C ? log2_decay(sg[lane]) : 0.0, sd[(i + 1) & 1],
                               kOut ? 0.0 : total, kOut ? 0.0 : total);
     if (mine) {
-      if (kTape) {
-        store_state(A.tape + ((int64_t)bh * A.nchunk + c) * DK * DV);
-      }
       Frag V[kCT][C / 32];
       schedule_end();
       if (kOut) {
@@ -261,9 +255,15 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
         for (int ct = 0; ct < kCT; ++ct) X::split(X::widen(V[ct][sb]) * a, part[ct][sb]);
       }
       const float whole = d.whole;
+      // the tape: rows of the state go out between the products, just before they
+      // change (64 memories x 2048 steps 57 us, 60 all at once in front of them)
+      const __amdgpu_buffer_rsrc_t tape =
+          buffer(kTape ? A.tape + ((int64_t)bh * A.nchunk + c) * DK * DV : nullptr,
+                 kTape ? DK * DV * 4 : 0);
       schedule_end();
 #pragma unroll
       for (int kt = 0; kt < kKT; ++kt) {
+        if (kTape) store_rows(tape, kt);
 #pragma unroll
         for (int ct = 0; ct < kCT; ++ct)
           if (kOut) S[kt][ct] *= whole;
@@ -276,11 +276,13 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
             for (int ct = 0; ct < kCT; ++ct) S[kt][ct] = X::mma(k, part[ct][sb][j], S[kt][ct]);
         }
       }
+      if (kTape) schedule_writes<kCT * 4>();
       schedule_reads<2 * X::kColReads>();  // two fragments ahead
 #pragma unroll
       for (int i = 0; i < kKT * (C / 32); ++i) {
         schedule_reads<X::kColReads>();
         schedule_products<X::kParts * kCT * X::kProducts>();
+        if (kTape) schedule_writes<kCT * 4 / (C / 32)>();
       }
       schedule_end();
     }
@@ -294,7 +296,11 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
   } else if (seg == A.nseg - 1) {
     to = A.S + (int64_t)bh * DK * DV;
   }
-  if (to && mine) store_state(to);
+  if (to && mine) {
+    const __amdgpu_buffer_rsrc_t state = buffer(to, DK * DV * 4);
+#pragma unroll
+    for (int kt = 0; kt < kKT; ++kt) store_rows(state, kt);
+  }
 }
 
 template <class T, int DK, int DV>

@@ -198,7 +198,7 @@ __device__ __forceinline__ void arrive(f32x4 (&x)[N]) {
 }
 
 // Orders of the instructions of a stretch of code between two calls of
-// schedule_end(): the next n LDS reads, the next n matrix instructions.
+// schedule_end(): the next n LDS reads, matrix instructions, writes to memory.
 template <int N>
 __device__ __forceinline__ void schedule_reads() {
   __builtin_amdgcn_sched_group_barrier(0x100, N, 0);
@@ -206,6 +206,10 @@ __device__ __forceinline__ void schedule_reads() {
 template <int N>
 __device__ __forceinline__ void schedule_products() {
   __builtin_amdgcn_sched_group_barrier(0x008, N, 0);
+}
+template <int N>
+__device__ __forceinline__ void schedule_writes() {
+  __builtin_amdgcn_sched_group_barrier(0x040, N, 0);
 }
 __device__ __forceinline__ void schedule_end() { __builtin_amdgcn_sched_barrier(0); }
 
