@@ -35,6 +35,12 @@
 namespace sdm {
 namespace lin {
 
+// The sum over lanes l, l ^ 16, l ^ 32 and l ^ 48.
+__device__ __forceinline__ float over_quarters(float x) {
+  x += __uint_as_float(lane_xor(__float_as_uint(x), 16));
+  return x + __uint_as_float(lane_xor(__float_as_uint(x), 32));
+}
+
 template <int DK, int DV>
 struct BackwardShape {
   static constexpr int kWaves = DK == 128 || DV == 128 ? 8 : 4;
@@ -65,7 +71,7 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
     // sums of W over the rows and columns of its tiles; row[tile of t][t]: the sum
     // of W_ij, i >= t > j, inside t's tile
     float row[kTT][C], col[kTT][C];
-    float e[kKT][4][C], f[kKT][4][C];  // by wavefronts and their lanes' quarters
+    float e[kKT][C], f[kKT][C];        // by wavefronts
     float x[kKT];                      // exp(L_C) <S, G>
   };
   __shared__ Paths paths[2];
@@ -154,11 +160,8 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
       }
 #pragma unroll
       for (int i = 0; i < kKT; ++i) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          e += (double)p.e[i][r][lane];
-          f += (double)p.f[i][r][lane];
-        }
+        e += (double)p.e[i][lane];
+        f += (double)p.f[i][lane];
         x += (double)p.x[i];
       }
     }
@@ -230,6 +233,7 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
       const int tt = u < 4 ? u >> 1 : 2 + ((u - 4) >> 2), st = u < 4 ? u & 1 : (u - 4) & 3;
       f32x4 p = {0, 0, 0, 0}, dp = {0, 0, 0, 0};
       const int t = tt * 16 + col, s = st * 16 + g4;
+      schedule_end();
 #pragma unroll
       for (int kb = 0; kb < DK / 32; ++kb)
         p = X::mma(X::template rows<DK>(sk, st * 16, kb * 32),
@@ -238,6 +242,13 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
       for (int vb = 0; vb < DV / 32; ++vb)
         dp = X::mma(X::template rows<DV>(sv, st * 16, vb * 32),
                     X::template rows<DV>(so, tt * 16, vb * 32), dp);
+      schedule_reads<6 * X::kRowReads>();  // three pairs ahead
+#pragma unroll
+      for (int i = 0; i < (DK + DV) / 32; ++i) {
+        schedule_reads<2 * X::kRowReads>();
+        schedule_products<X::kProducts>();
+      }
+      schedule_end();
       const f32x4 decay = decay_between<C>(d, t, s);
       const f32x4 raw = dp;
       p = decayed(p, decay, t, s);
@@ -252,8 +263,7 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
         if (col == 0) path.col[tt][s + j] = down;
         by_row += tt != st ? W : s + j < t ? down : 0.0f;
       }
-      by_row += __uint_as_float(lane_xor(__float_as_uint(by_row), 16));
-      by_row += __uint_as_float(lane_xor(__float_as_uint(by_row), 32));
+      by_row = over_quarters(by_row);
       if (lane < 16) path.row[st][t] = by_row;
       X::store4(sp + X::template at<C>(t, s), p);
       X::store4(sdp + X::template at<C>(t, s), dp);
@@ -314,8 +324,9 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
           const int t = i * 16 + col;
           a[i] *= d.into[t];
           const f32x4 q = X::load4(sq + X::template at<DK>(t, k0 + g4));
-          path.e[w][lane >> 4][t] =
-              (q[0] * a[i][0] + q[1] * a[i][1]) + (q[2] * a[i][2] + q[3] * a[i][3]);
+          const float e = over_quarters((q[0] * a[i][0] + q[1] * a[i][1]) +
+                                        (q[2] * a[i][2] + q[3] * a[i][3]));
+          if (lane < 16) path.e[w][t] = e;
 #pragma unroll
           for (int b = 0; b <= i / 2; ++b)
             a[i] = X::mma(kc[b], X::template rows<C>(sdp, i * 16, b * 32), a[i]);
@@ -345,8 +356,9 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
         const int t = i * 16 + col;
         a[i] *= d.onto[t];
         const f32x4 k = X::load4(sk + X::template at<DK>(t, k0 + g4));
-        path.f[w][lane >> 4][t] =
-            (k[0] * a[i][0] + k[1] * a[i][1]) + (k[2] * a[i][2] + k[3] * a[i][3]);
+        const float f = over_quarters((k[0] * a[i][0] + k[1] * a[i][1]) +
+                                      (k[2] * a[i][2] + k[3] * a[i][3]));
+        if (lane < 16) path.f[w][t] = f;
 #pragma unroll
         for (int b = i / 2; b < C / 32; ++b)
           a[i] = X::mma(qc[b], X::template cols<C>(sdp, b * 32, i * 16), a[i]);
