@@ -26,8 +26,8 @@
 //
 // Bound by a chunk's phases like the scan, with three times its products: 64
 // memories x 2048 steps of 128 x 128 bf16 in four segments, 26 us for the
-// segments' states and 135-147 for this pass (17 us a chunk of 64 steps; counted:
-// LDS active 45% of the time, vector arithmetic 39%, matrix cores 23%, memory 2.6 TB/s).
+// segments' states and 131-143 for this pass (17 us a chunk of 64 steps; counted:
+// LDS active 46% of the time, vector arithmetic 41%, matrix cores 23%, memory 2.7 TB/s).
 #pragma once
 #include "dense.h"
 #include "linear_tile.h"
