@@ -433,8 +433,8 @@ int sdm_touch_prepare(int B, int H, int64_t N, int64_t T, int W, int R, const in
  *         -128 (-infinity too) the step forgets the state: sequences can follow
  *         one another in one row of T steps.
  * Sums are fp32, states and decays hold fp32's precision for both types.  bf16:
- * out is rounded once to bf16, from the state and the products q_t . k_s rounded
- * to bf16 as operands of the matrix cores.  Every q, k, v and S has to be finite
+ * out is rounded once to bf16; the state and the products q_t . k_s enter it with
+ * 16 bits (two bf16 operands of the matrix cores, within 2^-16 of their value).  Every q, k, v and S has to be finite
  * and products to stay in fp32's range, as the decay over any stretch of steps
  * has to where g is positive (below 2^-126 it is 0): a NaN or an infinity spreads over all
  * outputs of its chunk of steps (below), earlier ones too, and the later ones.

@@ -47,14 +47,14 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
   constexpr int NW = kScanWaves, NT = kScanThreads;
   typedef Block<T, DK, NT> BlockK;
   typedef Block<T, DV, NT> BlockV;
-  constexpr int kSizeP = C * X::template kLd<C>;
+  typedef Pairs<T> P;
   constexpr int kTT = C / 16;                       // tiles of steps
   constexpr int kKT = DK / 16;                      // tiles of state rows
   constexpr int kCT = DV > 16 * NW ? DV / (16 * NW) : 1;  // tiles of state columns per wavefront
   __shared__ __align__(16) T sq[kOut ? BlockK::kSize : 8];
   __shared__ __align__(16) T sk[BlockK::kSize];
   __shared__ __align__(16) T sv[BlockV::kSize];
-  __shared__ __align__(16) T sp[kOut ? kSizeP : 8];  // q_t . k_s and its decay, rows t
+  __shared__ __align__(16) T sp[kOut ? P::kParts * P::kSize : 8];  // (q_t . k_s) decay(s, t)
   __shared__ Decays<C> sd[2];
   __shared__ float sg[C];  // g of the next chunk
 
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
           p = X::mma(X::template rows<DK>(sk, st * 16, kb * 32),
                      X::template rows<DK>(sq, tt * 16, kb * 32), p);
         p = decayed(p, decay_between<C>(d, t, s), t, s);
-        X::store4(sp + X::template at<C>(t, s), p);
+        P::store4(sp, t, s, p);
       }
       __syncthreads();
     }
@@ -187,8 +187,8 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
       schedule_end();
       if (kOut) {
         // outputs transposed: rows are columns of v, so a lane holds four
-        // consecutive values of step t.  The state enters rounded to T (bf16: the
-        // outputs are rounded to it as well), the accumulators keep fp32.
+        // consecutive values of step t.  The state enters in kOutParts operands, the
+        // accumulators keep fp32.
         const __amdgpu_buffer_rsrc_t out = buffer((T*)A.out + (row + (int64_t)c * C) * DV,
                                                   (uint32_t)(rows_of(i) * DV * (int)sizeof(T)));
         f32x4 o[kTT][kCT];
@@ -203,9 +203,12 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
           for (int tt = 0; tt < kTT; ++tt) q[tt] = X::template rows<DK>(sq, tt * 16, kb * 32);
 #pragma unroll
           for (int ct = 0; ct < kCT; ++ct) {
-            const Frag s = X::pack(S[2 * kb][ct], S[2 * kb + 1][ct]);
+            Frag s[X::kOutParts];
+            X::template split<X::kOutParts>(Tile<float>::pack(S[2 * kb][ct], S[2 * kb + 1][ct]), s);
 #pragma unroll
-            for (int tt = 0; tt < kTT; ++tt) o[tt][ct] = X::mma(s, q[tt], o[tt][ct]);
+            for (int j = 0; j < X::kOutParts; ++j)
+#pragma unroll
+              for (int tt = 0; tt < kTT; ++tt) o[tt][ct] = X::mma(s[j], q[tt], o[tt][ct]);
           }
         }
         // reads one block of products ahead
@@ -213,7 +216,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb) {
           schedule_reads<kTT * X::kRowReads>();
-          schedule_products<kTT * kCT * X::kProducts>();
+          schedule_products<kTT * kCT * X::kOutParts * X::kProducts>();
         }
         schedule_end();
 #pragma unroll
@@ -228,9 +231,12 @@ __global__ __launch_bounds__(kScanThreads, 2) void linear_kernel(LinearArgs A) {
           for (int ct = 0; ct < kCT; ++ct) o[tt][ct] *= into;
 #pragma unroll
           for (int sb = 0; sb <= tt / 2; ++sb) {
-            const Frag p = X::template rows<C>(sp, tt * 16, sb * 32);
 #pragma unroll
-            for (int ct = 0; ct < kCT; ++ct) o[tt][ct] = X::mma(V[ct][sb], p, o[tt][ct]);
+            for (int j = 0; j < P::kParts; ++j) {
+              const Frag p = P::rows(sp, j, tt * 16, sb * 32);
+#pragma unroll
+              for (int ct = 0; ct < kCT; ++ct) o[tt][ct] = X::mma(V[ct][sb], p, o[tt][ct]);
+            }
           }
 #pragma unroll
           for (int ct = 0; ct < kCT; ++ct)

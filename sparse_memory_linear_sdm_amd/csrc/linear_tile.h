@@ -41,6 +41,11 @@ struct Tile<uint16_t> {
   // Parts of a scaled operand whose product must keep fp32's precision: a bf16
   // part holds 8 of the 24 bits.
   static constexpr int kParts = 3;
+  // Parts of what fp32 holds (the state, products of steps) where a sum is rounded
+  // to bf16 behind the product: two are off by 2^-16 of it at most, beside the 2^-8
+  // of the rounding.  (One part, 2^-8 of every term, puts outputs 1.4 times as far
+  // from the exact ones as the rounding alone.)
+  static constexpr int kOutParts = 2;
   static constexpr int kRowReads = 1, kColReads = 2, kProducts = 1;  // instructions
   typedef bf16x8 Frag;
 
@@ -75,12 +80,22 @@ struct Tile<uint16_t> {
   static __device__ __forceinline__ f32x8 widen(Frag a) {
     return __builtin_convertvector(a, f32x8);
   }
-  // x as the sum of kParts operands, to within 2^-24 of it
+  // x as the sum of N operands, to within 2^-8N of it
+  template <int N = kParts>
   static __device__ __forceinline__ void split(f32x8 x, Frag* part) {
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
+    for (int p = 0; p < N; ++p) {
       part[p] = __builtin_convertvector(x, bf16x8);
       x = x - __builtin_convertvector(part[p], f32x8);
+    }
+  }
+  // x stored as the sum of kOutParts matrices, `size` values apart
+  static __device__ __forceinline__ void store4_parts(uint16_t* p, int size, f32x4 x) {
+#pragma unroll
+    for (int i = 0; i < kOutParts; ++i) {
+      const bf16x4 part = __builtin_convertvector(x, bf16x4);
+      *reinterpret_cast<bf16x4*>(p + i * size) = part;
+      x = x - __builtin_convertvector(part, f32x4);
     }
   }
   static __device__ __forceinline__ void store4(uint16_t* p, f32x4 x) {
@@ -104,7 +119,7 @@ struct Tile<float> {
   static __device__ __forceinline__ int at(int row, int col) {
     return row * kLd<D> + col;
   }
-  static constexpr int kParts = 1;
+  static constexpr int kParts = 1, kOutParts = 1;
   static constexpr int kRowReads = 2, kColReads = 8, kProducts = 8;
   typedef f32x8 Frag;
 
@@ -132,7 +147,13 @@ struct Tile<float> {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
   static __device__ __forceinline__ f32x8 widen(Frag a) { return a; }
-  static __device__ __forceinline__ void split(f32x8 x, Frag* part) { part[0] = x; }
+  template <int N = kParts>
+  static __device__ __forceinline__ void split(f32x8 x, Frag* part) {
+    part[0] = x;
+  }
+  static __device__ __forceinline__ void store4_parts(float* p, int, f32x4 x) {
+    *reinterpret_cast<f32x4*>(p) = x;
+  }
   static __device__ __forceinline__ void store4(float* p, f32x4 x) {
     *reinterpret_cast<f32x4*>(p) = x;
   }
@@ -141,6 +162,31 @@ struct Tile<float> {
   }
   static __device__ __forceinline__ f32x4 load4(const float* p) {
     return *reinterpret_cast<const f32x4*>(p);
+  }
+};
+
+// A matrix of pairs of a chunk's steps (t, s), s <= t, in LDS: rows t below 32
+// have columns for s below 32 only (with two parts of it the padded square of 64 x
+// 64 would leave reverse passes of 64 x 64 heads one workgroup a compute unit).
+template <class T>
+struct Pairs {
+  typedef Tile<T> X;
+  static constexpr int kUpper = 32 * X::template kLd<32>;
+  static constexpr int kSize = kUpper + (X::kChunk == 64 ? 32 * X::template kLd<64> : 0);
+  static constexpr int kParts = X::kOutParts;
+  static __device__ __forceinline__ void store4(T* m, int t, int s, f32x4 x) {  // four s
+    X::store4_parts(m + (t < 32 ? X::template at<32>(t, s) : kUpper + X::template at<64>(t - 32, s)),
+                    kSize, x);
+  }
+  // Step t0 + l % 16, inner values s0 .. s0 + 31.
+  static __device__ __forceinline__ typename X::Frag rows(const T* m, int part, int t0, int s0) {
+    m += part * kSize;
+    return t0 < 32 ? X::template rows<32>(m, t0, s0) : X::template rows<64>(m + kUpper, t0 - 32, s0);
+  }
+  // Step s0 + l % 16, inner values t0 .. t0 + 31 (t0 a multiple of 32).
+  static __device__ __forceinline__ typename X::Frag cols(const T* m, int part, int t0, int s0) {
+    m += part * kSize;
+    return t0 < 32 ? X::template cols<32>(m, 0, s0) : X::template cols<64>(m + kUpper, 0, s0);
   }
 };
 
