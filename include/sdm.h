@@ -434,10 +434,11 @@ int sdm_touch_prepare(int B, int H, int64_t N, int64_t T, int W, int R, const in
  *         one another in one row of T steps.
  * Sums are fp32, states and decays hold fp32's precision for both types.  bf16:
  * out is rounded once to bf16; the state and the products q_t . k_s enter it with
- * 16 bits (two bf16 operands of the matrix cores, within 2^-16 of their value).  Every q, k, v and S has to be finite
- * and products to stay in fp32's range, as the decay over any stretch of steps
- * has to where g is positive (below 2^-126 it is 0): a NaN or an infinity spreads over all
- * outputs of its chunk of steps (below), earlier ones too, and the later ones.
+ * 16 bits (two bf16 operands of the matrix cores, within 2^-16 of their value).
+ * Every q, k, v and S has to be finite and products to stay in fp32's range, as
+ * the decay over any stretch of steps has to where g is positive (below 2^-126 it
+ * is 0): a NaN or an infinity spreads over all outputs of its chunk of steps
+ * (below), earlier ones too, and the later ones.
  * d_k, d_v in {32, 64, 128}; B*H <= 2^20, T < 2^31.  S, q, k, v, out, tape and
  * their gradients 16-byte aligned.  A sequence may be split over consecutive
  * calls (equal up to the order of the fp32 sums).  Calls that overlap in time
@@ -478,7 +479,8 @@ size_t sdm_linear_backward_workspace_size(int dtype, int B, int H, int Hk, int d
  *   dq, dk [B, Hk, T, d_k] (summed over the heads that share them, in fp32),
  *          dv [B, H, T, d_v] out, of dtype;  dg [B, H, T] fp32 out, dL/dg (0 for
  *          steps that forget the state).
- * dg and G hold fp32's precision for both types.  Results are deterministic.
+ * dg and G hold fp32's precision for both types; in bf16 dq, dk and dv are rounded
+ * once, with operands of 16 bits as in the forward.  Results are deterministic.
  * B*H*T <= 2^26 - 4.  T = 0 is a valid no-op (G unchanged; every other array may
  * then be NULL).  workspace as for sdm_linear_scan. */
 int sdm_linear_backward(int dtype, int B, int H, int Hk, int d_k, int d_v, int64_t T,

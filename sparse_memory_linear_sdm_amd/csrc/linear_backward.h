@@ -56,15 +56,15 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
   constexpr int NW = BackwardShape<DK, DV>::kWaves, NT = NW * kWave;
   typedef Block<T, DK, NT> BlockK;
   typedef Block<T, DV, NT> BlockV;
-  constexpr int kSizeP = C * X::template kLd<C>;
+  typedef Pairs<T> P;
   constexpr int kTT = C / 16, kKT = DK / 16, kVT = DV / 16;
   static_assert(kKT <= NW && kVT <= NW, "one column tile a wavefront");
   __shared__ __align__(16) T sq[BlockK::kSize];
   __shared__ __align__(16) T sk[BlockK::kSize];
   __shared__ __align__(16) T sv[BlockV::kSize];
   __shared__ __align__(16) T so[BlockV::kSize];  // dout
-  __shared__ __align__(16) T sp[kSizeP];         // (q_t . k_s) D_ts, rows t
-  __shared__ __align__(16) T sdp[kSizeP];        // (do_t . v_s) D_ts, rows t
+  __shared__ __align__(16) T sp[P::kParts * P::kSize];   // (q_t . k_s) D_ts
+  __shared__ __align__(16) T sdp[P::kParts * P::kSize];  // (do_t . v_s) D_ts
   __shared__ Decays<C> sd[2];
   // what dg is summed from, for this chunk and the one before it
   struct Paths {
@@ -265,8 +265,8 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
       }
       by_row = over_quarters(by_row);
       if (lane < 16) path.row[st][t] = by_row;
-      X::store4(sp + X::template at<C>(t, s), p);
-      X::store4(sdp + X::template at<C>(t, s), dp);
+      P::store4(sp, t, s, p);
+      P::store4(sdp, t, s, dp);
     }
     if (w == NW - 1) scan_decays<C>(log2_decay(g_next), sd[(c - 1) & 1]);
     __syncthreads();
@@ -329,7 +329,9 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
           if (lane < 16) path.e[w][t] = e;
 #pragma unroll
           for (int b = 0; b <= i / 2; ++b)
-            a[i] = X::mma(kc[b], X::template rows<C>(sdp, i * 16, b * 32), a[i]);
+#pragma unroll
+            for (int j = 0; j < P::kParts; ++j)
+              a[i] = X::mma(kc[b], P::rows(sdp, j, i * 16, b * 32), a[i]);
         }
         store_rows(out_q);
       }
@@ -361,7 +363,9 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
         if (lane < 16) path.f[w][t] = f;
 #pragma unroll
         for (int b = i / 2; b < C / 32; ++b)
-          a[i] = X::mma(qc[b], X::template cols<C>(sdp, b * 32, i * 16), a[i]);
+#pragma unroll
+          for (int j = 0; j < P::kParts; ++j)
+            a[i] = X::mma(qc[b], P::cols(sdp, j, b * 32, i * 16), a[i]);
       }
       store_rows(out_k);
       Frag part[C / 32][X::kParts];
@@ -398,16 +402,20 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
       for (int i = 0; i < kTT; ++i) a[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int kb = 0; kb < DK / 32; ++kb) {
-        const Frag G = X::pack(Gk[2 * kb], Gk[2 * kb + 1]);
+        Frag G[X::kOutParts], k[kTT];
+        X::template split<X::kOutParts>(Tile<float>::pack(Gk[2 * kb], Gk[2 * kb + 1]), G);
 #pragma unroll
-        for (int i = 0; i < kTT; ++i)
-          a[i] = X::mma(G, X::template rows<DK>(sk, i * 16, kb * 32), a[i]);
+        for (int i = 0; i < kTT; ++i) k[i] = X::template rows<DK>(sk, i * 16, kb * 32);
+#pragma unroll
+        for (int j = 0; j < X::kOutParts; ++j)
+#pragma unroll
+          for (int i = 0; i < kTT; ++i) a[i] = X::mma(G[j], k[i], a[i]);
       }
       schedule_reads<2 * kTT * X::kRowReads>();
 #pragma unroll
       for (int kb = 0; kb < DK / 32; ++kb) {
         schedule_reads<kTT * X::kRowReads>();
-        schedule_products<kTT * X::kProducts>();
+        schedule_products<kTT * X::kOutParts * X::kProducts>();
       }
       schedule_end();
       Frag oc[C / 32];
@@ -418,7 +426,9 @@ __global__ __launch_bounds__((BackwardShape<DK, DV>::kThreads)) void linear_back
         a[i] *= d.onto[i * 16 + col];
 #pragma unroll
         for (int b = i / 2; b < C / 32; ++b)
-          a[i] = X::mma(oc[b], X::template cols<C>(sp, b * 32, i * 16), a[i]);
+#pragma unroll
+          for (int j = 0; j < P::kParts; ++j)
+            a[i] = X::mma(oc[b], P::cols(sp, j, b * 32, i * 16), a[i]);
         X::store4(out_v, (i * 16 + col) * DV + v0 + g4, a[i]);
       }
       Frag part[C / 32][X::kParts];
