@@ -430,8 +430,8 @@ int sdm_touch_prepare(int B, int H, int64_t N, int64_t T, int W, int R, const in
  *         keys of head h / (H / Hk).  Queries are taken as they are (a factor
  *         such as 1 / sqrt(d_k) is the caller's).
  *   g     [B, H, T] fp32 logarithms of the decays, normally <= 0.  At or below
- *         -128 (-infinity too) the step forgets the state: sequences can follow
- *         one another in one row of T steps.
+ *         -128 (-infinity too) the step forgets the state, whatever the decays
+ *         around it: sequences can follow one another in one row of T steps.
  * Sums are fp32, states and decays hold fp32's precision for both types.  bf16:
  * out is rounded once to bf16; the state and the products q_t . k_s enter it with
  * 16 bits (two bf16 operands of the matrix cores, within 2^-16 of their value).

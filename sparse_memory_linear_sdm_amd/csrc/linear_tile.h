@@ -273,10 +273,12 @@ struct alignas(16) Decays {
 // 2^x, 0 below 2^-126
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// log2 of one step's decay.  Below 2^-184 = exp(-128) it is 0 in fp32 with
-// any number of further steps; so is -infinity's, without infinities here.
+// log2 of one step's decay.  At or below exp(-128) the step forgets the state: -1024,
+// so that its sum with steps on both sides, whose own stretches stay below 2^128, is
+// far below 2^-149 and the decay across it exactly 0.  (The sums of a chunk's
+// 64 such steps keep 2^-33 beside 2^16.)
 __device__ __forceinline__ double log2_decay(float g) {
-  return (double)(g < -128.0f ? -128.0f : g) * 1.4426950408889634;
+  return g <= -128.0f ? -1024.0 : (double)g * 1.4426950408889634;
 }
 
 // x of the lane that the control kDpp names (in a row of 16), 0 where there is none
