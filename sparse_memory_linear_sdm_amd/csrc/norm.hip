@@ -95,9 +95,18 @@ __device__ __forceinline__ float sum8(f32x8 v) {
 }
 
 // 1 / (1 + exp(-z)), from the hardware's 2^x and 1/x (each within an ulp): a
-// row's gates cost more than its other arithmetic
+// row's gates cost more than its other arithmetic.  The exponent t = -z log2 e,
+// rounded, is off by up to 2^-24 of itself, which the power would multiply by z:
+// what t lacks, r, is put back as the factor 2^r = 1 + r ln 2.  Beyond the bounds
+// of z the result is 0 or 1 anyway, and r stays small.
 __device__ __forceinline__ float sigmoid(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896f));
+  constexpr float kL = -1.44269504088896f;       // -log2 e, and the rest of it
+  constexpr float kRest = (float)(-1.4426950408889634 - (double)kL);
+  z = __builtin_amdgcn_fmed3f(z, -104.0f, 88.0f);
+  const float t = z * kL;
+  const float r = __builtin_fmaf(z, kRest, __builtin_fmaf(z, kL, -t));
+  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(r, 0.693147181f, 1.0f);
+  return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 // Sums of N values over a row's lanes: `lanes` of them (a power of two up to 64)
@@ -230,6 +239,7 @@ __global__ __launch_bounds__(WIDE ? kWideMax / 2 : kNarrow) void norm_backward_k
     const bool here = r < A.rows;
     const int64_t yr = here ? y_row(A, (uint32_t)r) * A.d : 0, at = r * A.d;
     f32x8 y[V], D[V], z[V];
+    f32x8 gate;  // the sigmoids, where registers allow (V = 1)
     if (kRaw && !kAhead) fetch(r);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -254,7 +264,11 @@ __global__ __launch_bounds__(WIDE ? kWideMax / 2 : kNarrow) void norm_backward_k
       f32x8 a = D[i] * w[i];
       if (A.z) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] *= z[i][e] * sigmoid(z[i][e]);
+        for (int e = 0; e < 8; ++e) {
+          const float s = sigmoid(z[i][e]);
+          if (V == 1) gate[e] = s;
+          a[e] *= z[i][e] * s;
+        }
       }
       sums[0] += sum8(y[i] * y[i]);
       sums[1] += sum8(a * y[i]);
@@ -272,7 +286,7 @@ __global__ __launch_bounds__(WIDE ? kWideMax / 2 : kNarrow) void norm_backward_k
         f32x8 dz;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float s = sigmoid(z[i][e]);
+          const float s = V == 1 ? gate[e] : sigmoid(z[i][e]);
           dz[e] = D[i][e] * n[e] * w[i][e] * (s * (1.0f + z[i][e] * (1.0f - s)));
           a[e] *= z[i][e] * s;
         }
