@@ -452,7 +452,7 @@ size_t sdm_linear_scan_workspace_size(int dtype, int B, int H, int d_k, int d_v,
 /* T steps of every memory.
  *   tape  NULL, or [B, H, ceil(T/C), d_k, d_v] fp32 out, for
  *         sdm_linear_backward: the state before each chunk of C steps (C = 64
- *         for SDM_BF16, 32 for SDM_F32).
+ *         for SDM_BF16, 32 for SDM_F32).  With a tape B*H*T <= 2^26 - 4, as there.
  *   workspace  device buffer of at least sdm_linear_scan_workspace_size bytes,
  *         256-byte aligned (NULL if that is 0); its contents on entry do not
  *         matter.

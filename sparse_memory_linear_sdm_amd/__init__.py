@@ -853,7 +853,8 @@ def linear_scan(S, q, k, v, g, out=None, workspace=None, stream=None):
 
 def linear_scan_train(S, q, k, v, g, out=None, tape=None, workspace=None, stream=None):
     """linear_scan() that also keeps the state before each chunk of C steps (64
-    for bfloat16, 32 for float32): returns (out, tape [B,H,ceil(T/C),d_k,d_v])."""
+    for bfloat16, 32 for float32): returns (out, tape [B,H,ceil(T/C),d_k,d_v]).
+    B*H*T at most 2^26 - 4, as linear_backward takes."""
     return _linear_scan(S, q, k, v, g, out, tape, True, workspace, stream)
 
 

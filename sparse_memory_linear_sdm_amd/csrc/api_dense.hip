@@ -34,6 +34,13 @@ int check_linear_sizes(int dtype, int B, int H, int Hk, int d_k, int d_v, int64_
   return SDM_OK;
 }
 
+// What the reverse pass takes, so that no tape is made that it would refuse.
+int check_tape_steps(int B, int H, int64_t T) {
+  if ((int64_t)B * H * T > sdm::kMaxWaveUnits)
+    return fail(SDM_ERR_UNSUPPORTED, "B*H*T must be at most 2^26 - 4 per call with a tape");
+  return SDM_OK;
+}
+
 int check_linear_inputs(const void* q, const void* k, const void* v, const float* g) {
   int rc;
   if ((rc = check_array(q, 16, "q")) || (rc = check_array(k, 16, "k")) ||
@@ -89,6 +96,7 @@ int sdm_linear_scan(float* S, int dtype, int B, int H, int Hk, int d_k, int d_v,
                     float* tape, void* workspace, size_t workspace_bytes, void* stream) {
   int rc;
   if ((rc = check_linear_sizes(dtype, B, H, Hk, d_k, d_v, T))) return rc;
+  if (tape && (rc = check_tape_steps(B, H, T))) return rc;
   if ((rc = check_array(S, 16, "S"))) return rc;
   hipStream_t s = (hipStream_t)stream;
   if (T == 0) return finish("sdm_linear_scan", hipSuccess, s);  // the per-step arrays may be NULL
@@ -139,8 +147,7 @@ int sdm_linear_backward(int dtype, int B, int H, int Hk, int d_k, int d_v, int64
                         void* stream) {
   int rc;
   if ((rc = check_linear_sizes(dtype, B, H, Hk, d_k, d_v, T))) return rc;
-  if ((int64_t)B * H * T > sdm::kMaxWaveUnits)
-    return fail(SDM_ERR_UNSUPPORTED, "B*H*T must be at most 2^26 - 4 per call");
+  if ((rc = check_tape_steps(B, H, T))) return rc;
   if ((rc = check_array(G, 16, "G"))) return rc;
   hipStream_t s = (hipStream_t)stream;
   if (T == 0) return finish("sdm_linear_backward", hipSuccess, s);  // per-step arrays may be NULL
