@@ -144,7 +144,7 @@ __global__ __launch_bounds__(kThreads) void linear_step_kernel(float* S, const T
   constexpr int kRows = kThreads / kLanes;       // rows at a time
   constexpr int kN = DK / kRows;
   static_assert(DK % kRows == 0, "whole passes");
-  __shared__ float sq[DK], sk[DK];
+  __shared__ __align__(16) float sq[DK], sk[DK];
   __shared__ f32x4 sum[kThreads / kWave][kLanes];
   const int tid = threadIdx.x;
   const int64_t m = blockIdx.x / (DV / CT);
