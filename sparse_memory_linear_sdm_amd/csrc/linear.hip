@@ -221,19 +221,22 @@ hipError_t launch_step_type(float* S, int BH, int share, int d_k, int d_v, const
 
 // Segments of a memory's steps: as many as give every compute unit a workgroup
 // (a chunk is a chain of dependent phases, 5 us forward and 17 back at 128 x 128
-// in bf16, so chunks go side by side), two where a segment keeps 16 chunks even
-// so (16 memories x 32768 steps, bf16: 204 us with two, 213 with one; 64 x 2048
-// with a tape the other way, 105 and 80).  Segments cost a kernel for their
-// states and sums of these, 5 to 10 us.  Back they gain from 4 chunks on (4
-// memories x 500 steps of 128 x 128: 104 us by twos, 47 by ones).  Forward, where a
-// chunk takes 2 to 6 us, from 5 on at 128 x 128 if there are four or more (64
-// memories x 300 steps, bf16, 23.5 us in one piece and 22.3 in four; 8 x 201, fp32,
-// 44 and 22; two pieces of 128 x 300 28.7 for 25.0), else from 8 on (8 x 201 of 64 x
-// 32, fp32, seven chunks, 16.0 us in one piece and in seven, and a launch more; 24 x
-// 300 of 32 x 64, bf16, 11.3 and 15.5).
+// in bf16, so chunks go side by side), two where a segment of at most 32 memories
+// keeps 16 chunks even so (16 memories x 32768 steps, bf16: 225 us with two, 259
+// with one; 32 of 64 x 128 x 2047 steps, fp32, the other way, 56 and 52, and 64 x
+// 2048 with a tape 98 and 83).  Segments cost a kernel for their states and sums
+// of these, 5 to 10 us.  Back they gain from 4 chunks on (4 memories x 250 steps of
+// 128 x 128, bf16: 55 us in one piece, 32 cut; 64 x 256 58 and 40).  Forward a chunk
+// takes 1.3 to 6 us.  Four segments or more gain from 5 chunks on (64 memories, in
+// one piece and cut: 64 x 64 bf16 14.5 and 12.7 us, 64 x 128 19.6 and 17.3, 128 x 64
+// 19.7 and 16.7, 128 x 128 26.8 and 23.9, fp32 33.9 and 27.7; 24 of 64 x 128
+// 19.1 and 14.0), but by less than a launch takes on the host, 3.7 us, where heads
+// are below 64 x 64 (64 memories of 64 x 32 12.6 and 11.0; from 8 chunks on 18.7 and
+// 12.1).  Two segments (65 to 128 memories) gain from 8 on (128 of 64 x 128, 5
+// chunks, 20.6 and 23.4; 8 chunks 30.3 and 30.3; of 64 x 32 18.8 and 17.7).
 int linear_segments(int dtype, int64_t BH, int64_t T, int elems, bool backward) {
   const int64_t chunks = (T + linear_chunk(dtype) - 1) / linear_chunk(dtype);
-  if (chunks < (backward ? 4 : elems == 128 * 128 && BH <= 64 ? 5 : 8)) return 1;
+  if (chunks < (backward ? 4 : elems >= 64 * 64 && BH <= 64 ? 5 : 8)) return 1;
   int64_t n = 256 / BH;
   if (!backward && BH <= 32 && chunks >= 16 * (512 / BH)) n = 512 / BH;
   if (n > chunks) n = chunks;
