@@ -420,9 +420,11 @@ int sdm_state_init_backward(const float* G, int B, int H, int64_t N, int d_v,
 int sdm_touch_prepare(int B, int H, int64_t N, int64_t T, int W, int R, const int32_t* widx,
                       const int32_t* ridx, uint32_t* seen, uint64_t* first, void* stream);
 
-/* ---- The dense recurrence with a decay for each head (linear attention): the
- * dense state that the sparse table stands in place of ("Meccanismo Core",
- * item 1; section "Problema").  Per memory (b,h), with S of d_k x d_v values:
+/* ---- The dense recurrence with a decay for each head (linear attention; a
+ * state of the kind that section "Problema" names).  It writes k_t v_t^T as it
+ * stands: the delta update of the dense state that "Meccanismo Core" replaces by
+ * the table subtracts what the state returns for k_t, which no scaling of q, k or
+ * v brings about here.  Per memory (b,h), with S of d_k x d_v values:
  *   S_t = exp(g_t) * S_{t-1} + k_t v_t^T;   out_t = S_t^T q_t  (after the write).
  *   S     [B, H, d_k, d_v] fp32 state, updated in place.
  *   q, k  [B, Hk, T, d_k], v, out [B, H, T, d_v] fp32 (dtype SDM_F32) or bf16
@@ -435,9 +437,9 @@ int sdm_touch_prepare(int B, int H, int64_t N, int64_t T, int W, int R, const in
  * Sums are fp32, states and decays hold fp32's precision for both types.  bf16:
  * out is rounded once to bf16; the state and the products q_t . k_s enter it with
  * 16 bits (two bf16 operands of the matrix cores, within 2^-16 of their value).
- * Every q, k, v and S has to be finite and products to stay in fp32's range, as
- * the decay over any stretch of steps has to where g is positive (below 2^-126 it
- * is 0): a NaN or an infinity spreads over all outputs of its chunk of steps
+ * Every q, k, v and S has to be finite, and S, products and sums below 2^127 in
+ * magnitude, as the decay over any stretch of steps has to be where g is positive
+ * (below 2^-126 it is 0): a NaN or an infinity spreads over all outputs of its chunk of steps
  * (below), earlier ones too, and the later ones.
  * d_k, d_v in {32, 64, 128}; B*H <= 2^20, T < 2^31.  S, q, k, v, out, tape and
  * their gradients 16-byte aligned.  A sequence may be split over consecutive
@@ -502,8 +504,9 @@ int sdm_linear_backward(int dtype, int B, int H, int Hk, int d_k, int d_v, int64
  *   next_w, next  NULL, or (H = 1) [d] fp32 and [B, T, d] of out_dtype: the norm
  *         before the next block of the same row, next_w * out /
  *         sqrt(mean(out^2) + eps), from out before its rounding.
- * Arithmetic in fp32, each output rounded once.  d a multiple of 8 in
- * [8, 16384]; B*H*T < 2^31; all arrays 16-byte aligned; eps >= 0.  No rows
+ * Arithmetic in fp32, each output rounded once.  The sums of y^2 (and out^2) over a
+ * row have to stay in fp32's range; with eps = 0 a row of zeros gives NaN, as the
+ * formula does.  d a multiple of 8 in [8, 16384]; B*H*T < 2^31; all arrays 16-byte aligned; eps >= 0.  No rows
  * (B*T = 0) is a valid no-op (the arrays may then be NULL). */
 int sdm_norm(const void* y, int y_dtype, const float* w, const void* z, const void* x, float scale,
              float eps, int B, int H, int64_t T, int d, void* out, int out_dtype,
