@@ -220,7 +220,7 @@ hipError_t launch_step_type(float* S, int BH, int share, int d_k, int d_v, const
 }  // namespace
 
 // Segments of a memory's steps: as many as give every compute unit a workgroup
-// (a chunk is a chain of dependent phases, 5 us forward and 17 back at 128 x 128
+// (a chunk is a chain of dependent phases, 6 us forward and 18 back at 128 x 128
 // in bf16, so chunks go side by side), two where a segment of at most 32 memories
 // keeps 16 chunks even so (16 memories x 32768 steps, bf16: 225 us with two, 259
 // with one; 32 of 64 x 128 x 2047 steps, fp32, the other way, 56 and 52, and 64 x

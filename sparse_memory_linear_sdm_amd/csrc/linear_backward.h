@@ -25,9 +25,10 @@
 // wide: G, S and the loads ahead then fit in registers.
 //
 // Bound by a chunk's phases like the scan, with three times its products: 64
-// memories x 2048 steps of 128 x 128 bf16 in four segments, 26 us for the
-// segments' states and 131-143 for this pass (17 us a chunk of 64 steps; counted:
-// LDS active 46% of the time, vector arithmetic 41%, matrix cores 23%, memory 2.7 TB/s).
+// memories x 2048 steps of 128 x 128 bf16 in four segments, 25 us for the
+// segments' states and 141-149 for this pass (18 us a chunk of 64 steps; counted:
+// LDS active 50% of the time, vector arithmetic 45%, matrix cores 26%, memory 2.5
+// TB/s); fp32 50 + 279 us.
 #pragma once
 #include "dense.h"
 #include "linear_tile.h"

@@ -15,16 +15,18 @@
 //
 // Bound by the phases of a chunk, which follow each other (LDS stores, q.k,
 // outputs, state): 128 x 128 bf16, 64 memories x 4096 steps in four segments,
-// 33 us for the segments' states and 80 for the scan (5 us a chunk of 64 steps),
-// where its bytes need 40; 512 memories x 2048 steps 267 us (4.3 TB/s), since two
+// 33 us for the segments' states and 92 for the scan (6 us a chunk of 64 steps),
+// where its bytes need 40; 512 memories x 2048 steps 300 us (3.8 TB/s), since two
 // workgroups a compute unit then fill each other's waits, held back by power
 // (1.45 GHz) and LDS.  fp32, 64 x 128, 32 memories x 2047 steps in eight segments:
 // 17 + 40 us; a chunk of 32 steps there is eight times the matrix instructions of
-// bf16's, at twice the cycles each.  Four wavefronts of 32 columns read each
-// fragment of q and k for two products: eight wavefronts of 16 read LDS twice as
-// often (64 x 4096 141 us; 117).  One set of LDS blocks, the next chunk's loads in
-// registers: two sets need one barrier less but leave room for one workgroup a
-// compute unit (125 us).
+// bf16's, at twice the cycles each.  bf16's second parts of the state and of the
+// pairs, without which outputs are 1.4 times as far from the exact ones, cost 12 of
+// the 92 us.  Four wavefronts of 32 columns read each fragment of q and k for two
+// products: eight wavefronts of 16 read LDS twice as often (with one part each, 64 x
+// 4096 141 us; 117).  One set of LDS blocks, the next chunk's loads in registers:
+// two sets need one barrier less but leave room for one workgroup a compute unit
+// (with one part each 125 us).
 #pragma once
 #include "dense.h"
 #include "linear_tile.h"

@@ -11,11 +11,15 @@
 // Bound by memory: every value is read once into registers (8 at a time per
 // lane), sums are fp32.  Rows of up to 512 values take a power of two of lanes,
 // 256-thread workgroups several rows; longer rows take a workgroup each.  Measured:
-//   8192 rows of 8192 bf16 with gate, residual and next norm (671 MB) 126-133 us,
-//     5.1-5.3 TB/s (a copy of that mix, three arrays read and one written, 5.6);
-//   262144 rows of 128, fp32 to gated bf16 by heads (268 MB) 49 us, 5.4 TB/s;
-//   their reverse pass, 131072 rows of bf16 (168 MB) and the sum of dw, 36 + 4 us;
-//   4099 rows of 5128, fp32 from bf16 gradients (294 MB), 66 + 5 us, 4.4 TB/s;
+//   8192 rows of 8192 bf16 with gate, residual and next norm (671 MB) 127-136 us,
+//     4.9-5.3 TB/s (a copy of that mix, three arrays read and one written, 5.6);
+//   262144 rows of 128, fp32 to gated bf16 by heads (268 MB) 50 us, 5.4 TB/s;
+//   their reverse pass, 131072 rows of bf16 (168 MB) and the sum of dw, 34-39 + 4 us;
+//     in fp32 66-71 + 5;
+//   4099 rows of 5128, fp32 from bf16 gradients (294 MB), 66 + 6 us, 4.4 TB/s;
+//   reverse, whole rows of 16384, bf16, 4096 of them (537 MB) 122 + 7 us, 4.4 TB/s;
+//     fp32, 2048 of them (537 MB) 108-114 + 7, 4.7-5.0;
+//   without a gate, 32768 rows of 4096 bf16 or 8192 of 8192 fp32 (537 MB) 101 us, 5.3;
 //   one row of 8192 3 us.
 #include "dense.h"
 #include "device_common.h"
