@@ -504,7 +504,8 @@ int sdm_linear_backward(int dtype, int B, int H, int Hk, int d_k, int d_v, int64
  *   next_w, next  NULL, or (H = 1) [d] fp32 and [B, T, d] of out_dtype: the norm
  *         before the next block of the same row, next_w * out /
  *         sqrt(mean(out^2) + eps), from out before its rounding.
- * Arithmetic in fp32, each output rounded once.  The sums of y^2 (and out^2) over a
+ * Arithmetic in fp32, each output rounded once; a row's bits do not depend on the
+ * other rows or their number.  The sums of y^2 (and out^2) over a
  * row have to stay in fp32's range; with eps = 0 a row of zeros gives NaN, as the
  * formula does.  d a multiple of 8 in [8, 16384]; B*H*T < 2^31; all arrays 16-byte aligned; eps >= 0.  No rows
  * (B*T = 0) is a valid no-op (the arrays may then be NULL). */

@@ -11,8 +11,8 @@
 // Bound by memory: every value is read once into registers (8 at a time per
 // lane), sums are fp32.  Rows of up to 512 values take a power of two of lanes,
 // 256-thread workgroups several rows; longer rows take a workgroup each.  Measured:
-//   8192 rows of 8192 bf16 with gate, residual and next norm (671 MB) 127-136 us,
-//     4.9-5.3 TB/s (a copy of that mix, three arrays read and one written, 5.6);
+//   8192 rows of 8192 bf16 with gate, residual and next norm (671 MB) 130-138 us,
+//     4.9-5.2 TB/s (a copy of that mix, three arrays read and one written, 5.6);
 //   262144 rows of 128, fp32 to gated bf16 by heads (268 MB) 50 us, 5.4 TB/s;
 //   their reverse pass, 131072 rows of bf16 (168 MB) and the sum of dw, 34-39 + 4 us;
 //     in fp32 66-71 + 5;
@@ -137,6 +137,23 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int lanes, float (*lds)[
   __syncthreads();  // lds is free again
 }
 
+// Sum over a long row of what each thread has for its V vectors, by pieces of 64
+// vectors in their order: the same bits for one vector a thread and for two.
+template <int V>
+__device__ __forceinline__ float long_row_sum(const float (&v)[V], float* lds) {
+  const int waves = (int)(blockDim.x / kWave);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float s = wave_sum_f32(v[i]);
+    if (lane_id() == 0) lds[i * waves + threadIdx.x / kWave] = s;
+  }
+  __syncthreads();
+  float sum = lds[0];
+  for (int w = 1; w < V * waves; ++w) sum += lds[w];
+  __syncthreads();  // lds is free again
+  return sum;
+}
+
 // Row r of the outputs (b, t, h), as a row of y.
 __device__ __forceinline__ int64_t y_row(const NormArgs& A, uint32_t r) {
   if (A.H == 1) return r;
@@ -147,10 +164,18 @@ __device__ __forceinline__ int64_t y_row(const NormArgs& A, uint32_t r) {
 
 template <class Ty, class To, int V, bool WIDE>
 __global__ __launch_bounds__(WIDE ? kWideMax : kNarrow) void norm_kernel(NormArgs A, int lanes) {
-  __shared__ float lds[1][kWideMax / kWave];
+// A row's bits do not depend on the variant that takes it: the kernel's products
+// and sums are rounded as they stand (the compiler might fuse them differently).
+#pragma clang fp contract(off)
+  __shared__ float lds[WIDE ? V * kWideMax / kWave : 1];
   const int nvec = A.d / 8;
   const int group = WIDE ? 0 : threadIdx.x / lanes, me = WIDE ? threadIdx.x : threadIdx.x % lanes;
   const int per_block = WIDE ? 1 : kNarrow / lanes, L = WIDE ? (int)blockDim.x : lanes;
+  const auto row_sum = [&](float (&v)[V]) {
+    if constexpr (WIDE) return long_row_sum(v, lds);
+    for (int o = 1; o < lanes; o <<= 1) v[0] += __shfl_xor(v[0], o);
+    return v[0];
+  };
   // every lane of a wavefront runs the same passes (the sums exchange lanes)
   for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < A.rows;
        r0 += (int64_t)gridDim.x * per_block) {
@@ -158,7 +183,7 @@ __global__ __launch_bounds__(WIDE ? kWideMax : kNarrow) void norm_kernel(NormArg
     const bool here = r < A.rows;
     const int64_t yr = here ? y_row(A, (uint32_t)r) * A.d : 0, at = r * A.d;
     f32x8 y[V];
-    float ss[1] = {0.0f};
+    float ss[V];  // squares, by vectors
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int j = me + i * L;
@@ -174,13 +199,12 @@ __global__ __launch_bounds__(WIDE ? kWideMax : kNarrow) void norm_kernel(NormArg
       }
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) ss[0] += sum8(y[i] * y[i]);
-    row_sums<WIDE>(ss, lanes, lds);
-    const float rs = A.scale / sqrtf(ss[0] / (float)A.d + A.eps);
-    ss[0] = 0.0f;
+    for (int i = 0; i < V; ++i) ss[i] = sum8(y[i] * y[i]);
+    const float rs = A.scale / sqrtf(row_sum(ss) / (float)A.d + A.eps);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int j = me + i * L;
+      ss[i] = 0.0f;
       if (!here || j >= nvec) continue;
       y[i] = y[i] * rs * weights8(A.w, j * 8);
       if (A.z) {
@@ -189,11 +213,10 @@ __global__ __launch_bounds__(WIDE ? kWideMax : kNarrow) void norm_kernel(NormArg
       }
       if (A.x) y[i] += x[i];
       store8<To>(A.out, at + j * 8, y[i]);
-      ss[0] += sum8(y[i] * y[i]);
+      ss[i] = sum8(y[i] * y[i]);
     }
     if (A.next_w) {
-      row_sums<WIDE>(ss, lanes, lds);
-      const float rn = 1.0f / sqrtf(ss[0] / (float)A.d + A.eps);
+      const float rn = 1.0f / sqrtf(row_sum(ss) / (float)A.d + A.eps);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int j = me + i * L;
