@@ -439,8 +439,8 @@ int sdm_touch_prepare(int B, int H, int64_t N, int64_t T, int W, int R, const in
  * 16 bits (two bf16 operands of the matrix cores, within 2^-16 of their value).
  * Every q, k, v and S has to be finite, and S, products and sums below 2^127 in
  * magnitude, as the decay over any stretch of steps has to be where g is positive
- * (below 2^-126 it is 0): a NaN or an infinity spreads over all outputs of its chunk of steps
- * (below), earlier ones too, and the later ones.
+ * (below 2^-126 it is 0): a NaN or an infinity spreads over all outputs of its
+ * chunk of steps (below), earlier ones too, and the later ones.
  * d_k, d_v in {32, 64, 128}; B*H <= 2^20, T < 2^31.  S, q, k, v, out, tape and
  * their gradients 16-byte aligned.  A sequence may be split over consecutive
  * calls (equal up to the order of the fp32 sums).  Calls that overlap in time
@@ -505,10 +505,10 @@ int sdm_linear_backward(int dtype, int B, int H, int Hk, int d_k, int d_v, int64
  *         before the next block of the same row, next_w * out /
  *         sqrt(mean(out^2) + eps), from out before its rounding.
  * Arithmetic in fp32, each output rounded once; a row's bits do not depend on the
- * other rows or their number.  The sums of y^2 (and out^2) over a
- * row have to stay in fp32's range; with eps = 0 a row of zeros gives NaN, as the
- * formula does.  d a multiple of 8 in [8, 16384]; B*H*T < 2^31; all arrays 16-byte aligned; eps >= 0.  No rows
- * (B*T = 0) is a valid no-op (the arrays may then be NULL). */
+ * other rows or their number.  The sums of y^2 (and out^2) over a row have to stay
+ * in fp32's range; with eps = 0 a row of zeros gives NaN, as the formula does.  d a
+ * multiple of 8 in [8, 16384]; B*H*T < 2^31; all arrays 16-byte aligned; eps >= 0.
+ * No rows (B*T = 0) is a valid no-op (the arrays may then be NULL). */
 int sdm_norm(const void* y, int y_dtype, const float* w, const void* z, const void* x, float scale,
              float eps, int B, int H, int64_t T, int d, void* out, int out_dtype,
              const float* next_w, void* next, void* stream);

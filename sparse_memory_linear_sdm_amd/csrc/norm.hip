@@ -408,8 +408,10 @@ hipError_t norm_types(const NormArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   const dim3 blocks((unsigned)(a.rows < kMaxBlocks ? a.rows : kMaxBlocks));
-  // few rows: a row's latency counts, so as many threads as it has vectors;
-  // otherwise two vectors a thread (8192 rows of 8192: two 126 us, one 131, four 166)
+  // few rows: a row's latency counts, so as many threads as it has vectors (256 rows
+  // of 4096 bf16 6.1 us, 8.0 with two a thread; 512 of 8192 11.5, 12.0); otherwise
+  // two vectors a thread (8192 rows of 8192, replayed from a graph, 134 us, one 137;
+  // 16384 of 4096 55.8, one 58.5; fp32 rows the other way, 133 and 129)
   if (a.rows <= kFewRows && a.d <= 8 * kWideMax)
     hipLaunchKernelGGL((norm_kernel<Ty, To, 1, true>), blocks, dim3(wide_threads(a.d, 1)), 0, s, a, 0);
   else
